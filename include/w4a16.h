@@ -53,7 +53,11 @@ extern "C" {
 /* Same type as cudaStream_t. */
 typedef struct CUstream_st *w4a16_stream_t;
 
-typedef enum { W4A16_F16 = 0, W4A16_BF16 = 1 } w4a16_dtype;
+typedef enum {
+  W4A16_F16 = 0,
+  W4A16_BF16 = 1,
+  W4A16_F32 = 2 /* logits of w4a16_token_logprobs only */
+} w4a16_dtype;
 
 typedef enum {
   W4A16_OK = 0,
@@ -259,6 +263,126 @@ w4a16_status w4a16_layer_gemm(w4a16_layer_t layer, const void *a, void *out, int
                               size_t workspace_bytes, w4a16_stream_t stream);
 size_t w4a16_layer_workspace_size(w4a16_layer_t layer, int64_t m);
 w4a16_status w4a16_layer_destroy(w4a16_layer_t layer);
+
+/*
+ * Serving operators next to the linear layer: what a model's step runs between its W4A16 projections
+ * and after its last one, with one to 64 drafted tokens for each sequence (one: plain decoding).
+ *
+ * Strides are in elements; the last dimension of a strided tensor is contiguous. All of them are
+ * stream-ordered, allocate nothing, do not synchronise and can be captured; validation happens before any
+ * launch. Index tensors are read on the device: an index out of range never leads to an access out of
+ * range, each function says what it does instead.
+ */
+
+/* Rotary positions: positions int64 [tokens]; table float32 [table_rows, rot_dim], row p = the rot_dim / 2
+ * cosines, then the rot_dim / 2 sines of position p (long-context scaling is in the table). The first
+ * rot_dim elements of a head turn, the rest stay. interleaved 0: element i pairs with i + rot_dim / 2;
+ * otherwise 2 i with 2 i + 1. A position outside the table gives NaN. */
+typedef struct {
+  const int64_t *positions;
+  const float *table;
+  int64_t table_rows;
+  int32_t rot_dim;
+  int32_t interleaved;
+} w4a16_rope_t;
+
+/* Quantised paged cache of keys and values: device uint8 [num_pages, kv_heads, page_size / 16,
+ * w4a16_kv_tile_bytes(head_dim, bits)], 128-byte aligned. A tile holds 16 consecutive tokens of one head:
+ *   K codes [16][head_dim * bits / 8], V codes [16][head_dim * bits / 8], K parameters uint32 [16],
+ *   V parameters uint32 [16]; a parameter is the scale's 16 bits (of the activations' dtype) in its low half
+ *   and the zero point in its high half. 4-bit codes: element 2 i in the low nibble of byte i, 2 i + 1 in
+ *   the high one. Value = (code - zero) * scale, one scale and zero point for each token, head and K | V.
+ * Slot s of the cache is token s % page_size of page s / page_size. bits: 4 or 8; head_dim: 64, 128 or
+ * 256; page_size: a multiple of 16. */
+typedef struct {
+  void *data;
+  int64_t num_pages;
+  int32_t kv_heads, head_dim, page_size, bits;
+} w4a16_kv_cache_t;
+
+/* Bytes of a cache tile: 16 * (2 * head_dim * bits / 8 + 8) (0 for values that the cache does not take). */
+size_t w4a16_kv_tile_bytes(int head_dim, int bits);
+
+/*
+ * w4a16_rope - out = x with its heads turned to their tokens' positions, products and sums in fp32, one rounding.
+ *   x, out: [tokens, heads, head_dim] of dtype; out may be x itself (same pointer and strides).
+ *   16-byte aligned pointers, strides in multiples of 8 elements and rot_dim in multiples of 16 (8
+ *   interleaved) run with vector accesses, anything else element by element.
+ * Errors: INVALID_ARG (sizes, nulls, overlap), UNSUPPORTED (dtype), MISALIGNED (natural alignment).
+ */
+w4a16_status w4a16_rope(const w4a16_rope_t *rope, const void *x, int64_t x_token_stride, int64_t x_head_stride, void *out,
+                        int64_t out_token_stride, int64_t out_head_stride, int64_t tokens, int heads, int head_dim,
+                        w4a16_dtype dtype, w4a16_stream_t stream);
+
+/*
+ * w4a16_kv_write - quantises k and v into the cache's slots; with rope, k (and q, when given) turn first.
+ *   k, v: [tokens, kv_heads, head_dim]; q: [tokens, q_heads, head_dim] or NULL (only with rope);
+ *   q_out: contiguous [tokens, q_heads, head_dim]. All of dtype, 16-byte aligned, strides multiples of 8.
+ *   slots: int64 [tokens], all different; a token whose slot is negative or past the cache is not stored.
+ * A row x of head_dim elements, L = 2^bits - 1: lo = min(0, min x), hi = max(0, max x),
+ *   scale = RNE_dtype(hi * (1/L) - lo * (1/L)), zero = rint(-lo / scale), code = clamp(rint(x / scale) + zero, 0, L)
+ * (fp32; turned keys are rounded to dtype first). A scale below 2^-126 is stored as zero and the row reads as
+ * zeros; a row with an infinity or a NaN is stored as NaN.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, bits, head_dim), MISALIGNED.
+ */
+w4a16_status w4a16_kv_write(const w4a16_kv_cache_t *cache, const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                            const void *v, int64_t v_token_stride, int64_t v_head_stride, const int64_t *slots,
+                            int64_t tokens, const w4a16_rope_t *rope, const void *q, int64_t q_token_stride,
+                            int64_t q_head_stride, int q_heads, void *q_out, w4a16_dtype dtype, w4a16_stream_t stream);
+
+/*
+ * w4a16_kv_read - k_out, v_out [tokens, kv_heads, head_dim] (contiguous, 16-byte aligned) = RNE_dtype((code - zero) * scale)
+ * of the given slots (int64 [tokens]); zeros for a slot that is negative or past the cache.
+ * dtype is the one that the cache was written with. Errors: as w4a16_kv_write.
+ */
+w4a16_status w4a16_kv_read(const w4a16_kv_cache_t *cache, const int64_t *slots, int64_t tokens, void *k_out, void *v_out,
+                           w4a16_dtype dtype, w4a16_stream_t stream);
+
+/*
+ * w4a16_tree_attention - out = softmax(softmax_scale * q k^T) v over each sequence's cached tokens.
+ *   q           [total_q, q_heads, head_dim], strided, 16-byte aligned, strides multiples of 8; query heads
+ *               h * q_heads / kv_heads ... share cache head h
+ *   q_start     int32 [batch + 1]: sequence b has the query tokens q_start[b] .. q_start[b + 1] - 1, at most
+ *               max_q (<= 64) of them; NULL: one for each sequence (total_q == batch)
+ *   kv_lens     int32 [batch]: cached tokens of each sequence, its query tokens (already written) the last of them
+ *   page_table  int32 [batch, max_pages]: pages of each sequence; tokens of a page outside the cache, and
+ *               tokens past max_pages pages, are not seen
+ *   tree_mask   uint64 [total_q]: bit j of a query token's word: it sees the j-th query token of its own
+ *               sequence (set its own bit too); NULL: a chain (it sees those up to itself). Cached tokens before
+ *               the query tokens are seen by all.
+ *   out         [total_q, q_heads, head_dim] contiguous, 16-byte aligned; lse: float32 [total_q, q_heads] or NULL,
+ *               the natural log of the softmax's denominator
+ * A query that sees nothing gives zeros and lse = -infinity. Query tokens past max_q of a sequence, and rows
+ * that no sequence owns, are not written. Scores, softmax statistics and sums are fp32; the probabilities are
+ * rounded to 11 significant bits for the product with the values' codes.
+ *   workspace   device memory, 256-byte aligned, w4a16_tree_attention_workspace_size bytes, as for w4a16_gemm_ws: its
+ *               first 4 KiB zero before first use (every call leaves them zero; the same buffer may serve both
+ *               functions on one stream). NULL or a smaller one: a sequence's tokens are not split over CTAs.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, bits, head_dim, max_q), MISALIGNED, CUDA. A kernel that gives up a
+ * bounded wait is reported by w4a16_get_device_error.
+ */
+w4a16_status w4a16_tree_attention(const w4a16_kv_cache_t *cache, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                  int q_heads, int64_t total_q, const int32_t *q_start, int64_t batch, int max_q,
+                                  const int32_t *kv_lens, const int32_t *page_table, int64_t max_pages,
+                                  const uint64_t *tree_mask, float softmax_scale, void *out, float *lse, w4a16_dtype dtype,
+                                  void *workspace, size_t workspace_bytes, w4a16_stream_t stream);
+/* Bytes of workspace w4a16_tree_attention uses for these sizes on the current device. */
+size_t w4a16_tree_attention_workspace_size(int max_q, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * w4a16_token_logprobs - natural log probabilities under softmax(logits row).
+ *   logits        [rows, vocab], rows row_stride elements apart, dtype F16, BF16 or F32
+ *   tokens        int64 [rows, n_tokens] (n_tokens may be 0); logprobs float32 [rows, n_tokens]; a token outside
+ *                 the vocabulary gives NaN
+ *   entropy       float32 [rows] or NULL: -sum p log p
+ *   top_ids       int64 [rows, top_k], top_logprobs float32 [rows, top_k]: the top_k (<= 32) largest, in descending
+ *                 order, equal logits by ascending index
+ * Logits of -infinity have probability zero. A row with no finite logit, or with a NaN or +infinity, gives NaN (its
+ * top_ids are indices of the vocabulary or -1). Errors: INVALID_ARG, UNSUPPORTED (dtype, top_k), MISALIGNED, CUDA.
+ */
+w4a16_status w4a16_token_logprobs(const void *logits, int64_t row_stride, int64_t rows, int64_t vocab, w4a16_dtype dtype,
+                                  const int64_t *tokens, int n_tokens, int top_k, float *logprobs, float *entropy,
+                                  int64_t *top_ids, float *top_logprobs, w4a16_stream_t stream);
 
 /*
  * w4a16_can_implement - host-only check of a layer configuration, mirroring

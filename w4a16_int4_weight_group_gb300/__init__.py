@@ -445,3 +445,9 @@ __all__ = ["w4a16_pack", "w4a16_unpack", "w4a16_prepack", "w4a16_dequant", "w4a1
            "w4a16_debug_inject_stall",
            "w4a16_debug_launch_count", "w4a16_version", "W4A16Error", "lib", "last_error", "LIB_PATH",
            "SIGNATURES", "PATHS"]
+
+from . import serving as _serving  # noqa: E402  (the serving operators build on the helpers above)
+from .serving import *  # noqa: E402,F401,F403
+
+SIGNATURES += _serving.SIGNATURES
+__all__ += _serving.__all__

@@ -23,6 +23,8 @@ namespace {
 thread_local std::string g_last_error;
 std::atomic<uint64_t> g_launches{0};
 
+}  // namespace
+
 w4a16_status fail(w4a16_status st, const char *fmt, ...) {
   char buf[512];
   va_list ap;
@@ -42,16 +44,7 @@ w4a16_status cuda_fail(cudaError_t e, const char *what) {
   return fail(W4A16_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-Range range(const void *p, int64_t bytes) {
-  const auto lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, lo + static_cast<uintptr_t>(bytes)};
-}
-bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
+namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 31;
 constexpr int64_t kMaxN = int64_t(1) << 24;  // column tiles index a grid dimension of at most 65535

@@ -9,6 +9,22 @@
 
 namespace w4a16 {
 
+// Status of an entry point: sets (or clears) the calling thread's last error message.
+w4a16_status fail(w4a16_status st, const char *fmt, ...);
+w4a16_status ok();
+w4a16_status cuda_fail(cudaError_t e, const char *what);
+
+// Argument checks shared by the entry points.
+inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+struct Range {
+  uintptr_t lo, hi;  // [lo, hi)
+};
+inline Range range(const void *p, int64_t bytes) {
+  const auto lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + static_cast<uintptr_t>(bytes)};
+}
+inline bool overlaps(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
+
 struct GemmArgs {
   const void *a;
   const int32_t *b_q;
@@ -109,5 +125,74 @@ cudaError_t launch_gemm_prefill(const GemmArgs &g, const w4a16_plan_t &p, const 
 cudaError_t prefill_take_device_error(uint32_t *err);
 cudaError_t prefill_set_wait_limit_ns(uint64_t ns);
 cudaError_t prefill_set_stall(bool on);
+
+// ---------------------------------------------------------------------------------------------
+// Serving operators: rotary positions, quantised paged cache, attention over it, log probabilities
+// ---------------------------------------------------------------------------------------------
+constexpr int kTileTokens = 16;  // tokens of one cache tile
+
+inline int64_t kv_tile_bytes(int head_dim, int bits) { return int64_t(kTileTokens) * (2 * head_dim * bits / 8 + 8); }
+
+// A strided [tokens, heads, head_dim] tensor of 16-bit elements; head_dim is contiguous. Strides in
+// elements.
+struct HeadsView {
+  const void *ptr;
+  int64_t token_stride, head_stride;
+};
+
+struct RopeArgs {
+  const int64_t *positions;
+  const float *table;  // [table_rows, rot_dim]: cosines, then sines
+  int64_t table_rows;
+  int rot_dim;
+  bool interleaved;
+};
+
+cudaError_t launch_rope(const HeadsView &x, const HeadsView &out, int64_t tokens, int heads, int head_dim, int dtype,
+                        const RopeArgs &rope, cudaStream_t stream);
+// rope and q may be absent (rope.positions == null, q.ptr == null).
+cudaError_t launch_kv_write(const w4a16_kv_cache_t &cache, const HeadsView &k, const HeadsView &v, const int64_t *slots,
+                            int64_t tokens, int dtype, const RopeArgs &rope, const HeadsView &q, int q_heads, void *q_out,
+                            cudaStream_t stream);
+cudaError_t launch_kv_read(const w4a16_kv_cache_t &cache, const int64_t *slots, int64_t tokens, void *k_out, void *v_out,
+                           int dtype, cudaStream_t stream);
+
+struct AttentionArgs {
+  w4a16_kv_cache_t cache;
+  HeadsView q;
+  int q_heads;
+  int64_t total_q;
+  const int32_t *q_start;  // null: one query token for each sequence
+  int64_t batch;
+  int max_q;
+  const int32_t *kv_lens;
+  const int32_t *page_table;
+  int64_t max_pages;  // entries of one sequence in the page table
+  const uint64_t *tree_mask;  // null: a chain
+  float scale;
+  void *out;   // [total_q, q_heads, head_dim]
+  float *lse;  // [total_q, q_heads] or null
+  int dtype;
+  void *workspace;
+  size_t workspace_bytes;
+  cudaStream_t stream;
+};
+cudaError_t launch_tree_attention(const AttentionArgs &a, const DeviceInfo &dev);
+size_t tree_attention_workspace_bytes(int max_q, int q_heads, int kv_heads, int head_dim, int num_sms);
+
+struct LogprobArgs {
+  const void *logits;
+  int64_t row_stride, rows, vocab;
+  int dtype;
+  const int64_t *tokens;  // [rows, n_tokens]
+  int n_tokens;
+  int top_k;
+  float *logprobs;      // [rows, n_tokens]
+  float *entropy;       // [rows] or null
+  int64_t *top_ids;     // [rows, top_k]
+  float *top_logprobs;  // [rows, top_k]
+  cudaStream_t stream;
+};
+cudaError_t launch_token_logprobs(const LogprobArgs &a, const DeviceInfo &dev);
 
 }  // namespace w4a16

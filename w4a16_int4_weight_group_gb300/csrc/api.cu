@@ -689,11 +689,12 @@ int w4a16_debug_selected_path(int64_t m, int64_t k, int64_t n, int group_size) {
 w4a16_status w4a16_get_device_error(void) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "synchronise");
-  uint32_t err = 0, err2 = 0;
+  uint32_t err = 0, err2 = 0, err3 = 0;
   e = prefill_take_device_error(&err);
   if (e == cudaSuccess) e = decode_take_device_error(&err2);
+  if (e == cudaSuccess) e = attention_take_device_error(&err3);
   if (e != cudaSuccess) return cuda_fail(e, "read device error word");
-  err |= err2;
+  err |= err2 | err3;
   if (err) return fail(W4A16_ERR_TIMEOUT, "a bounded device-side wait gave up (code 0x%x)", err);
   return ok();
 }
@@ -719,6 +720,7 @@ w4a16_status w4a16_debug_decode_override(int consumer_groups, int k_split, int k
 w4a16_status w4a16_debug_set_wait_limit_ns(uint64_t ns) {
   cudaError_t e = prefill_set_wait_limit_ns(ns);
   if (e == cudaSuccess) e = decode_set_wait_limit_ns(ns);
+  if (e == cudaSuccess) e = attention_set_wait_limit_ns(ns);
   if (e != cudaSuccess) return cuda_fail(e, "set wait limit");
   return ok();
 }
@@ -726,6 +728,7 @@ w4a16_status w4a16_debug_set_wait_limit_ns(uint64_t ns) {
 w4a16_status w4a16_debug_inject_stall(int on) {
   cudaError_t e = prefill_set_stall(on != 0);
   if (e == cudaSuccess) e = decode_set_stall(on != 0);
+  if (e == cudaSuccess) e = attention_set_stall(on != 0);
   if (e != cudaSuccess) return cuda_fail(e, "set stall hook");
   return ok();
 }

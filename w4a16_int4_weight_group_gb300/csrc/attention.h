@@ -1,0 +1,47 @@
+// Shared between the translation units of the attention (one for each head size, compiled in parallel).
+#pragma once
+
+#include "internal.h"
+
+namespace w4a16 {
+namespace attention {
+
+// Failure detection: error word, limit of the bounded waits (0: the default) and the test hook.
+struct Control {
+  unsigned int error;
+  unsigned int stall;  // the workers first wait on a barrier that nothing arrives on
+  unsigned long long limit_ns;
+};
+
+struct Params {
+  const uint8_t *cache;
+  const uint16_t *q;
+  int64_t q_ts, q_hs;
+  const int32_t *q_start, *kv_lens, *page_table;
+  int64_t max_pages, num_pages, tile_bytes;
+  const uint64_t *tree_mask;
+  float scale;
+  uint16_t *out;
+  float *lse;
+  int64_t total_q;
+  int batch, q_heads, kv_heads, group, page_tiles, max_q;
+  int bf16;
+  unsigned int *flags;  // one counter for each CTA, zero before and after; null: no sequence is split
+  float *partials;
+  Control *control;
+};
+
+// Workspace: the counters first (the area that calls leave zero), then two partial results for each CTA.
+constexpr size_t kFlagBytes = 4096;
+constexpr int kMaxCtas = kFlagBytes / 4;
+// Floats of one partial result of `rows` rows: the sums, the maxima, the denominators.
+inline int64_t partial_floats(int rows, int head_dim) { return int64_t(rows) * (head_dim + 2); }
+
+// Rows of a row tile of the streaming kernel for sequences of max_rows query rows on a cache head.
+inline int stream_rows(int max_rows, int head_dim) { return max_rows <= 8 ? 8 : max_rows <= 16 || head_dim == 256 ? 16 : 32; }
+
+template <int D>
+cudaError_t launch_stream(const Params &p, int bits, int rows, int num_sms, cudaStream_t stream);
+
+}  // namespace attention
+}  // namespace w4a16

@@ -1,0 +1,12 @@
+// The attention kernels for heads of 128 elements (a translation unit of their own, to compile in parallel).
+#include <atomic>
+
+#include "attention_stream.cuh"
+
+namespace w4a16 {
+namespace attention {
+
+template cudaError_t launch_stream<128>(const Params &, int, int, int, cudaStream_t);
+
+}  // namespace attention
+}  // namespace w4a16

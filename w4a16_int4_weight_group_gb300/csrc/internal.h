@@ -179,6 +179,9 @@ struct AttentionArgs {
 };
 cudaError_t launch_tree_attention(const AttentionArgs &a, const DeviceInfo &dev);
 size_t tree_attention_workspace_bytes(int max_q, int q_heads, int kv_heads, int head_dim, int num_sms);
+cudaError_t attention_take_device_error(uint32_t *err);
+cudaError_t attention_set_wait_limit_ns(uint64_t ns);
+cudaError_t attention_set_stall(bool on);
 
 struct LogprobArgs {
   const void *logits;

@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(HERE, "libw4a16.so")
 
 SOURCES = ["api.cu", "pack.cu", "gemm_generic.cu", "gemm_decode.cu", "gemm_prefill.cu", "serve_api.cu", "kv_cache.cu",
            "attention.cu", "attention_d64.cu", "attention_d128.cu", "attention_d256.cu", "logprobs.cu"]
-# CPython argument marshalling for the prepared-layer call (optional: the binding uses ctypes when it
+# CPython argument marshalling for the prepared-layer call and the serving operators (optional: the binding uses ctypes when it
 # cannot be built, e.g. without the Python headers)
 PYCALL_SRC = os.path.join(CSRC, "pycall.c")
 PYCALL_PATH = os.path.join(HERE, "_w4a16_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
@@ -54,7 +54,9 @@ def up_to_date() -> bool:
 
 def build_pycall(force: bool = False) -> bool:
     """Compile the CPython marshalling module beside the library; False when it cannot be built."""
-    if not force and os.path.exists(PYCALL_PATH) and os.path.getmtime(PYCALL_PATH) >= os.path.getmtime(PYCALL_SRC):
+    header = os.path.join(INCLUDE, "w4a16.h")
+    if not force and os.path.exists(PYCALL_PATH) and os.path.getmtime(PYCALL_PATH) >= max(
+            os.path.getmtime(PYCALL_SRC), os.path.getmtime(header)):
         return True
     inc = sysconfig.get_paths().get("include")
     if not inc or not os.path.exists(os.path.join(inc, "Python.h")):
@@ -63,7 +65,7 @@ def build_pycall(force: bool = False) -> bool:
     if not cc:
         return False
     tmp = PYCALL_PATH + ".tmp"
-    r = subprocess.run([cc, "-O2", "-shared", "-fPIC", "-I", inc, PYCALL_SRC, "-o", tmp], capture_output=True, text=True)
+    r = subprocess.run([cc, "-O2", "-shared", "-fPIC", "-I", inc, "-I", INCLUDE, PYCALL_SRC, "-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:
         return False
     os.replace(tmp, PYCALL_PATH)

@@ -55,6 +55,9 @@ cudaError_t launch_tree_attention(const AttentionArgs &a, const DeviceInfo &dev)
   p.group = a.q_heads / a.cache.kv_heads;
   p.page_tiles = a.cache.page_size / kTileTokens;
   p.max_q = a.max_q;
+  p.page_shift = -1;
+  for (int i = 0; i < 20; ++i)
+    if (p.page_tiles == 1 << i) p.page_shift = i;
   p.bf16 = a.dtype == W4A16_BF16;
   if (a.workspace && a.workspace_bytes >= tree_attention_workspace_bytes(a.max_q, a.q_heads, p.kv_heads, a.cache.head_dim, dev.num_sms)) {
     p.flags = static_cast<unsigned int *>(a.workspace);

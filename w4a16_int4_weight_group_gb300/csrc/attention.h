@@ -25,6 +25,7 @@ struct Params {
   float *lse;
   int64_t total_q;
   int batch, q_heads, kv_heads, group, page_tiles, max_q;
+  int page_shift;  // log2 of page_tiles, or -1
   int bf16;
   unsigned int *flags;  // one counter for each CTA, zero before and after; null: no sequence is split
   float *partials;

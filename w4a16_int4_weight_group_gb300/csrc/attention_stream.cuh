@@ -75,45 +75,52 @@ struct StreamLayout {
   static constexpr int kOffM = kOffQs + R * 4;                // [W][R] maxima, then denominators
   static constexpr int kOffBar = (kOffM + 2 * W * R * 4 + 7) / 8 * 8;
   static constexpr int kOffMisc = kOffBar + 8 * (W * S + 1);  // abort flag, last flag, start, scan
-  static constexpr int kSmem = kOffMisc + 16 + 16 + 8 * W + 8;
+  static constexpr int kSmem = kOffMisc + 32 + 8 * W;
   static_assert(S >= 2, "a ring of two stages at least");
   static_assert(kSmem <= kBudget, "shared memory");
   static_assert(kOffRing % 128 == 0 && kOffO % 16 == 0 && kTile % 128 == 0, "alignment");
 };
 
-// Position in the list of units.
+// Position in the list of units, and what of the sequence it takes to walk on.
 struct Cursor {
   int b, h, rt, blk;
-  int nb, nrt;      // of the sequence: units of a segment, row tiles
-  int len, n, first;  // cached tokens, query tokens, position of the first of them
-  int64_t q0;
+  int nb, nrt;  // of the sequence: units of a segment, row tiles
+  int len;      // cached tokens
+};
+// What a segment takes beyond that.
+struct Queries {
+  int64_t q0;    // row of the first query token
+  int n, first;  // query tokens, cache position of the first of them
 };
 
 __device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+__device__ __forceinline__ int length_of(const Params &p, int b) {
+  const int64_t cap = p.max_pages * p.page_tiles * 16;
+  const int len = p.kv_lens[b];
+  return len < 0 ? 0 : static_cast<int>(min(int64_t(len), cap));
+}
+__device__ __forceinline__ Queries queries_of(const Params &p, int b, int len) {
+  const int64_t q0 = p.q_start ? p.q_start[b] : b, q1 = p.q_start ? p.q_start[b + 1] : b + 1;
+  int64_t n = q1 - q0;
+  if (n < 0 || q0 < 0 || q1 > p.total_q) n = 0;
+  return Queries{q0, static_cast<int>(min(n, int64_t(p.max_q))), static_cast<int>(len - n)};
+}
+
 // Loads sequence b into the cursor; units of the sequence (0: nothing to do).
 template <class L>
 __device__ __forceinline__ int64_t load_sequence(const Params &p, int b, Cursor &c) {
-  const int64_t q0 = p.q_start ? p.q_start[b] : b, q1 = p.q_start ? p.q_start[b + 1] : b + 1;
-  const int64_t cap = p.max_pages * p.page_tiles * 16;
-  const int64_t len = p.kv_lens[b];
   c.b = b;
   c.h = c.rt = c.blk = 0;
-  c.len = static_cast<int>(len < 0 ? 0 : len < cap ? len : cap);
-  int64_t n = q1 - q0;
-  if (n < 0 || q0 < 0 || q1 > p.total_q) n = 0;
-  c.first = static_cast<int>(c.len - n);
-  c.n = static_cast<int>(n < p.max_q ? n : p.max_q);
-  c.q0 = q0;
-  c.nrt = static_cast<int>(ceil_div(int64_t(c.n) * p.group, L::R));
+  c.len = length_of(p, b);
+  c.nrt = static_cast<int>((int64_t(queries_of(p, b, c.len).n) * p.group + L::R - 1) / L::R);
   c.nb = c.len > 0 ? (c.len + L::kUnit - 1) / L::kUnit : 1;
   return int64_t(c.nb) * c.nrt * p.kv_heads;
 }
 
-// Next unit (the caller knows that there is one).
+// The first unit of the next segment (the caller knows that there is one).
 template <class L>
-__device__ __forceinline__ void advance(const Params &p, Cursor &c) {
-  if (++c.blk < c.nb) return;
+__device__ __forceinline__ void next_segment(const Params &p, Cursor &c) {
   c.blk = 0;
   if (++c.rt < c.nrt) return;
   c.rt = 0;
@@ -265,20 +272,18 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
   int64_t units = u1 - u0;
   if (!p.flags) {
     // no workspace: the share is the segments that start in [u0, u1), whole
-    while (cur.blk != 0 && units > 0) {
-      const int64_t skip = min(int64_t(cur.nb - cur.blk), units);
-      units -= skip;
-      cur.blk += static_cast<int>(skip) - 1;
+    if (cur.blk != 0) {
+      units -= min(int64_t(cur.nb - cur.blk), units);
       if (units == 0) return;
-      advance<L>(p, cur);
+      next_segment<L>(p, cur);
     }
     Cursor c = cur;
     int64_t left = units, whole = 0;
-    while (left > 0) {
+    while (true) {
       whole += c.nb;
       left -= c.nb;
-      c.blk = c.nb - 1;
-      if (left > 0) advance<L>(p, c);
+      if (left <= 0) break;
+      next_segment<L>(p, c);
     }
     units = whole;
   }
@@ -289,38 +294,36 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
   uint32_t valid = 0;   // TPS bits for each stage: tiles that are there
   uint32_t phases = 0;  // parity of each stage's next completion
   auto issue = [&](int s) {
+    if (to_issue == 0) return;
+    const int tile0 = (ahead.blk * W + warp) * TPS;
     uint32_t v = 0;
-    if (to_issue > 0) {
-      const int t0 = (ahead.blk * W + warp) * (TPS * 16);
-      int64_t from[TPS];
+    int64_t from[TPS];
 #pragma unroll
-      for (int j = 0; j < TPS; ++j) {
-        const int t = t0 + 16 * j;
-        from[j] = 0;
-        if (t < ahead.len) {
-          const int tile = t >> 4;
-          const int page_i = tile / p.page_tiles;
-          const int page = __ldg(p.page_table + ahead.b * p.max_pages + page_i);
-          if (page >= 0 && page < p.num_pages) {
-            v |= 1u << j;
-            from[j] = ((int64_t(page) * p.kv_heads + ahead.h) * p.page_tiles + (tile - page_i * p.page_tiles)) * L::kTile;
-          }
+    for (int j = 0; j < TPS; ++j) {
+      const int tile = tile0 + j;
+      from[j] = 0;
+      if (tile * 16 < ahead.len) {
+        const int page_i = p.page_shift >= 0 ? tile >> p.page_shift : tile / p.page_tiles;
+        const int page = __ldg(p.page_table + ahead.b * p.max_pages + page_i);
+        if (page >= 0 && page < p.num_pages) {
+          v |= 1u << j;
+          from[j] = ((int64_t(page) * p.kv_heads + ahead.h) * p.page_tiles + (tile - page_i * p.page_tiles)) * L::kTile;
         }
       }
-      if (v != 0 && lane == 0) {
-        const uint32_t dst = ring + static_cast<uint32_t>(s * L::kStage);
-        mbar_arrive_expect_tx(bars + 8u * s, static_cast<uint32_t>(__popc(v)) * L::kTile);
-        if (TPS == 2 && v == 3 && from[TPS - 1] == from[0] + L::kTile) {
-          bulk_load(dst, p.cache + from[0], 2 * L::kTile, bars + 8u * s);
-        } else {
-#pragma unroll
-          for (int j = 0; j < TPS; ++j)
-            if (v & (1u << j)) bulk_load(dst + j * L::kTile, p.cache + from[j], L::kTile, bars + 8u * s);
-        }
-      }
-      if (--to_issue > 0) advance<L>(p, ahead);
     }
-    valid = (valid & ~(((1u << TPS) - 1u) << (TPS * s))) | (v << (TPS * s));
+    if (v != 0 && lane == 0) {
+      const uint32_t dst = ring + static_cast<uint32_t>(s * L::kStage);
+      mbar_arrive_expect_tx(bars + 8u * s, static_cast<uint32_t>(__popc(v)) * L::kTile);
+      if (TPS == 2 && v == 3 && from[TPS - 1] == from[0] + L::kTile) {
+        bulk_load(dst, p.cache + from[0], 2 * L::kTile, bars + 8u * s);
+      } else {
+#pragma unroll
+        for (int j = 0; j < TPS; ++j)
+          if (v & (1u << j)) bulk_load(dst + j * L::kTile, p.cache + from[j], L::kTile, bars + 8u * s);
+      }
+    }
+    valid |= v << (TPS * s);
+    if (--to_issue > 0 && ++ahead.blk == ahead.nb) next_segment<L>(p, ahead);
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) issue(s);
@@ -337,8 +340,10 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
   while (units > 0) {
     // ---------------------------------------------------------------- segment: (sequence, head, row tile)
     const Cursor seg = cur;
+    const Queries qu = queries_of(p, seg.b, seg.len);
     const int count = static_cast<int>(min(int64_t(seg.nb - seg.blk), units));
-    const int rows = min(R, seg.n * p.group - seg.rt * R);  // of them in use
+    const int rows = min(R, qu.n * p.group - seg.rt * R);  // of them in use
+    const int plain = min(qu.first, seg.len);  // all rows see the tokens before this one
     // Q: a row scaled by a power of two, in the order of the operands (see the codes' order below)
     {
       constexpr int LN = D / 8;  // lanes of a row
@@ -352,13 +357,13 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
           const int gr = seg.rt * R + row;
           const int i = gr / p.group;
           const int h = seg.h * p.group + (gr - i * p.group);
-          const uint4 wv = *reinterpret_cast<const uint4 *>(p.q + (seg.q0 + i) * p.q_ts + h * p.q_hs + c * 8);
+          const uint4 wv = *reinterpret_cast<const uint4 *>(p.q + (qu.q0 + i) * p.q_ts + h * p.q_hs + c * 8);
           const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = bits_to_float(static_cast<uint16_t>(ww[j >> 1] >> (16 * (j & 1))), p.bf16 != 0);
           if (c == 0) {
             const int j = i;  // a chain sees the query tokens up to itself
-            mask_s[row] = p.tree_mask ? p.tree_mask[seg.q0 + i] : (j >= 63 ? ~0ull : (2ull << j) - 1);
+            mask_s[row] = p.tree_mask ? p.tree_mask[qu.q0 + i] : (j >= 63 ? ~0ull : (2ull << j) - 1);
           }
         } else if (c == 0) {
           mask_s[row] = ~0ull;
@@ -417,12 +422,15 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
       const uint32_t v = (valid >> (TPS * stage)) & ((1u << TPS) - 1u);
       if (v != 0 && ok) {
         ok = __all_sync(0xFFFFFFFFu, wait_phase(bars + 8u * stage, (phases >> stage) & 1u, abort_flag, limit_ns, error));
-        if (ok) phases ^= 1u << stage, valid &= ~(((1u << TPS) - 1u) << (TPS * stage));
+        if (ok) {
+          phases ^= 1u << stage;
+          valid ^= v << (TPS * stage);
+        }
       }
       if (v != 0 && ok) {
         const uint32_t st = ring + static_cast<uint32_t>(stage * L::kStage);
         const int t0 = ((seg.blk + u) * W + warp) * (TPS * 16);
-        const bool whole = v == (1u << TPS) - 1u && t0 + TPS * 16 <= min(seg.first, seg.len);  // all rows see all tokens
+        const bool whole = v == (1u << TPS) - 1u && t0 + TPS * 16 <= plain;  // all rows see all tokens
         // ---- scores of the step's tokens: lane: tokens g, g + 8 of each tile, rows 2 r, 2 r + 1
         float y[TPS][NT][4];
         float sv[TPS][2];
@@ -440,16 +448,17 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
           sv[j][1] = in1 ? bits_to_float(pv1 & 0xFFFFu, p.bf16 != 0) : 0.f;
           const uint32_t z0 = pk0 >> 16, z1 = pk1 >> 16;
           const uint32_t lo0 = (0x6400u + z0) * 0x10001u, lo1 = (0x6400u + z1) * 0x10001u;
-          float acc[NT][4];
+          constexpr int NA = NT == 1 ? 2 : 1;  // chains of products (one row group alone would wait for each product)
+          float acc[NA][NT][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+          for (int x = 0; x < NA * NT * 4; ++x) acc[x / (4 * NT)][x / 4 % NT][x % 4] = 0.f;
           auto step = [&](int kk, const uint32_t (&a)[4]) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               uint32_t b0, b1;
               if constexpr (L::kQSmem) lds64(base + L::kOffQ + ((kk * NT + nt) * 32 + lane) * 8, b0, b1);
               else b0 = qreg[2 * (kk * NT + nt)], b1 = qreg[2 * (kk * NT + nt) + 1];
-              mma_16816<false>(acc[nt], a, b0, b1);
+              mma_16816<false>(acc[kk % NA][nt], a, b0, b1);
             }
           };
           if constexpr (BITS == 8) {
@@ -489,10 +498,8 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            y[j][nt][0] = acc[nt][0] * sk0;
-            y[j][nt][1] = acc[nt][1] * sk0;
-            y[j][nt][2] = acc[nt][2] * sk1;
-            y[j][nt][3] = acc[nt][3] * sk1;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[j][nt][c] = (NA == 2 ? acc[0][nt][c] + acc[NA - 1][nt][c] : acc[0][nt][c]) * (c < 2 ? sk0 : sk1);
           }
         }
         // ---- what the rows do not see
@@ -504,7 +511,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
             for (int c = 0; c < 4; ++c) {
               const int t = t0 + 16 * j + g + 8 * (c >> 1);
               const bool there = ((v >> j) & 1u) && t < seg.len;
-              const int at = t - seg.first;
+              const int at = t - qu.first;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 const bool see = there && (at < 0 || (at < 64 && ((mask_s[8 * nt + 2 * r + (c & 1)] >> at) & 1ull)));
@@ -675,8 +682,9 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
       __syncwarp();  // every lane has read the stage
       if (ok) issue(stage);
       stage = stage + 1 == S ? 0 : stage + 1;
-      if (--units > 0) advance<L>(p, cur);
     }
+    units -= count;
+    if (units > 0) next_segment<L>(p, cur);
 
     // ---------------------------------------------------------------- join the warps
 #pragma unroll
@@ -757,7 +765,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
         if (is_whole) {
           if (row < rows) {
             const int gr = seg.rt * R + row, qi = gr / p.group;
-            const int64_t at = (seg.q0 + qi) * p.q_heads + seg.h * p.group + (gr - qi * p.group);
+            const int64_t at = (qu.q0 + qi) * p.q_heads + seg.h * p.group + (gr - qi * p.group);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
             store_out4(p, at * D + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
             if (p.lse && d == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top == -INFINITY ? sum : (top + log2f(sum)) * kLn2);
@@ -783,26 +791,66 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
         __syncthreads();
         if (*last_s) {
           __threadfence();
-          auto slot_of = [&](int64_t c) { return p.partials + (2 * c + (c == c0 ? 1 : 0)) * int64_t(R) * (D + 2); };
-          for (int i = tid; i < rows * D / 4; i += L::kThreads) {
-            const int row = i / (D / 4), d = (i % (D / 4)) * 4;
-            float top = -INFINITY, sum = 0.f;
-            for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(slot_of(c) + R * D + row));
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          // The parts' maxima and denominators first (side by side: the parts of one long sequence are many),
+          // then their sums, weighted, in the order of the CTAs.
+          const int parts = static_cast<int>(c1 - c0) + 1;
+          auto slot_of = [&](int c) { return p.partials + (2 * (c0 + c) + (c == 0 ? 1 : 0)) * int64_t(R) * (D + 2); };
+          float *red = o_s;              // [kThreads / R][R]
+          float *wgt = o_s + L::kThreads;  // [kChunk][R]
+          constexpr int kChunk = 32, kLanes = L::kThreads / R;
+          const int row_t = tid % R, lane_t = tid / R;
+          float top = -INFINITY;
 #pragma unroll 4
-            for (int64_t c = c0; c <= c1; ++c) {
-              const float *s = slot_of(c);
-              const float mc = __ldcg(s + R * D + row), lc = __ldcg(s + R * (D + 1) + row);
-              const float4 x = __ldcg(reinterpret_cast<const float4 *>(s + row * D + d));
+          for (int c = lane_t; c < parts; c += kLanes) top = fmaxf(top, __ldcg(slot_of(c) + R * D + row_t));
+          red[tid] = top;
+          __syncthreads();
+#pragma unroll
+          for (int x = 0; x < kLanes; ++x) top = fmaxf(top, red[x * R + row_t]);
+          constexpr int kPer = (R * D / 4 + L::kThreads - 1) / L::kThreads;  // groups of four elements of a thread
+          const bool works = R * D / 4 >= L::kThreads || tid < R * D / 4;
+          float4 v[kPer];
+          float sum[kPer];
+#pragma unroll
+          for (int x = 0; x < kPer; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f), sum[x] = 0.f;
+          __syncthreads();
+          if (lane_t == 0) red[row_t] = top;
+          for (int cc = 0; cc < parts; cc += kChunk) {
+            const int now = min(kChunk, parts - cc);
+            for (int c = lane_t; c < now; c += kLanes) {
+              const float mc = __ldcg(slot_of(cc + c) + R * D + row_t), lc = __ldcg(slot_of(cc + c) + R * (D + 1) + row_t);
               const float f = mc == -INFINITY ? (lc == 0.f ? 0.f : 1.f) : exp2_approx(mc - top);
-              sum += lc * f;
-              v = make_float4(fmaf(x.x, f, v.x), fmaf(x.y, f, v.y), fmaf(x.z, f, v.z), fmaf(x.w, f, v.w));
+              wgt[(2 * c) * R + row_t] = f;
+              wgt[(2 * c + 1) * R + row_t] = lc * f;
             }
-            const int gr = seg.rt * R + row, qi = gr / p.group;
-            const int64_t at = (seg.q0 + qi) * p.q_heads + seg.h * p.group + (gr - qi * p.group);
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            store_out4(p, at * D + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-            if (p.lse && d == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top == -INFINITY ? sum : (top + log2f(sum)) * kLn2);
+            __syncthreads();
+#pragma unroll 4
+            for (int c = 0; c < now; ++c) {
+              const float4 *src = reinterpret_cast<const float4 *>(slot_of(cc + c)) + tid;
+#pragma unroll
+              for (int x = 0; x < kPer; ++x) {
+                if (!works) continue;
+                const int row = (tid + x * L::kThreads) / (D / 4);
+                const float4 y = __ldcg(src + x * L::kThreads);
+                const float f = wgt[2 * c * R + row];
+                sum[x] += wgt[(2 * c + 1) * R + row];
+                v[x] = make_float4(fmaf(y.x, f, v[x].x), fmaf(y.y, f, v[x].y), fmaf(y.z, f, v[x].z), fmaf(y.w, f, v[x].w));
+              }
+            }
+            __syncthreads();
+          }
+#pragma unroll
+          for (int x = 0; x < kPer; ++x) {
+            const int i = tid + x * L::kThreads, row = i / (D / 4), d = (i % (D / 4)) * 4;
+            if (works && row < rows) {
+              const int gr = seg.rt * R + row, qi = gr / p.group;
+              const int64_t at = (qu.q0 + qi) * p.q_heads + seg.h * p.group + (gr - qi * p.group);
+              const float inv = sum[x] == 0.f ? 0.f : 1.f / sum[x];
+              store_out4(p, at * D + d, make_float4(v[x].x * inv, v[x].y * inv, v[x].z * inv, v[x].w * inv));
+              if (p.lse && d == 0) {
+                const float t = red[row];
+                p.lse[at] = sum[x] == 0.f ? -INFINITY : (t == -INFINITY ? sum[x] : (t + log2f(sum[x])) * kLn2);
+              }
+            }
           }
         }
       }

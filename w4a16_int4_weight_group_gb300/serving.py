@@ -20,7 +20,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import W4A16Error, _check, _dtype_code, _ptr, _stream, lib, workspace_for
+from . import W4A16Error, _check, _dtype_code, _raw_stream, lib, workspace_for
 
 _i64, _i32, _vp, _f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
 
@@ -107,54 +107,144 @@ def w4a16_kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int 
     return torch.zeros(num_pages, kv_heads, page_size // 16, tile, dtype=torch.uint8, device=device)
 
 
-def _cache(cache: torch.Tensor, head_dim: int) -> KVCache:
-    """The C view of a cache tensor; its bits follow from the tile's bytes."""
-    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous():
+_calls = None  # the C entry points with flat arguments (see csrc/pycall.c)
+
+
+def _bind():
+    """The marshalling module's calls when it was built (less host time a call than ctypes), else the same
+    calls through ctypes."""
+    global _calls
+    L = lib()
+    try:
+        from . import _w4a16_call as m
+    except ImportError:
+        m = None
+    if m is not None and hasattr(m, "bind_serving"):
+        m.bind_serving(*(ctypes.cast(getattr(L, "w4a16_" + n), _vp).value
+                         for n in ("rope", "kv_write", "kv_read", "tree_attention", "token_logprobs")))
+        _calls = m
+    else:
+        _calls = _Ctypes()
+    return _calls
+
+
+class _Ctypes:
+    """The flat calls of the marshalling module through ctypes."""
+
+    @staticmethod
+    def rope(*a):
+        return lib().w4a16_rope(ctypes.byref(Rope(*a[:5])), *a[5:])
+
+    @staticmethod
+    def kv_write(*a):
+        rope = ctypes.byref(Rope(*a[14:19])) if a[14] else None
+        return lib().w4a16_kv_write(ctypes.byref(KVCache(*a[:6])), *a[6:14], rope, *a[19:])
+
+    @staticmethod
+    def kv_read(*a):
+        return lib().w4a16_kv_read(ctypes.byref(KVCache(*a[:6])), *a[6:])
+
+    @staticmethod
+    def tree_attention(*a):
+        return lib().w4a16_tree_attention(ctypes.byref(KVCache(*a[:6])), *a[6:])
+
+    @staticmethod
+    def token_logprobs(*a):
+        return lib().w4a16_token_logprobs(*a)
+
+
+# The checks below use the cheapest tensor queries and read each once: the smallest calls take a few
+# microseconds, of which these are a part.
+_codes = {torch.float16: 0, torch.bfloat16: 1}
+_bits = {(4 * d * b + 128, d): b for d in (64, 128, 256) for b in (4, 8)}
+
+
+def _device(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
+    return t.get_device()
+
+
+def _code(dtype) -> int:
+    c = _codes.get(dtype)
+    return _dtype_code(dtype) if c is None else c  # raises
+
+
+def _current_stream(dev: int) -> int:
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _cache_fields(cache: torch.Tensor, head_dim: int, dev: int):
+    """The fields of w4a16_kv_cache_t of a cache tensor; its bits follow from the tile's bytes."""
+    if cache.dtype is not torch.uint8 or not cache.is_contiguous() or cache.dim() != 4:
         raise ValueError("cache must be a contiguous uint8 tensor [pages, kv_heads, page_size / 16, tile bytes]")
+    if cache.get_device() != dev:
+        raise ValueError("all tensors must be CUDA tensors on the same device")
     pages, heads, tiles, tile = cache.shape
-    for bits in (4, 8):
-        if tile == 4 * head_dim * bits + 128:
-            return KVCache(cache.data_ptr(), pages, heads, head_dim, tiles * 16, bits)
-    raise ValueError(f"cache tiles of {tile} bytes hold neither 4- nor 8-bit heads of {head_dim} elements")
+    bits = _bits.get((tile, head_dim))
+    if bits is None:
+        raise ValueError(f"cache tiles of {tile} bytes hold neither 4- nor 8-bit heads of {head_dim} elements")
+    return cache.data_ptr(), pages, heads, head_dim, tiles * 16, bits
 
 
-def _heads(t: torch.Tensor, name: str, dtype=None):
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+def _cache(cache: torch.Tensor, head_dim: int) -> KVCache:
+    """w4a16_kv_cache_t of a cache tensor, for calls of the C entry points."""
+    return KVCache(*_cache_fields(cache, head_dim, cache.get_device()))
+
+
+def _index(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of this dtype, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on device {dev}")
+    return t.data_ptr()
+
+
+def _heads(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    """Address, token stride and head stride of a [tokens, heads, head_dim] tensor."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} on device {dev}")
+    ts, hs, es = t.stride()
+    if es != 1:
         raise ValueError(f"{name} must be [tokens, heads, head_dim] with a contiguous last dimension")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must have dtype {dtype} (got {t.dtype})")
-    return t
+    return t.data_ptr(), ts, hs
 
 
-def _index(t: torch.Tensor, name: str, dtype, shape, dev):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {dev}")
-    return t
+def _rope(positions, table, interleaved, tokens: int, dev: int):
+    pp = _index(positions, "positions", torch.int64, (tokens,), dev)
+    if table.dtype is not torch.float32 or table.dim() != 2 or not table.is_contiguous() or table.get_device() != dev:
+        raise ValueError(f"table must be a contiguous float32 tensor [positions, rot_dim] on device {dev}")
+    rows, rot = table.shape
+    return pp, table.data_ptr(), rows, rot, 1 if interleaved else 0
 
 
-def _rope(positions, table, interleaved, tokens, dev) -> Rope:
-    _index(positions, "positions", torch.int64, (tokens,), dev)
-    if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous() or table.device != dev:
-        raise ValueError(f"table must be a contiguous float32 tensor [positions, rot_dim] on {dev}")
-    return Rope(positions.data_ptr(), table.data_ptr(), table.shape[0], table.shape[1], int(bool(interleaved)))
+_no_rope = (0, 0, 0, 0, 0)
+
+
+def _three(t: torch.Tensor, name: str):
+    s = t.shape
+    if len(s) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] with a contiguous last dimension")
+    return s
 
 
 def w4a16_rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, interleaved: bool = False,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """x [tokens, heads, head_dim] with its heads turned to `positions` (int64 [tokens]); `out` may be x itself."""
-    _heads(x, "x")
+    shape = _three(x, "x")
+    dev = _device(x)
+    dtype = x.dtype
+    code = _code(dtype)
+    T, H, D = shape
+    xa = _heads(x, "x", dtype, shape, dev)
+    r = _rope(positions, table, interleaved, T, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _heads(out, "out", x.dtype)
-    if out.shape != x.shape or out.device != x.device:
-        raise ValueError("out must have the shape and device of x")
-    code = _dtype_code(x.dtype)
-    if not x.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors")
-    T, H, D = x.shape
-    r = _rope(positions, table, interleaved, T, x.device)
-    _check(lib().w4a16_rope(ctypes.byref(r), x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0),
-                            out.stride(1), T, H, D, code, _stream(x.device)))
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+        oa = (out.data_ptr(), H * D, D)
+    else:
+        oa = _heads(out, "out", dtype, shape, dev)
+    st = (_calls or _bind()).rope(*r, *xa, *oa, T, H, D, code, _current_stream(dev))
+    if st:
+        _check(st)
     return out
 
 
@@ -164,39 +254,37 @@ def w4a16_kv_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots:
                    q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
     """Quantise k and v [tokens, kv_heads, head_dim] into the cache's `slots` (int64 [tokens]). With positions and
     table, k turns first, and q [tokens, q_heads, head_dim], when given, is turned into the returned q_out."""
-    _heads(k, "k")
-    _heads(v, "v", k.dtype)
-    dev = k.device
-    if not k.is_cuda or v.device != dev or cache.device != dev:
-        raise ValueError("all tensors must be CUDA tensors on the same device")
-    T, Hk, D = k.shape
-    if v.shape != k.shape or cache.shape[1] != Hk:
-        raise ValueError(f"k, v and the cache must agree: k {list(k.shape)}, v {list(v.shape)}, cache heads {cache.shape[1]}")
-    code = _dtype_code(k.dtype)
-    c = _cache(cache, D)
-    _index(slots, "slots", torch.int64, (T,), dev)
-    r = None
+    shape = _three(k, "k")
+    dev = _device(k)
+    dtype = k.dtype
+    code = _code(dtype)
+    T, Hk, D = shape
+    ka, va = _heads(k, "k", dtype, shape, dev), _heads(v, "v", dtype, shape, dev)
+    c = _cache_fields(cache, D, dev)
+    if c[2] != Hk:
+        raise ValueError(f"k and v have {Hk} heads, the cache {c[2]}")
+    sp = _index(slots, "slots", torch.int64, (T,), dev)
     if (positions is None) != (table is None):
         raise ValueError("positions and table go together")
-    if positions is not None:
-        r = _rope(positions, table, interleaved, T, dev)
-    qp = (None, 0, 0, 0, None)
+    r = _no_rope if positions is None else _rope(positions, table, interleaved, T, dev)
+    qa = (0, 0, 0, 0, 0)
     if q is not None:
-        if r is None:
+        if positions is None:
             raise ValueError("q is only taken with positions and table (it is turned, not cached)")
-        _heads(q, "q", k.dtype)
-        if q.shape[0] != T or q.shape[2] != D or q.device != dev:
-            raise ValueError("q must be [tokens, q_heads, head_dim] on the device of k")
+        qs = _three(q, "q")
+        Hq = qs[1]
+        qv = _heads(q, "q", dtype, (T, Hq, D), dev)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.device != dev or not q_out.is_contiguous():
-            raise ValueError("q_out must be a contiguous tensor like q")
-        qp = (q.data_ptr(), q.stride(0), q.stride(1), q.shape[1], q_out.data_ptr())
+            q_out = torch.empty(qs, dtype=dtype, device=k.device)
+            qo = q_out.data_ptr()
+        else:
+            qo = _index(q_out, "q_out", dtype, qs, dev)
+        qa = (*qv, Hq, qo)
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    _check(lib().w4a16_kv_write(ctypes.byref(c), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-                                v.stride(1), slots.data_ptr(), T, None if r is None else ctypes.byref(r), *qp, code,
-                                _stream(dev)))
+    st = (_calls or _bind()).kv_write(*c, *ka, *va, sp, T, *r, *qa, code, _current_stream(dev))
+    if st:
+        _check(st)
     return q_out
 
 
@@ -204,23 +292,31 @@ def w4a16_kv_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype
                   k_out: Optional[torch.Tensor] = None,
                   v_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Keys and values [tokens, kv_heads, head_dim] of the given slots, dequantised to dtype (the one written)."""
-    dev = cache.device
-    if not cache.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors")
-    c = _cache(cache, head_dim)
-    code = _dtype_code(dtype)
+    dev = _device(cache)
+    c = _cache_fields(cache, head_dim, dev)
+    code = _code(dtype)
     if slots.dim() != 1:
         raise ValueError("slots must be a 1-D int64 tensor")
     T = slots.shape[0]
-    _index(slots, "slots", torch.int64, (T,), dev)
-    shape = (T, cache.shape[1], head_dim)
-    k_out = torch.empty(shape, dtype=dtype, device=dev) if k_out is None else _index(k_out, "k_out", dtype, shape, dev)
-    v_out = torch.empty(shape, dtype=dtype, device=dev) if v_out is None else _index(v_out, "v_out", dtype, shape, dev)
-    _check(lib().w4a16_kv_read(ctypes.byref(c), slots.data_ptr(), T, k_out.data_ptr(), v_out.data_ptr(), code, _stream(dev)))
+    sp = _index(slots, "slots", torch.int64, (T,), dev)
+    shape = (T, c[2], head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=cache.device)
+        kp = k_out.data_ptr()
+    else:
+        kp = _index(k_out, "k_out", dtype, shape, dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=cache.device)
+        vp = v_out.data_ptr()
+    else:
+        vp = _index(v_out, "v_out", dtype, shape, dev)
+    st = (_calls or _bind()).kv_read(*c, sp, T, kp, vp, code, _current_stream(dev))
+    if st:
+        _check(st)
     return k_out, v_out
 
 
-_attention_ws: dict = {}  # workspace bytes per (device, max_q, q_heads, kv_heads, head_dim)
+_attention_ws: dict = {}  # workspace bytes: a pure function of the sizes and the device
 
 
 def w4a16_tree_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -235,41 +331,47 @@ def w4a16_tree_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch
     a sequence, at most 64 (unless given: min(total_q, 64), 1 without q_start). Returns out, or (out, lse) with lse
     float32 [total_q, q_heads]. A query that sees nothing gives zeros and -inf.
     """
-    _heads(q, "q")
-    dev = q.device
-    if not q.is_cuda or cache.device != dev:
-        raise ValueError("all tensors must be CUDA tensors on the same device")
-    total, Hq, D = q.shape
-    code = _dtype_code(q.dtype)
-    c = _cache(cache, D)
-    if page_table.dim() != 2:
+    shape = _three(q, "q")
+    dev = _device(q)
+    dtype = q.dtype
+    code = _code(dtype)
+    total, Hq, D = shape
+    qa = _heads(q, "q", dtype, shape, dev)
+    c = _cache_fields(cache, D, dev)
+    pt = page_table.shape
+    if len(pt) != 2:
         raise ValueError("page_table must be [batch, max_pages]")
-    B, cols = page_table.shape
-    _index(page_table, "page_table", torch.int32, (B, cols), dev)
-    _index(kv_lens, "kv_lens", torch.int32, (B,), dev)
-    if q_start is not None:
-        _index(q_start, "q_start", torch.int32, (B + 1,), dev)
-    if tree_mask is not None:
-        _index(tree_mask, "tree_mask", torch.int64, (total,), dev)
+    B, cols = pt
+    pp = _index(page_table, "page_table", torch.int32, pt, dev)
+    lp = _index(kv_lens, "kv_lens", torch.int32, (B,), dev)
+    sp = 0 if q_start is None else _index(q_start, "q_start", torch.int32, (B + 1,), dev)
+    mp = 0 if tree_mask is None else _index(tree_mask, "tree_mask", torch.int64, (total,), dev)
     if max_q is None:
         max_q = 1 if q_start is None else max(1, min(total, 64))
     if softmax_scale is None:
         softmax_scale = D ** -0.5
     if out is None:
-        out = torch.empty((total, Hq, D), dtype=q.dtype, device=dev)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+        op = out.data_ptr()
     else:
-        _index(out, "out", q.dtype, (total, Hq, D), dev)
-    lse = torch.empty((total, Hq), dtype=torch.float32, device=dev) if return_lse else None
-    key = (dev.index, max_q, Hq, c.kv_heads, D)
+        op = _index(out, "out", dtype, shape, dev)
+    lse, sep = None, 0
+    if return_lse:
+        lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
+        sep = lse.data_ptr()
+    stream = _current_stream(dev)
+    key = (dev, max_q, Hq, c[2], D)
     need = _attention_ws.get(key)
     if need is None:
-        need = _attention_ws[key] = int(lib().w4a16_tree_attention_workspace_size(max_q, Hq, c.kv_heads, D))
-    stream = _stream(dev)
-    ws = workspace_for(dev, stream.value or 0, need) if need else None
-    _check(lib().w4a16_tree_attention(ctypes.byref(c), q.data_ptr(), q.stride(0), q.stride(1), Hq, total, _ptr(q_start), B,
-                                      max_q, kv_lens.data_ptr(), page_table.data_ptr(), cols, _ptr(tree_mask),
-                                      softmax_scale, out.data_ptr(), _ptr(lse), code, _ptr(ws),
-                                      0 if ws is None else ws.numel(), stream))
+        need = _attention_ws[key] = int(lib().w4a16_tree_attention_workspace_size(max_q, Hq, c[2], D))
+    wp = wb = 0
+    if need:
+        ws = workspace_for(q.device, stream, need)
+        wp, wb = ws.data_ptr(), ws.numel()
+    st = (_calls or _bind()).tree_attention(*c, *qa, Hq, total, sp, B, max_q, lp, pp, cols, mp, softmax_scale, op, sep, code, wp, wb,
+                                            stream)
+    if st:
+        _check(st)
     return (out, lse) if return_lse else out
 
 
@@ -278,26 +380,32 @@ def w4a16_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = 
 
     tokens: int64 [rows] or [rows, n]; logprobs float32 of its shape; entropy float32 [rows]; top_ids int64 and
     top_logprobs float32 [rows, top_k] (top_k <= 32), descending, equal logits by ascending index. Natural logs."""
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    s = logits.shape
+    if len(s) != 2:
         raise ValueError("logits must be [rows, vocab] with contiguous rows")
-    if not logits.is_cuda:
-        raise ValueError("all tensors must be CUDA tensors")
-    dev = logits.device
-    rows, vocab = logits.shape
-    code = 2 if logits.dtype == torch.float32 else _dtype_code(logits.dtype)
+    rows, vocab = s
+    stride, es = logits.stride()
+    if es != 1 and vocab > 1:
+        raise ValueError("logits must be [rows, vocab] with contiguous rows")
+    dev = _device(logits)
+    device = logits.device
+    code = 2 if logits.dtype is torch.float32 else _code(logits.dtype)
     if tokens is None:
-        tokens = torch.empty((rows, 0), dtype=torch.int64, device=dev)
-    if tokens.dim() not in (1, 2):
-        raise ValueError("tokens must be [rows] or [rows, n]")
-    _index(tokens, "tokens", torch.int64, (rows,) + tuple(tokens.shape[1:]), dev)
-    n = 1 if tokens.dim() == 1 else tokens.shape[1]
-    lp = torch.empty(tokens.shape, dtype=torch.float32, device=dev)
-    entropy = torch.empty(rows, dtype=torch.float32, device=dev)
-    ids = torch.empty((rows, top_k), dtype=torch.int64, device=dev)
-    top = torch.empty((rows, top_k), dtype=torch.float32, device=dev)
-    stride = logits.stride(0) if rows > 1 else vocab
-    _check(lib().w4a16_token_logprobs(logits.data_ptr(), stride, rows, vocab, code, tokens.data_ptr(), n, top_k, lp.data_ptr(),
-                                      entropy.data_ptr(), ids.data_ptr(), top.data_ptr(), _stream(dev)))
+        shape, n, tp = (rows, 0), 0, 0
+    else:
+        shape = tokens.shape
+        if len(shape) not in (1, 2) or shape[0] != rows:
+            raise ValueError("tokens must be [rows] or [rows, n]")
+        tp = _index(tokens, "tokens", torch.int64, shape, dev)
+        n = 1 if len(shape) == 1 else shape[1]
+    lp = torch.empty(shape, dtype=torch.float32, device=device)
+    entropy = torch.empty(rows, dtype=torch.float32, device=device)
+    ids = torch.empty((rows, top_k), dtype=torch.int64, device=device)
+    top = torch.empty((rows, top_k), dtype=torch.float32, device=device)
+    st = (_calls or _bind()).token_logprobs(logits.data_ptr(), stride if rows > 1 else vocab, rows, vocab, code, tp, n, top_k,
+                                            lp.data_ptr(), entropy.data_ptr(), ids.data_ptr(), top.data_ptr(), _current_stream(dev))
+    if st:
+        _check(st)
     return lp, entropy, ids, top
 
 

@@ -1,5 +1,5 @@
 // Attention of drafted tokens over the quantised paged cache: dispatch, workspace and failure detection
-// (the kernels: attention_stream.cuh).
+// (the kernels: attention_stream.cuh and attention_tiles.cuh).
 #include <mutex>
 
 #include "attention.h"
@@ -65,6 +65,9 @@ cudaError_t launch_tree_attention(const AttentionArgs &a, const DeviceInfo &dev)
   }
   const cudaError_t e = control_of(dev.device, &p.control);
   if (e != cudaSuccess) return e;
+  if (use_tiles(a.max_q * p.group, a.cache.head_dim))
+    return a.cache.head_dim == 64 ? launch_tiles<64>(p, a.cache.bits, dev.num_sms, a.stream)
+                                  : launch_tiles<128>(p, a.cache.bits, dev.num_sms, a.stream);
   const int rows = stream_rows(a.max_q * p.group, a.cache.head_dim);
   if (a.cache.head_dim == 64) return launch_stream<64>(p, a.cache.bits, rows, dev.num_sms, a.stream);
   if (a.cache.head_dim == 128) return launch_stream<128>(p, a.cache.bits, rows, dev.num_sms, a.stream);
@@ -72,8 +75,10 @@ cudaError_t launch_tree_attention(const AttentionArgs &a, const DeviceInfo &dev)
 }
 
 size_t tree_attention_workspace_bytes(int max_q, int q_heads, int kv_heads, int head_dim, int num_sms) {
-  const int rows = stream_rows(max_q * (q_heads / kv_heads), head_dim);
-  const int64_t ctas = 2 * num_sms < kMaxCtas ? 2 * num_sms : kMaxCtas;
+  const int max_rows = max_q * (q_heads / kv_heads);
+  const bool tiles = use_tiles(max_rows, head_dim);
+  const int rows = tiles ? kTileRows : stream_rows(max_rows, head_dim);
+  const int64_t want = tiles ? num_sms : 2 * num_sms, ctas = want < kMaxCtas ? want : kMaxCtas;
   return kFlagBytes + static_cast<size_t>(2 * ctas * partial_floats(rows, head_dim) * 4);
 }
 

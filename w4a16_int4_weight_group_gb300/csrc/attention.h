@@ -41,6 +41,12 @@ inline int64_t partial_floats(int rows, int head_dim) { return int64_t(rows) * (
 // Rows of a row tile of the streaming kernel for sequences of max_rows query rows on a cache head.
 inline int stream_rows(int max_rows, int head_dim) { return max_rows <= 8 ? 8 : max_rows <= 16 || head_dim == 256 ? 16 : 32; }
 
+// Query rows of a cache head from which the kernel on the fifth-generation tensor cores takes over, and its row tile.
+constexpr int kTileRows = 128;
+inline bool use_tiles(int max_rows, int head_dim) { return max_rows > 32 && head_dim <= 128; }
+
+template <int D>
+cudaError_t launch_tiles(const Params &p, int bits, int num_sms, cudaStream_t stream);  // head_dim 64 and 128
 template <int D>
 cudaError_t launch_stream(const Params &p, int bits, int rows, int num_sms, cudaStream_t stream);
 

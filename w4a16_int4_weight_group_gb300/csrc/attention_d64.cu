@@ -1,6 +1,4 @@
-// The attention kernels for heads of 64 elements (a translation unit of their own, to compile in parallel).
-#include <atomic>
-
+// The streaming attention kernel for heads of 64 elements (a translation unit of their own, to compile in parallel).
 #include "attention_stream.cuh"
 
 namespace w4a16 {

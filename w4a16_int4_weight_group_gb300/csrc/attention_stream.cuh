@@ -32,20 +32,11 @@
 #pragma once
 
 #include "attention.h"
+#include "attention_common.cuh"
 #include "common.cuh"
 
 namespace w4a16 {
 namespace attention {
-
-constexpr uint64_t kDefaultWaitNs = 2000000000ull;  // 2 s
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 1.f;        // how far (powers of two) scores may exceed the running maximum
-constexpr float kProbExp = 14.f;     // probabilities are held times 2^14: at most 2^15 with the slack, under 65504
-constexpr float kProbUnit = 16384.f;
-constexpr float kSmall = 6.103515625e-05f;  // 2^-14, the smallest normal fp16 number
-constexpr float kPlane = 268435456.f;       // 2^28
-constexpr int kPlanes = 5;                  // 2^-14 - 4 * 28 = 2^-126
 
 template <int D_, int BITS_, int NT_>
 struct StreamLayout {
@@ -81,68 +72,10 @@ struct StreamLayout {
   static_assert(kOffRing % 128 == 0 && kOffO % 16 == 0 && kTile % 128 == 0, "alignment");
 };
 
-// Position in the list of units, and what of the sequence it takes to walk on.
-struct Cursor {
-  int b, h, rt, blk;
-  int nb, nrt;  // of the sequence: units of a segment, row tiles
-  int len;      // cached tokens
-};
-// What a segment takes beyond that.
-struct Queries {
-  int64_t q0;    // row of the first query token
-  int n, first;  // query tokens, cache position of the first of them
-};
-
-__device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-__device__ __forceinline__ int length_of(const Params &p, int b) {
-  const int64_t cap = p.max_pages * p.page_tiles * 16;
-  const int len = p.kv_lens[b];
-  return len < 0 ? 0 : static_cast<int>(min(int64_t(len), cap));
-}
-__device__ __forceinline__ Queries queries_of(const Params &p, int b, int len) {
-  const int64_t q0 = p.q_start ? p.q_start[b] : b, q1 = p.q_start ? p.q_start[b + 1] : b + 1;
-  int64_t n = q1 - q0;
-  if (n < 0 || q0 < 0 || q1 > p.total_q) n = 0;
-  return Queries{q0, static_cast<int>(min(n, int64_t(p.max_q))), static_cast<int>(len - n)};
-}
-
-// Loads sequence b into the cursor; units of the sequence (0: nothing to do).
-template <class L>
-__device__ __forceinline__ int64_t load_sequence(const Params &p, int b, Cursor &c) {
-  c.b = b;
-  c.h = c.rt = c.blk = 0;
-  c.len = length_of(p, b);
-  c.nrt = static_cast<int>((int64_t(queries_of(p, b, c.len).n) * p.group + L::R - 1) / L::R);
-  c.nb = c.len > 0 ? (c.len + L::kUnit - 1) / L::kUnit : 1;
-  return int64_t(c.nb) * c.nrt * p.kv_heads;
-}
-
-// The first unit of the next segment (the caller knows that there is one).
-template <class L>
-__device__ __forceinline__ void next_segment(const Params &p, Cursor &c) {
-  c.blk = 0;
-  if (++c.rt < c.nrt) return;
-  c.rt = 0;
-  if (++c.h < p.kv_heads) return;
-  int b = c.b + 1;
-  while (b < p.batch && load_sequence<L>(p, b, c) == 0) ++b;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) { return sub2_rn<false>(a, b); }
 __device__ __forceinline__ uint32_t transpose8(uint32_t a) {  // 8 x 8 matrix of 16-bit elements
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&h);
 }
 // N 32-bit words from shared memory
 template <int N>
@@ -178,18 +111,6 @@ __device__ __forceinline__ void add_product(float (&acc)[4], const uint32_t (&a)
   }
 }
 
-// Writes a finished value group of four elements of a row.
-__device__ __forceinline__ void store_out4(const Params &p, int64_t at, float4 v) {
-  uint2 w;
-  if (p.bf16) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    w = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-  } else {
-    w = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
-  }
-  *reinterpret_cast<uint2 *>(p.out + at) = w;
-}
-
 template <class L>
 __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Params p) {
   constexpr int D = L::D, BITS = L::BITS, NT = L::NT, R = L::R, RB = L::RB, W = L::W, S = L::S, TPS = L::TPS;
@@ -208,8 +129,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
   const uint32_t stall_bar = base + L::kOffBar + 8u * S * W;
   const uint32_t abort_flag = base + L::kOffMisc;
   volatile uint32_t *last_s = reinterpret_cast<volatile uint32_t *>(smem + L::kOffMisc + 4);
-  volatile int *start_s = reinterpret_cast<volatile int *>(smem + L::kOffMisc + 8);  // sequence that the share starts in
-  volatile int64_t *rest_s = reinterpret_cast<volatile int64_t *>(smem + L::kOffMisc + 16);  // units before it in the sequence
+  volatile int64_t *share_s = reinterpret_cast<volatile int64_t *>(smem + L::kOffMisc + 8);
   int64_t *scan_s = reinterpret_cast<int64_t *>(smem + L::kOffMisc + 32);
   const uint32_t ring = base + L::kOffRing + static_cast<uint32_t>(warp * S * L::kStage);
 
@@ -226,67 +146,10 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
   const uint64_t limit_ns = lim ? lim : kDefaultWaitNs;
   unsigned int *error = &p.control->error;
 
-  // ---- this CTA's share of the units
   Cursor cur;
-  const int slice = (p.batch + L::kThreads - 1) / L::kThreads;
-  int64_t mine = 0;
-  for (int b = tid * slice; b < min(p.batch, (tid + 1) * slice); ++b) mine += load_sequence<L>(p, b, cur);
-  int64_t upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) scan_s[warp] = upto;
-  __syncthreads();
-  int64_t before = upto - mine, total = 0;
-  for (int w = 0; w < W; ++w) {
-    if (w < warp) before += scan_s[w];
-    total += scan_s[w];
-  }
-  const int64_t ctas = total < gridDim.x ? total : gridDim.x;
+  int64_t u1, total, ctas, units;
+  if (!share_of<L, W>(p, scan_s, share_s, cur, u1, total, ctas, units)) return;  // nothing for this CTA
   const int64_t cta = blockIdx.x;
-  if (cta >= ctas) return;  // the whole CTA
-  int64_t u0 = cta * total / ctas, u1 = (cta + 1) * total / ctas;
-  if (u0 >= before && u0 < before + mine) {
-    int64_t at = u0 - before;
-    for (int b = tid * slice;; ++b) {
-      const int64_t units = load_sequence<L>(p, b, cur);
-      if (at < units) {
-        *start_s = b;
-        *rest_s = at;
-        break;
-      }
-      at -= units;
-    }
-  }
-  __syncthreads();
-  {
-    load_sequence<L>(p, *start_s, cur);
-    int64_t at = *rest_s;
-    cur.h = static_cast<int>(at / (int64_t(cur.nb) * cur.nrt));
-    at -= int64_t(cur.h) * cur.nb * cur.nrt;
-    cur.rt = static_cast<int>(at / cur.nb);
-    cur.blk = static_cast<int>(at - int64_t(cur.rt) * cur.nb);
-  }
-  int64_t units = u1 - u0;
-  if (!p.flags) {
-    // no workspace: the share is the segments that start in [u0, u1), whole
-    if (cur.blk != 0) {
-      units -= min(int64_t(cur.nb - cur.blk), units);
-      if (units == 0) return;
-      next_segment<L>(p, cur);
-    }
-    Cursor c = cur;
-    int64_t left = units, whole = 0;
-    while (true) {
-      whole += c.nb;
-      left -= c.nb;
-      if (left <= 0) break;
-      next_segment<L>(p, c);
-    }
-    units = whole;
-  }
 
   // ---- the ring: copies are issued S steps ahead, across segments
   Cursor ahead = cur;
@@ -351,33 +214,17 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
       for (int row = tid / LN; row < R; row += L::kThreads / LN) {
         const int c = tid % LN;
         float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = 0.f;
-        if (row < rows) {
-          const int gr = seg.rt * R + row;
-          const int i = gr / p.group;
-          const int h = seg.h * p.group + (gr - i * p.group);
-          const uint4 wv = *reinterpret_cast<const uint4 *>(p.q + (qu.q0 + i) * p.q_ts + h * p.q_hs + c * 8);
-          const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = bits_to_float(static_cast<uint16_t>(ww[j >> 1] >> (16 * (j & 1))), p.bf16 != 0);
-          if (c == 0) {
-            const int j = i;  // a chain sees the query tokens up to itself
-            mask_s[row] = p.tree_mask ? p.tree_mask[qu.q0 + i] : (j >= 63 ? ~0ull : (2ull << j) - 1);
-          }
-        } else if (c == 0) {
-          mask_s[row] = ~0ull;
-        }
+        load_query<8>(p, seg, qu, row, rows, R, c * 8, x);
+        if (c == 0) mask_s[row] = row < rows ? mask_word(p, qu, (seg.rt * R + row) / p.group) : ~0ull;
         float top = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
         const uint32_t lanes = LN == 32 ? 0xFFFFFFFFu : ((1u << (LN & 31)) - 1u) << (lane / LN * LN);
 #pragma unroll
         for (int s = LN / 2; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, s));
-        int e = top > 0.f ? 12 - (static_cast<int>((__float_as_uint(top) >> 23) & 0xFFu) - 127) : 0;
-        e = min(e, 100);
-        const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23) * (p.scale < 0.f ? -1.f : 1.f);
-        if (c == 0) qs_s[row] = fabsf(p.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        float up, unit;
+        query_unit(p, top, up, unit);
+        if (c == 0) qs_s[row] = unit;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int d = c * 8 + j;
@@ -791,67 +638,9 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
         __syncthreads();
         if (*last_s) {
           __threadfence();
-          // The parts' maxima and denominators first (side by side: the parts of one long sequence are many),
-          // then their sums, weighted, in the order of the CTAs.
           const int parts = static_cast<int>(c1 - c0) + 1;
           auto slot_of = [&](int c) { return p.partials + (2 * (c0 + c) + (c == 0 ? 1 : 0)) * int64_t(R) * (D + 2); };
-          float *red = o_s;              // [kThreads / R][R]
-          float *wgt = o_s + L::kThreads;  // [kChunk][R]
-          constexpr int kChunk = 32, kLanes = L::kThreads / R;
-          const int row_t = tid % R, lane_t = tid / R;
-          float top = -INFINITY;
-#pragma unroll 4
-          for (int c = lane_t; c < parts; c += kLanes) top = fmaxf(top, __ldcg(slot_of(c) + R * D + row_t));
-          red[tid] = top;
-          __syncthreads();
-#pragma unroll
-          for (int x = 0; x < kLanes; ++x) top = fmaxf(top, red[x * R + row_t]);
-          constexpr int kPer = (R * D / 4 + L::kThreads - 1) / L::kThreads;  // groups of four elements of a thread
-          const bool works = R * D / 4 >= L::kThreads || tid < R * D / 4;
-          float4 v[kPer];
-          float sum[kPer];
-#pragma unroll
-          for (int x = 0; x < kPer; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f), sum[x] = 0.f;
-          __syncthreads();
-          if (lane_t == 0) red[row_t] = top;
-          for (int cc = 0; cc < parts; cc += kChunk) {
-            const int now = min(kChunk, parts - cc);
-            for (int c = lane_t; c < now; c += kLanes) {
-              const float mc = __ldcg(slot_of(cc + c) + R * D + row_t), lc = __ldcg(slot_of(cc + c) + R * (D + 1) + row_t);
-              const float f = mc == -INFINITY ? (lc == 0.f ? 0.f : 1.f) : exp2_approx(mc - top);
-              wgt[(2 * c) * R + row_t] = f;
-              wgt[(2 * c + 1) * R + row_t] = lc * f;
-            }
-            __syncthreads();
-#pragma unroll 4
-            for (int c = 0; c < now; ++c) {
-              const float4 *src = reinterpret_cast<const float4 *>(slot_of(cc + c)) + tid;
-#pragma unroll
-              for (int x = 0; x < kPer; ++x) {
-                if (!works) continue;
-                const int row = (tid + x * L::kThreads) / (D / 4);
-                const float4 y = __ldcg(src + x * L::kThreads);
-                const float f = wgt[2 * c * R + row];
-                sum[x] += wgt[(2 * c + 1) * R + row];
-                v[x] = make_float4(fmaf(y.x, f, v[x].x), fmaf(y.y, f, v[x].y), fmaf(y.z, f, v[x].z), fmaf(y.w, f, v[x].w));
-              }
-            }
-            __syncthreads();
-          }
-#pragma unroll
-          for (int x = 0; x < kPer; ++x) {
-            const int i = tid + x * L::kThreads, row = i / (D / 4), d = (i % (D / 4)) * 4;
-            if (works && row < rows) {
-              const int gr = seg.rt * R + row, qi = gr / p.group;
-              const int64_t at = (qu.q0 + qi) * p.q_heads + seg.h * p.group + (gr - qi * p.group);
-              const float inv = sum[x] == 0.f ? 0.f : 1.f / sum[x];
-              store_out4(p, at * D + d, make_float4(v[x].x * inv, v[x].y * inv, v[x].z * inv, v[x].w * inv));
-              if (p.lse && d == 0) {
-                const float t = red[row];
-                p.lse[at] = sum[x] == 0.f ? -INFINITY : (t == -INFINITY ? sum[x] : (t + log2f(sum[x])) * kLn2);
-              }
-            }
-          }
+          join_parts<R, D, L::kThreads, 32>(p, seg, qu, rows, parts, slot_of, o_s, tid, [] { __syncthreads(); });
         }
       }
     }
@@ -864,40 +653,13 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
   }
 }
 
-template <class L>
-cudaError_t start(const Params &p, int num_sms, cudaStream_t stream) {
-  static std::atomic<uint64_t> raised{0};  // devices whose limit on dynamic shared memory has been raised
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(raised.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(stream_kernel<L>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) raised.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
-  }
-  cudaLaunchConfig_t cfg = {};
-  int ctas = num_sms * L::kCtas;
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas < kMaxCtas ? ctas : kMaxCtas), 1, 1);
-  cfg.blockDim = dim3(L::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = L::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, stream_kernel<L>, p);
-  if (e == cudaSuccess) note_launch();
-  return e;
-}
-
 template <int D>
 cudaError_t launch_stream(const Params &p, int bits, int rows, int num_sms, cudaStream_t stream) {
-  if (rows == 8) return bits == 8 ? start<StreamLayout<D, 8, 1>>(p, num_sms, stream) : start<StreamLayout<D, 4, 1>>(p, num_sms, stream);
+  if (rows == 8) return bits == 8 ? start_kernel<StreamLayout<D, 8, 1>>(stream_kernel<StreamLayout<D, 8, 1>>, num_sms * StreamLayout<D, 8, 1>::kCtas, p, stream) : start_kernel<StreamLayout<D, 4, 1>>(stream_kernel<StreamLayout<D, 4, 1>>, num_sms * StreamLayout<D, 4, 1>::kCtas, p, stream);
   if constexpr (D != 256) {
-    if (rows == 32) return bits == 8 ? start<StreamLayout<D, 8, 4>>(p, num_sms, stream) : start<StreamLayout<D, 4, 4>>(p, num_sms, stream);
+    if (rows == 32) return bits == 8 ? start_kernel<StreamLayout<D, 8, 4>>(stream_kernel<StreamLayout<D, 8, 4>>, num_sms * StreamLayout<D, 8, 4>::kCtas, p, stream) : start_kernel<StreamLayout<D, 4, 4>>(stream_kernel<StreamLayout<D, 4, 4>>, num_sms * StreamLayout<D, 4, 4>::kCtas, p, stream);
   }
-  return bits == 8 ? start<StreamLayout<D, 8, 2>>(p, num_sms, stream) : start<StreamLayout<D, 4, 2>>(p, num_sms, stream);
+  return bits == 8 ? start_kernel<StreamLayout<D, 8, 2>>(stream_kernel<StreamLayout<D, 8, 2>>, num_sms * StreamLayout<D, 8, 2>::kCtas, p, stream) : start_kernel<StreamLayout<D, 4, 2>>(stream_kernel<StreamLayout<D, 4, 2>>, num_sms * StreamLayout<D, 4, 2>::kCtas, p, stream);
 }
 
 }  // namespace attention

@@ -9,10 +9,11 @@
 // element); the threads' triples are joined at the end, the CTAs of a row (a thread-block cluster, when
 // there are few rows) through distributed shared memory, in a fixed order.
 //
-// The alternatives come from the same pass. After the first step every group of eight threads knows its
+// The alternatives come from the same pass. After the first step every group of four threads knows its
 // largest element; the k-th largest of these 64 is a bound that at least k elements reach, so only
-// elements that reach it can be among the k largest. They go to a list in shared memory (about 1.5 k of
-// 128000 normal logits for k = 20), whose members are ranked by counting at the end. Elements are ordered
+// elements that reach it can be among the k largest. They go to a list in shared memory, whose members are ranked
+// by counting; after 1, 2, 4, .. steps only the k largest are kept and the last of them is the new bound (so about
+// k of them are added while the elements seen double). Elements are ordered
 // by (value, lower index), a total order, so equal logits, and masked rows in which most elements are the
 // same, neither overflow the list nor make the result depend on timing. A row that rises along its length
 // can overflow it; it is then read again k times.
@@ -22,11 +23,13 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kCtas = 4;  // on an SM
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroups = kThreads / 8;
+constexpr int kGroupLanes = 4;
+constexpr int kGroups = kThreads / kGroupLanes;
 constexpr int kMaxTopK = 32;
-constexpr int kList = 2560;  // at least 2048 + 14: a segment in which fewer than k groups have elements fits
+constexpr int kList = 1280;  // at least 1024 + 14: a segment in which fewer than k groups have elements fits
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFar = -1.0e4f;  // exp(kFar) is zero; keeps -inf and the type's lowest value out of products
 
@@ -41,36 +44,60 @@ struct Params {
   int64_t *top_ids;
 };
 
+// Two fp32 numbers in one 64-bit register pair
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 struct F32 {};
 template <class DT>
 struct Elem {
   static constexpr int kBytes = 2, kVec = 8;
+  static constexpr uint32_t kNone = DT::kBF16 ? 0xFF80FF80u : 0xFC00FC00u;  // -infinity
+  static __device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (DT::kBF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ uint64_t two(uint32_t w) {
+    if constexpr (DT::kBF16) {
+      return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+      return pair(f.x, f.y);
+    }
+  }
+
   static __device__ __forceinline__ float at(const void *p, int64_t i) {
     return bits_to_float(reinterpret_cast<const uint16_t *>(p)[i], DT::kBF16);
-  }
-  static __device__ __forceinline__ void unpack(const uint4 &w, float *x) {
-    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT::kBF16) {
-        x[2 * i] = __uint_as_float(r[i] << 16);
-        x[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-      }
-    }
   }
 };
 template <>
 struct Elem<F32> {
   static constexpr int kBytes = 4, kVec = 4;
+  static constexpr uint32_t kNone = 0xFF800000u;
   static __device__ __forceinline__ float at(const void *p, int64_t i) { return reinterpret_cast<const float *>(p)[i]; }
-  static __device__ __forceinline__ void unpack(const uint4 &w, float *x) {
-    x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y);
-    x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
-  }
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -82,6 +109,32 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// The largest element of N vectors, NaN if one is NaN.
+template <class DT, int N>
+__device__ __forceinline__ float top_of(const uint4 (&w)[N]) {
+  if constexpr (Elem<DT>::kVec == 4) {
+    float t = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      t = max_nan(max_nan(t, max_nan(__uint_as_float(w[i].x), __uint_as_float(w[i].y))),
+                  max_nan(__uint_as_float(w[i].z), __uint_as_float(w[i].w)));
+    return t;
+  } else {
+    using E = Elem<DT>;
+    uint32_t t = E::max_words(E::max_words(w[0].x, w[0].y), E::max_words(w[0].z, w[0].w));
+#pragma unroll
+    for (int i = 1; i < N; ++i) t = E::max_words(t, E::max_words(E::max_words(w[i].x, w[i].y), E::max_words(w[i].z, w[i].w)));
+    float a, b;
+    unpair(E::two(t), a, b);
+    return max_nan(a, b);
+  }
+}
+// Elements 2 i and 2 i + 1 of a vector (F32: i = 0, 1; else 0 .. 3)
+template <class DT>
+__device__ __forceinline__ uint64_t two_of(const uint4 &w, int i) {
+  if constexpr (Elem<DT>::kVec == 4) return i == 0 ? pair(__uint_as_float(w.x), __uint_as_float(w.y)) : pair(__uint_as_float(w.z), __uint_as_float(w.w));
+  else return Elem<DT>::two(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w);
 }
 // A whole number that orders by value, then by the lower index. -0 counts as +0.
 __device__ __forceinline__ uint64_t key_of(float v, uint32_t index) {
@@ -116,7 +169,7 @@ __device__ __forceinline__ void join(Stats &a, Stats b) {
 }
 
 template <class DT, int U>
-__global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kCtas) logprobs_kernel(const Params p) {
   using E = Elem<DT>;
   constexpr int kVec = E::kVec;
   __shared__ uint64_t list[kList];
@@ -163,40 +216,55 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Params p) {
     }
   };
 
-  for (int j0 = 0; j0 == 0 || j0 < n_vec; j0 += kThreads * U) {
-    uint4 w[U];
+  uint4 w[U], ahead[U];
+  auto fetch = [&](uint4 (&v)[U], int j0) {
+    if (j0 + U * kThreads <= n_vec) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * kThreads + tid;
-      if (j < n_vec) w[u] = __ldcs(vec + j);
-    }
-    float x[U * kVec];
+      for (int u = 0; u < U; ++u) v[u] = __ldcs(vec + j0 + u * kThreads + tid);
+    } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (j0 + u * kThreads + tid < n_vec) {
-        E::unpack(w[u], x + u * kVec);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) x[u * kVec + e] = -INFINITY;
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * kThreads + tid;
+        v[u] = make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+        if (j < n_vec) v[u] = __ldcs(vec + j);
       }
     }
-    float sm = j0 == 0 ? xe : -INFINITY;
-#pragma unroll
-    for (int e = 0; e < U * kVec; ++e) sm = max_nan(sm, x[e]);
-    rescale(st, max_nan(st.m, sm));
+  };
+  fetch(w, 0);
+  uint64_t s2 = 0, t2 = 0;  // the sums of the even and the odd elements
+  for (int j0 = 0; j0 == 0 || j0 < n_vec; j0 += kThreads * U) {
+    if (j0 + kThreads * U < n_vec) fetch(ahead, j0 + kThreads * U);  // in flight while this step is computed
+    float sm = top_of<DT>(w);
+    if (j0 == 0) sm = max_nan(sm, xe);
+    {
+      // to the new maximum (as rescale(), for both halves of the sums)
+      const float m = max_nan(st.m, sm);
+      const float d = st.m == -INFINITY ? kFar : max_nan(st.m - shift_of(m), kFar);
+      const float f = exp2_approx(d * kLog2e);
+      t2 = mul2(pair(f, f), fma2(pair(d, d), s2, t2));
+      s2 = mul2(pair(f, f), s2);
+      st.m = m;
+    }
     const float shift = shift_of(st.m);
+    const uint64_t minus = pair(-shift, -shift), unit = pair(kLog2e, kLog2e);
 #pragma unroll
-    for (int e = 0; e < U * kVec; ++e) {
-      const float d = max_nan(x[e] - shift, kFar);
-      const float y = exp2_approx(d * kLog2e);
-      st.s += y;
-      st.t += d * y;
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int e = 0; e < kVec / 2; ++e) {
+        float d0, d1, a0, a1;
+        unpair(add2(two_of<DT>(w[u], e), minus), d0, d1);
+        const uint64_t d = pair(max_nan(d0, kFar), max_nan(d1, kFar));
+        unpair(mul2(d, unit), a0, a1);
+        const uint64_t y = pair(exp2_approx(a0), exp2_approx(a1));
+        s2 = add2(s2, y);
+        t2 = fma2(d, y, t2);
+      }
     }
     if (j0 == 0 && has_e) {
       const float d = max_nan(xe - shift, kFar);
       const float y = exp2_approx(d * kLog2e);
-      st.s += y;
-      st.t += d * y;
+      s2 = add2(s2, pair(y, 0.f));
+      t2 = add2(t2, pair(d * y, 0.f));
     }
     if (k > 0) {
       if (j0 == 0) {
@@ -207,40 +275,91 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Params p) {
           const int j = u * kThreads + tid;
           if (j < n_vec) {
 #pragma unroll
-            for (int e = kVec - 1; e >= 0; --e)
-              if (x[u * kVec + e] == sm) at = first + static_cast<uint32_t>(j) * kVec + e;
+            for (int e = kVec / 2 - 1; e >= 0; --e) {
+              float a, b;
+              unpair(two_of<DT>(w[u], e), a, b);
+              const uint32_t i = first + static_cast<uint32_t>(j) * kVec + 2 * e;
+              if (b == sm) at = i + 1;
+              if (a == sm) at = i;
+            }
           }
         }
         if (has_e && xe == sm && (tid < head || at >= 0x80000000u)) at = xe_i;
         uint64_t key = key_of(sm, at);
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, o));
-        if ((lane & 7) == 0) group_key[tid >> 3] = key;
+        for (int o = kGroupLanes / 2; o > 0; o >>= 1) key = max(key, __shfl_xor_sync(0xFFFFFFFFu, key, o));
+        if ((lane & (kGroupLanes - 1)) == 0) group_key[tid / kGroupLanes] = key;
         __syncthreads();
-        // warp w ranks groups 4 w .. 4 w + 3, eight lanes each
-        const uint64_t mine = group_key[warp * 4 + (lane >> 3)];
+        // four lanes rank one group
+        const uint64_t mine = group_key[tid / 4];
         int above = 0;
 #pragma unroll
-        for (int g = 0; g < kGroups / 8; ++g) above += group_key[(lane & 7) + 8 * g] > mine;
+        for (int g = 0; g < kGroups / 4; ++g) above += group_key[(lane & 3) + 4 * g] > mine;
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
-        if (above == k - 1 && (lane & 7) == 0) bound = mine;
+        for (int o = 2; o > 0; o >>= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
+        if (above == k - 1 && (lane & 3) == 0) bound = mine;
         __syncthreads();
         tau_v = value_of(bound);
         tau_i = index_of(bound);
         if (has_e) push(xe, xe_i);
       }
       if (!(sm < tau_v)) {
+        uint32_t hits = 0;  // bit u * kVec + e: elements that may be among the k largest
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int j = j0 + u * kThreads + tid;
-          if (j < n_vec) {
+          const uint4 one[1] = {w[u]};
+          if (j0 + u * kThreads + tid < n_vec && !(top_of<DT>(one) < tau_v)) {
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) push(x[u * kVec + e], first + static_cast<uint32_t>(j) * kVec + e);
+            for (int e = 0; e < kVec / 2; ++e) {
+              float a, b;
+              unpair(two_of<DT>(w[u], e), a, b);
+              if (!(a < tau_v)) hits |= 1u << (u * kVec + 2 * e);
+              if (!(b < tau_v)) hits |= 1u << (u * kVec + 2 * e + 1);
+            }
+          }
+        }
+#pragma unroll 1
+        while (hits) {  // (compact code, for one element in a thousand: the element is read again)
+          const int at = __ffs(hits) - 1;
+          hits &= hits - 1;
+          const uint32_t i = first + static_cast<uint32_t>(j0 + at / kVec * kThreads + tid) * kVec + at % kVec;
+          push(E::at(x_row, i), i);
+        }
+      }
+      // after 1, 2, 4, 8 .. steps: the k largest so far, in order, and their last as the bound
+      const int step = j0 / (kThreads * U) + 1;
+      if ((step & (step - 1)) == 0 && j0 + kThreads * U < n_vec) {
+        __syncthreads();
+        const unsigned int n = count;
+        if (n <= kThreads) {  // (more: leave it to the end)
+          const uint64_t mine = tid < n ? list[tid] : 0;
+          int above = kThreads;
+          if (tid < n) {
+            above = 0;
+#pragma unroll 4
+            for (unsigned int j = 0; j < n; ++j) above += list[j] > mine;
+          }
+          __syncthreads();
+          if (above < k) list[above] = mine;
+          if (tid == 0) count = min(n, static_cast<unsigned int>(k));
+          __syncthreads();
+          if (n >= static_cast<unsigned int>(k)) {
+            const uint64_t key = list[k - 1];
+            tau_v = value_of(key);
+            tau_i = index_of(key);
           }
         }
       }
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = ahead[u];
+  }
+  {
+    float a, b;
+    unpair(s2, a, b);
+    st.s = a + b;
+    unpair(t2, a, b);
+    st.t = a + b;
   }
 
   // join the statistics: lanes, warps (warp 0), then the CTAs of the row
@@ -314,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 2) logprobs_kernel(const Params p) {
       }
       uint64_t mine = 0;
       int above = kMaxTopK;
-      if (tid < p.csize * k) {
+      if (tid < p.csize * k) {  // (at most 8 * 32)
         mine = list[tid];
         above = 0;
         for (int j = 0; j < p.csize * k; ++j) above += list[j] > mine;
@@ -382,7 +501,7 @@ cudaError_t launch_token_logprobs(const LogprobArgs &a, const DeviceInfo &dev) {
   p.top_logprobs = a.top_logprobs;
   // few rows: up to eight CTAs (one cluster) share a row, while each keeps at least 4096 elements
   int c = 1;
-  while (c < 8 && a.rows * c * 2 <= 2 * dev.num_sms && a.vocab / (c * 2) >= 4096) c *= 2;
+  while (c < 8 && a.rows * c * 2 <= kCtas * dev.num_sms && a.vocab / (c * 2) >= 4096) c *= 2;
   p.csize = c;
   p.share = ((a.vocab + c - 1) / c + 63) / 64 * 64;
   if (a.dtype == W4A16_F32) return go<F32>(p, a.rows, a.stream);

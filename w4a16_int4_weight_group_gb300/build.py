@@ -21,7 +21,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libw4a16.so")
 
 SOURCES = ["api.cu", "pack.cu", "gemm_generic.cu", "gemm_decode.cu", "gemm_prefill.cu", "serve_api.cu", "kv_cache.cu",
-           "attention.cu", "attention_d64.cu", "attention_d128.cu", "attention_d256.cu",
+           "attention.cu", *(f"attention_d{d}_{b}bit.cu" for d in (64, 128, 256) for b in (4, 8)),
            "attention_tiles_d64.cu", "attention_tiles_d128.cu", "logprobs.cu"]
 # CPython argument marshalling for the prepared-layer call and the serving operators (optional: the binding uses ctypes when it
 # cannot be built, e.g. without the Python headers)

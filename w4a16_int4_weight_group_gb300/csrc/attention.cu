@@ -69,9 +69,12 @@ cudaError_t launch_tree_attention(const AttentionArgs &a, const DeviceInfo &dev)
     return a.cache.head_dim == 64 ? launch_tiles<64>(p, a.cache.bits, dev.num_sms, a.stream)
                                   : launch_tiles<128>(p, a.cache.bits, dev.num_sms, a.stream);
   const int rows = stream_rows(a.max_q * p.group, a.cache.head_dim);
-  if (a.cache.head_dim == 64) return launch_stream<64>(p, a.cache.bits, rows, dev.num_sms, a.stream);
-  if (a.cache.head_dim == 128) return launch_stream<128>(p, a.cache.bits, rows, dev.num_sms, a.stream);
-  return launch_stream<256>(p, a.cache.bits, rows, dev.num_sms, a.stream);
+  const bool wide = a.cache.bits == 8;
+  switch (a.cache.head_dim) {
+    case 64: return wide ? launch_stream<64, 8>(p, rows, dev.num_sms, a.stream) : launch_stream<64, 4>(p, rows, dev.num_sms, a.stream);
+    case 128: return wide ? launch_stream<128, 8>(p, rows, dev.num_sms, a.stream) : launch_stream<128, 4>(p, rows, dev.num_sms, a.stream);
+    default: return wide ? launch_stream<256, 8>(p, rows, dev.num_sms, a.stream) : launch_stream<256, 4>(p, rows, dev.num_sms, a.stream);
+  }
 }
 
 size_t tree_attention_workspace_bytes(int max_q, int q_heads, int kv_heads, int head_dim, int num_sms) {

@@ -47,8 +47,8 @@ inline bool use_tiles(int max_rows, int head_dim) { return max_rows > 32 && head
 
 template <int D>
 cudaError_t launch_tiles(const Params &p, int bits, int num_sms, cudaStream_t stream);  // head_dim 64 and 128
-template <int D>
-cudaError_t launch_stream(const Params &p, int bits, int rows, int num_sms, cudaStream_t stream);
+template <int D, int BITS>
+cudaError_t launch_stream(const Params &p, int rows, int num_sms, cudaStream_t stream);
 
 }  // namespace attention
 }  // namespace w4a16

@@ -12,9 +12,9 @@ namespace attention {
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;  // 2 s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 1.f;        // how far (powers of two) scores may exceed the running maximum
-constexpr float kProbExp = 14.f;     // probabilities are held times 2^14: at most 2^15 with the slack, under 65504
-constexpr float kProbUnit = 16384.f;
+constexpr float kSlack = 3.f;        // how far (powers of two) scores may exceed the running maximum
+constexpr float kProbExp = 12.f;     // probabilities are held times 2^12: at most 2^15 with the slack, under 65504
+constexpr float kProbUnit = 4096.f;
 constexpr float kSmall = 6.103515625e-05f;  // 2^-14, the smallest normal fp16 number
 constexpr float kPlane = 268435456.f;       // 2^28
 constexpr int kPlanes = 5;                  // 2^-14 - 4 * 28 = 2^-126

@@ -23,11 +23,11 @@
 //    subtraction of 1024 + z leaves u - z. So the products are of exact integers; the key's scale multiplies
 //    the fp32 score, the value's scale goes into the probability.
 //  * Ranges. A query row is scaled by a power of two to a largest element near 2^12. The probabilities times
-//    the values' scales are kept relative to a running power of two sref above every scale seen, times 2^14:
-//    fp16 holds them with 11 bits down to 2^-28 of the largest. A step that has smaller ones (a value's code
+//    the values' scales are kept relative to a running power of two sref above every scale seen, times 2^12:
+//    fp16 holds them with 11 bits down to 2^-26 of the largest. A step that has smaller ones (a value's code
 //    may be its zero point at every larger one) takes them in further products of 28 powers of two each, so
 //    that every probability counts with 11 bits over the range of fp32.
-//  * The running maximum is raised only when a score exceeds it by more than 1 (in powers of two), so most
+//  * The running maximum is raised only when a score exceeds it by more than 3 (in powers of two), so most
 //    steps need neither the reduction across lanes nor the rescaling of the sums.
 #pragma once
 
@@ -38,21 +38,22 @@
 namespace w4a16 {
 namespace attention {
 
-template <int D_, int BITS_, int NT_>
+template <int D_, int BITS_, int NT_, bool BF_>
 struct StreamLayout {
   static constexpr int D = D_, BITS = BITS_, NT = NT_;
+  static constexpr bool BF = BF_;
   static constexpr int R = 8 * NT;              // query rows of a row tile
   static constexpr int RB = D * BITS / 8;       // bytes of a token's codes
   static constexpr int kTile = 16 * (2 * RB + 8);
   static constexpr int TPS = kTile <= 2176 && NT < 4 ? 2 : 1;  // tiles of a warp's step
-  static constexpr int W = kTile > 4224 ? 4 : 8;     // warps
+  static constexpr int W = D == 256 ? 4 : 8;         // warps
   static constexpr int kThreads = 32 * W;
   static constexpr int kStage = TPS * kTile;
   static constexpr int kUnit = W * TPS * 16;    // tokens of a unit
-  static constexpr int MB = 4;                  // sums kept in shared memory when the warps join
+  static constexpr int MB = W / 2;              // sums kept in shared memory when the warps join
   static constexpr int kPad = D + 4;            // floats of a row of them
   static constexpr bool kQSmem = NT * D >= 256; // Q's operands stay in shared memory, not in registers
-  static constexpr int kCtas = NT * D >= 512 ? 1 : 2;  // on an SM
+  static constexpr int kCtas = NT * D >= 512 && D < 256 ? 1 : 2;  // on an SM
   static constexpr int kQBytes = R * D * 2;
   static constexpr int kFixed = kQBytes + MB * R * kPad * 4 + R * (8 + 4) + 2 * W * R * 4 + 512;
   static constexpr int kBudget = (kCtas == 2 ? 113 : 226) * 1024;
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
   uint32_t qreg[L::kQSmem ? 1 : KS * NT * 2];
   float o[KS][NT][4];
   float m[NT][2], l[NT][2], qs[NT][2];  // rows 8 nt + 2 r, + 1
-  float sref = 0.f;
+  float sref = 0.f, isref = 0.f;
 
   while (units > 0) {
     // ---------------------------------------------------------------- segment: (sequence, head, row tile)
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
     }
-    sref = 0.f;
+    sref = isref = 0.f;
 
     for (int u = 0; u < count; ++u) {
       const uint32_t v = (valid >> (TPS * stage)) & ((1u << TPS) - 1u);
@@ -289,10 +290,10 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
           const uint32_t pv0 = lds32(par + 64 + 4 * g), pv1 = lds32(par + 64 + 4 * g + 32);
           const bool there = (v >> j) & 1u;
           const bool in0 = whole || (there && t0 + 16 * j + g < seg.len), in1 = whole || (there && t0 + 16 * j + g + 8 < seg.len);
-          const float sk0 = in0 ? bits_to_float(pk0 & 0xFFFFu, p.bf16 != 0) : 0.f;
-          const float sk1 = in1 ? bits_to_float(pk1 & 0xFFFFu, p.bf16 != 0) : 0.f;
-          sv[j][0] = in0 ? bits_to_float(pv0 & 0xFFFFu, p.bf16 != 0) : 0.f;
-          sv[j][1] = in1 ? bits_to_float(pv1 & 0xFFFFu, p.bf16 != 0) : 0.f;
+          const float sk0 = in0 ? bits_to_float(pk0 & 0xFFFFu, L::BF) : 0.f;
+          const float sk1 = in1 ? bits_to_float(pk1 & 0xFFFFu, L::BF) : 0.f;
+          sv[j][0] = in0 ? bits_to_float(pv0 & 0xFFFFu, L::BF) : 0.f;
+          sv[j][1] = in1 ? bits_to_float(pv1 & 0xFFFFu, L::BF) : 0.f;
           const uint32_t z0 = pk0 >> 16, z1 = pk1 >> 16;
           const uint32_t lo0 = (0x6400u + z0) * 0x10001u, lo1 = (0x6400u + z1) * 0x10001u;
           constexpr int NA = NT == 1 ? 2 : 1;  // chains of products (one row group alone would wait for each product)
@@ -396,6 +397,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
             const float next = __uint_as_float(e << 23);
             ratio = sref / next;
             sref = next;
+            isref = 1.f / next;
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -413,8 +415,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
             }
         }
         // ---- probabilities, times the values' scales, as operands (rows, tokens)
-        const float isref = sref > 0.f ? 1.f / sref : 0.f;
-        bool small = false;
+        float least = INFINITY;  // the smallest of them that is not hidden
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float ms0 = kProbExp - (m[nt][0] == -INFINITY ? 0.f : m[nt][0]), ms1 = kProbExp - (m[nt][1] == -INFINITY ? 0.f : m[nt][1]);
@@ -426,15 +427,17 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
               e[c] = exp2_approx(fmaf(y[j][nt][c], qs[nt][c & 1], (c & 1) ? ms1 : ms0));
               y[j][nt][c] = e[c] * (sv[j][c >> 1] * isref);
             }
-            if (!whole) {
+            if (whole) {
+              least = fminf(fminf(least, fminf(y[j][nt][0], y[j][nt][1])), fminf(y[j][nt][2], y[j][nt][3]));
+            } else {
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 4; ++c) {
                 if (hidden & (1u << ((j * NT + nt) * 4 + c))) e[c] = y[j][nt][c] = 0.f;
+                else least = fminf(least, y[j][nt][c]);
+              }
             }
             l[nt][0] += e[0] + e[2];
             l[nt][1] += e[1] + e[3];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) small |= y[j][nt][c] < kSmall && y[j][nt][c] > 0.f;
           }
         }
         // ---- sums over the tokens: lane: elements g D / 8 .. of the values, tokens 2 r, 2 r + 1, 2 r + 8, 2 r + 9
@@ -492,7 +495,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
           }
         };
         uint32_t pb[TPS][NT][2];
-        if (!__any_sync(0xFFFFFFFFu, small)) {
+        if (!__any_sync(0xFFFFFFFFu, least < kSmall)) {
 #pragma unroll
           for (int j = 0; j < TPS; ++j)
 #pragma unroll
@@ -653,13 +656,20 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
   }
 }
 
-template <int D>
-cudaError_t launch_stream(const Params &p, int bits, int rows, int num_sms, cudaStream_t stream) {
-  if (rows == 8) return bits == 8 ? start_kernel<StreamLayout<D, 8, 1>>(stream_kernel<StreamLayout<D, 8, 1>>, num_sms * StreamLayout<D, 8, 1>::kCtas, p, stream) : start_kernel<StreamLayout<D, 4, 1>>(stream_kernel<StreamLayout<D, 4, 1>>, num_sms * StreamLayout<D, 4, 1>::kCtas, p, stream);
+template <class L>
+cudaError_t start_stream(const Params &p, int num_sms, cudaStream_t stream) {
+  return start_kernel<L>(stream_kernel<L>, num_sms * L::kCtas, p, stream);
+}
+
+template <int D, int BITS>
+cudaError_t launch_stream(const Params &p, int rows, int num_sms, cudaStream_t stream) {
+  if (rows == 8)
+    return p.bf16 ? start_stream<StreamLayout<D, BITS, 1, true>>(p, num_sms, stream) : start_stream<StreamLayout<D, BITS, 1, false>>(p, num_sms, stream);
   if constexpr (D != 256) {
-    if (rows == 32) return bits == 8 ? start_kernel<StreamLayout<D, 8, 4>>(stream_kernel<StreamLayout<D, 8, 4>>, num_sms * StreamLayout<D, 8, 4>::kCtas, p, stream) : start_kernel<StreamLayout<D, 4, 4>>(stream_kernel<StreamLayout<D, 4, 4>>, num_sms * StreamLayout<D, 4, 4>::kCtas, p, stream);
+    if (rows == 32)
+      return p.bf16 ? start_stream<StreamLayout<D, BITS, 4, true>>(p, num_sms, stream) : start_stream<StreamLayout<D, BITS, 4, false>>(p, num_sms, stream);
   }
-  return bits == 8 ? start_kernel<StreamLayout<D, 8, 2>>(stream_kernel<StreamLayout<D, 8, 2>>, num_sms * StreamLayout<D, 8, 2>::kCtas, p, stream) : start_kernel<StreamLayout<D, 4, 2>>(stream_kernel<StreamLayout<D, 4, 2>>, num_sms * StreamLayout<D, 4, 2>::kCtas, p, stream);
+  return p.bf16 ? start_stream<StreamLayout<D, BITS, 2, true>>(p, num_sms, stream) : start_stream<StreamLayout<D, BITS, 2, false>>(p, num_sms, stream);
 }
 
 }  // namespace attention

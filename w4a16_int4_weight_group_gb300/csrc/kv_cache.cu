@@ -17,7 +17,9 @@
 // parameters), so that the attention fetches a tile with one bulk copy.
 //
 // All three kernels are bound by memory: a lane handles 8 elements (16 bytes), so that the lanes of a
-// row are 8, 16 or 32 neighbours and its minimum and maximum are a few shuffles.
+// row are 8, 16 or 32 neighbours and its minimum and maximum are a few shuffles. A thread takes up to four heads of
+// one token: their loads are in flight together, and the token's cosines and sines (four times the bytes of a
+// 16-bit vector), its slot and its place in the cache are fetched once for them. With little work it takes one.
 #include "common.cuh"
 #include "internal.h"
 
@@ -25,6 +27,7 @@ namespace w4a16 {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kHeads = 4;  // heads whose loads a thread has in flight together
 constexpr float kSmallest = 1.17549435e-38f;  // smallest normal fp32 number
 
 template <class DT>
@@ -80,10 +83,10 @@ struct RopeParams {
   const int64_t *positions;
   const float *table;
   int64_t table_rows;
-  int64_t tokens;
+  uint32_t threads;  // tokens * head_groups * units
   int heads, head_dim, rot;
-  int units;        // pieces of a row that one thread each handles
-  int head_groups;  // threads that share a (token, unit): each takes every head_groups-th head
+  uint32_t units;        // pieces of a row that one thread each handles
+  uint32_t head_groups;  // threads that share a (token, unit): each takes every head_groups-th head
   bool copy_rest;   // out is not x: elements from rot on are copied
 };
 
@@ -94,105 +97,123 @@ template <class DT, int V, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t idx = blockIdx.x * int64_t(kThreads) + threadIdx.x;
-  const int64_t row = idx / p.units;
+  const uint32_t idx = blockIdx.x * kThreads + threadIdx.x;
+  if (idx >= p.threads) return;
+  const uint32_t row = idx / p.units;
   const int u = static_cast<int>(idx - row * p.units);
   const int64_t t = row / p.head_groups;
-  const int h0 = static_cast<int>(row - t * p.head_groups);
-  if (t >= p.tokens) return;
+  const int h0 = static_cast<int>(row - static_cast<uint32_t>(t) * p.head_groups);
+  const int step = static_cast<int>(p.head_groups);
   const int64_t pos = p.positions[t];
   const bool known = pos >= 0 && pos < p.table_rows;
   const float *row_c = p.table + (known ? pos : 0) * p.rot;
   const int half = p.rot / 2;
   const float nan = __int_as_float(0x7FFFFFFF);
+  const uint16_t *x_t = p.x + t * p.x_ts;
+  uint16_t *o_t = p.out + t * p.o_ts;
   if constexpr (V == 8) {
-    if constexpr (INTER) {
-      const bool turned = u * 8 < p.rot;
-      if (!turned && !p.copy_rest) return;
-      float c[4], s[4];
-      if (turned) {
+    const int pairs = half / 8;
+    const bool turned = INTER ? u * 8 < p.rot : u < pairs;
+    if (!turned && !p.copy_rest) return;
+    const int d = INTER || turned ? u * 8 : p.rot + (u - pairs) * 8;
+    float c[8], s[8];
+    if (turned) {
+      if constexpr (INTER) {
         const float4 a = __ldg(reinterpret_cast<const float4 *>(row_c + u * 4));
         const float4 b = __ldg(reinterpret_cast<const float4 *>(row_c + half + u * 4));
         c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
         s[0] = b.x; s[1] = b.y; s[2] = b.z; s[3] = b.w;
+      } else {
+        load8(row_c + u * 8, c);
+        load8(row_c + half + u * 8, s);
       }
-#pragma unroll 4
-      for (int h = h0; h < p.heads; h += p.head_groups) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p.x + t * p.x_ts + h * p.x_hs + u * 8);
-        uint4 r = w;
-        if (turned) {
+    }
+    for (int hb = h0; hb < p.heads; hb += kHeads * step) {
+      uint4 w[kHeads], w2[kHeads];  // all loads first: the stores might, as far as the compiler knows, touch them
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        const int h = hb + i * step;
+        if (h < p.heads) {
+          w[i] = *reinterpret_cast<const uint4 *>(x_t + h * p.x_hs + d);
+          if (!INTER && turned) w2[i] = *reinterpret_cast<const uint4 *>(x_t + h * p.x_hs + d + half);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        const int h = hb + i * step;
+        if (h >= p.heads) continue;
+        uint16_t *dst = o_t + h * p.o_hs + d;
+        if (!turned) {
+          *reinterpret_cast<uint4 *>(dst) = w[i];
+        } else if constexpr (INTER) {
           float x[8], y[8];
-          unpack8<DT>(w, x);
+          unpack8<DT>(w[i], x);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             y[2 * j] = known ? turn_first(x[2 * j], x[2 * j + 1], c[j], s[j]) : nan;
             y[2 * j + 1] = known ? turn_second(x[2 * j], x[2 * j + 1], c[j], s[j]) : nan;
           }
-          r = pack8<DT>(y);
-        }
-        *reinterpret_cast<uint4 *>(p.out + t * p.o_ts + h * p.o_hs + u * 8) = r;
-      }
-    } else {
-      const int pairs = half / 8;
-      if (u >= pairs) {  // a vector that is not turned
-        if (!p.copy_rest) return;
-        const int d = p.rot + (u - pairs) * 8;
-        for (int h = h0; h < p.heads; h += p.head_groups)
-          *reinterpret_cast<uint4 *>(p.out + t * p.o_ts + h * p.o_hs + d) =
-              *reinterpret_cast<const uint4 *>(p.x + t * p.x_ts + h * p.x_hs + d);
-        return;
-      }
-      float c[8], s[8];
-      load8(row_c + u * 8, c);
-      load8(row_c + half + u * 8, s);
-#pragma unroll 4
-      for (int h = h0; h < p.heads; h += p.head_groups) {
-        const uint16_t *src = p.x + t * p.x_ts + h * p.x_hs + u * 8;
-        float a[8], b[8], y1[8], y2[8];
-        unpack8<DT>(*reinterpret_cast<const uint4 *>(src), a);
-        unpack8<DT>(*reinterpret_cast<const uint4 *>(src + half), b);
+          *reinterpret_cast<uint4 *>(dst) = pack8<DT>(y);
+        } else {
+          float a[8], b[8], y1[8], y2[8];
+          unpack8<DT>(w[i], a);
+          unpack8<DT>(w2[i], b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          y1[j] = known ? turn_first(a[j], b[j], c[j], s[j]) : nan;
-          y2[j] = known ? turn_second(a[j], b[j], c[j], s[j]) : nan;
+          for (int j = 0; j < 8; ++j) {
+            y1[j] = known ? turn_first(a[j], b[j], c[j], s[j]) : nan;
+            y2[j] = known ? turn_second(a[j], b[j], c[j], s[j]) : nan;
+          }
+          *reinterpret_cast<uint4 *>(dst) = pack8<DT>(y1);
+          *reinterpret_cast<uint4 *>(dst + half) = pack8<DT>(y2);
         }
-        uint16_t *dst = p.out + t * p.o_ts + h * p.o_hs + u * 8;
-        *reinterpret_cast<uint4 *>(dst) = pack8<DT>(y1);
-        *reinterpret_cast<uint4 *>(dst + half) = pack8<DT>(y2);
       }
     }
   } else {
     if (u >= half) {
       if (!p.copy_rest) return;
       const int d = p.rot + (u - half);
-      for (int h = h0; h < p.heads; h += p.head_groups) p.out[t * p.o_ts + h * p.o_hs + d] = p.x[t * p.x_ts + h * p.x_hs + d];
+      for (int h = h0; h < p.heads; h += step) o_t[h * p.o_hs + d] = x_t[h * p.x_hs + d];
       return;
     }
     const int d1 = INTER ? 2 * u : u, d2 = INTER ? 2 * u + 1 : u + half;
     const float c = row_c[u], s = row_c[half + u];
-    for (int h = h0; h < p.heads; h += p.head_groups) {
-      const uint16_t *src = p.x + t * p.x_ts + h * p.x_hs;
+    for (int h = h0; h < p.heads; h += step) {
+      const uint16_t *src = x_t + h * p.x_hs;
       const float a = lo16<DT>(src[d1]), b = lo16<DT>(src[d2]);
-      uint16_t *dst = p.out + t * p.o_ts + h * p.o_hs;
+      uint16_t *dst = o_t + h * p.o_hs;
       dst[d1] = static_cast<uint16_t>(pack16<DT>(known ? turn_first(a, b, c, s) : nan, 0.f));
       dst[d2] = static_cast<uint16_t>(pack16<DT>(known ? turn_second(a, b, c, s) : nan, 0.f));
     }
   }
 }
 
+// A cache as the kernels see it.
+struct CacheView {
+  uint8_t *data;
+  int64_t slots_total, tile_bytes;
+  int kv_heads, page_tiles;
+  int page_shift;  // log2 of page_tiles, or -1
+};
+// Tile of cache head 0 that holds a slot (the tile of head h: h * page_tiles further), and the row in it.
+__device__ __forceinline__ int64_t tile_of(const CacheView &c, int64_t slot, int &row) {
+  const uint32_t tile = static_cast<uint32_t>(slot / kTileTokens);  // the cache holds fewer than 2^31 tiles
+  row = static_cast<int>(slot % kTileTokens);
+  const uint32_t page = c.page_shift >= 0 ? tile >> c.page_shift : tile / static_cast<uint32_t>(c.page_tiles);
+  return int64_t(page) * c.kv_heads * c.page_tiles + (tile - page * c.page_tiles);
+}
+
 struct WriteParams {
-  uint8_t *cache;
+  CacheView cache;
   const uint16_t *k, *v, *q;
   uint16_t *q_out;
   int64_t k_ts, k_hs, v_ts, v_hs, q_ts, q_hs;
   const int64_t *slots, *positions;
   const float *table;
-  int64_t table_rows, tokens, slots_total;
-  int q_heads, kv_heads, rot;
-  int page_tiles;
-  int64_t tile_bytes;
+  int64_t table_rows;
+  uint32_t groups;      // tokens * row_groups
+  uint32_t row_groups;  // groups of up to ROWS rows of a token: q heads, then k, then v
+  int q_heads, rot, bits;
   bool interleaved;
-  bool pair_vectors;  // rot / 2 is a multiple of 8 and the table's rows are 16-byte aligned
 };
 
 // Minimum or maximum that keeps a NaN.
@@ -207,184 +228,245 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// One lane's 8 elements x (d0 = 8 * chunk) turned; src points at the row (the pair's other half is read
-// from it again: it is in the first-level cache).
-template <class DT>
-__device__ __forceinline__ void turn8(const WriteParams &p, const uint16_t *src, int d0, int64_t t, float (&x)[8]) {
-  if (d0 >= p.rot) return;
+// How a row's elements turn: not at all; in the half layout with whole vectors (rot / 2 a multiple of 8); interleaved
+// (rot a multiple of 8); any other layout, element by element.
+enum Mode { kNone, kHalf, kInterleaved, kElements };
+
+// The cosines and sines of a lane's 8 elements (d0 = 8 * lane) at its token's position, so that an element x with its
+// pair's other element o becomes x c + o s (the sign of the pair's first element is in s).
+struct Turn {
+  float c[8], s[8];
+};
+template <int MODE>
+__device__ __forceinline__ void load_turn(const WriteParams &p, int64_t t, int d0, Turn &w) {
   const int64_t pos = p.positions[t];
   const bool known = pos >= 0 && pos < p.table_rows;
   const float *row = p.table + (known ? pos : 0) * p.rot;
   const int half = p.rot / 2;
-  float y[8];
-  if (p.pair_vectors && !p.interleaved) {
+  if constexpr (MODE == kHalf) {
     const bool first = d0 < half;
     const int i0 = first ? d0 : d0 - half;
-    float o[8], c[8], s[8];
-    unpack8<DT>(*reinterpret_cast<const uint4 *>(src + (first ? d0 + half : d0 - half)), o);
-    load8(row + i0, c);
-    load8(row + half + i0, s);
+    load8(row + i0, w.c);
+    load8(row + half + i0, w.s);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = first ? turn_first(x[j], o[j], c[j], s[j]) : turn_second(o[j], x[j], c[j], s[j]);
+    for (int j = 0; j < 8; ++j) w.s[j] = first ? -w.s[j] : w.s[j];
+  } else if constexpr (MODE == kInterleaved) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(row + d0 / 2));
+    const float4 b = __ldg(reinterpret_cast<const float4 *>(row + half + d0 / 2));
+    const float c[4] = {a.x, a.y, a.z, a.w}, s[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w.c[j] = c[j / 2];
+      w.s[j] = j & 1 ? s[j / 2] : -s[j / 2];
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int d = d0 + j;
-      const bool first = p.interleaved ? (d & 1) == 0 : d < half;
+      const bool in = d < p.rot, first = p.interleaved ? (d & 1) == 0 : d < half;
       const int i = p.interleaved ? d >> 1 : (first ? d : d - half);
-      const bool in = d < p.rot;
-      const int od = p.interleaved ? d ^ 1 : (first ? d + half : d - half);
-      const float o = in ? lo16<DT>(src[od]) : 0.f;
-      const float c = in ? __ldg(row + i) : 0.f, s = in ? __ldg(row + half + i) : 0.f;
-      y[j] = !in ? x[j] : (first ? turn_first(x[j], o, c, s) : turn_second(o, x[j], c, s));
+      w.c[j] = in ? __ldg(row + i) : 1.f;
+      w.s[j] = in ? (first ? -__ldg(row + half + i) : __ldg(row + half + i)) : 0.f;
     }
   }
-  const float nan = __int_as_float(0x7FFFFFFF);
+  if (!known) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = (known || d0 + j >= p.rot) ? y[j] : nan;
+    for (int j = 0; j < 8; ++j)
+      if (MODE != kElements || d0 + j < p.rot) w.c[j] = __int_as_float(0x7FFFFFFF);
+  }
+}
+// x: the lane's elements of the row at src; other: their pairs' other elements (kHalf).
+template <class DT, int MODE>
+__device__ __forceinline__ void turn8(const WriteParams &p, const uint16_t *src, int d0, const Turn &w, const uint4 &other, float (&x)[8]) {
+  float o[8];
+  if constexpr (MODE == kHalf) {
+    unpack8<DT>(other, o);
+  } else if constexpr (MODE == kInterleaved) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = x[j ^ 1];
+  } else {
+    const int half = p.rot / 2;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int d = d0 + j;
+      o[j] = d < p.rot ? lo16<DT>(src[p.interleaved ? d ^ 1 : (d < half ? d + half : d - half)]) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float y = __fadd_rn(__fmul_rn(x[j], w.c[j]), __fmul_rn(o[j], w.s[j]));
+    if (MODE != kElements || d0 + j < p.rot) x[j] = y;
+  }
 }
 
-// A row (token, head of q, k or v) for each group of LANES = head_dim / 8 lanes.
-template <class DT, int LANES, int BITS, bool ROPE>
-__global__ void __launch_bounds__(kThreads) kv_write_kernel(const WriteParams p) {
+// Up to ROWS consecutive rows (q heads, k heads, v heads) of a token for each group of LANES = head_dim / 8 lanes.
+template <class DT, int LANES, int MODE, int ROWS>
+__global__ void __launch_bounds__(kThreads, 3) kv_write_kernel(const WriteParams p) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int D = LANES * 8;
-  const int64_t idx = (blockIdx.x * int64_t(kThreads) + threadIdx.x) / LANES;
-  const int lane = threadIdx.x % LANES;
-  const int rows = p.q_heads + 2 * p.kv_heads;
-  const int64_t t = idx / rows;
-  const int r = static_cast<int>(idx - t * rows);
-  if (t >= p.tokens) return;
+  const uint32_t idx = (blockIdx.x * kThreads + threadIdx.x) / LANES;
+  const int lane = threadIdx.x % LANES, d0 = lane * 8;
+  if (idx >= p.groups) return;  // the whole group leaves together
+  const uint32_t t = idx / p.row_groups;
+  const int r0 = static_cast<int>(idx - t * p.row_groups) * ROWS;
+  const int kv = p.cache.kv_heads, turned = p.q_heads + kv, rows = turned + kv;
   const uint32_t mask = LANES == 32 ? 0xFFFFFFFFu : ((1u << (LANES & 31)) - 1u) << ((threadIdx.x & 31) / LANES * LANES);
-  const bool is_q = r < p.q_heads;
-  const int kind = is_q ? 0 : (r - p.q_heads) / p.kv_heads;  // of the cached rows: 0 keys, 1 values
-  const int h = is_q ? r : r - p.q_heads - kind * p.kv_heads;
-  const uint16_t *src = is_q ? p.q + t * p.q_ts + h * p.q_hs
-                             : (kind == 0 ? p.k + t * p.k_ts + h * p.k_hs : p.v + t * p.v_ts + h * p.v_hs);
-  const uint4 w = *reinterpret_cast<const uint4 *>(src + lane * 8);
-  float x[8];
-  unpack8<DT>(w, x);
-  if constexpr (ROPE) {
-    if (is_q || kind == 0) turn8<DT>(p, src, lane * 8, t, x);
-  }
-  if (is_q) {
-    *reinterpret_cast<uint4 *>(p.q_out + (t * p.q_heads + h) * D + lane * 8) = pack8<DT>(x);
-    return;
-  }
-  const int64_t slot = p.slots[t];
-  if (slot < 0 || slot >= p.slots_total) return;  // the whole group leaves together
-  if constexpr (ROPE) {
-    const uint4 y = pack8<DT>(x);  // the key as a dtype tensor would hold it
-    unpack8<DT>(y, x);
-  }
-  float lo = x[0], hi = x[0];
+  const bool some_turn = MODE != kNone && d0 < p.rot && r0 < turned;
+  const int half = p.rot / 2;
+  uint4 w[ROWS], other[MODE == kHalf ? ROWS : 1];
+  auto source = [&](int r) {
+    return r < p.q_heads ? p.q + t * p.q_ts + r * p.q_hs
+                         : r < turned ? p.k + t * p.k_ts + (r - p.q_heads) * p.k_hs : p.v + t * p.v_ts + (r - turned) * p.v_hs;
+  };
 #pragma unroll
-  for (int j = 1; j < 8; ++j) {
-    lo = min_nan(lo, x[j]);
-    hi = max_nan(hi, x[j]);
+  for (int i = 0; i < ROWS; ++i) {
+    const int r = r0 + i;
+    if (r >= rows) break;
+    const uint16_t *src = source(r);
+    w[i] = *reinterpret_cast<const uint4 *>(src + d0);
+    if (MODE == kHalf && some_turn && r < turned) other[i] = *reinterpret_cast<const uint4 *>(src + (d0 < half ? d0 + half : d0 - half));
   }
+  Turn turn;
+  if (some_turn) load_turn<MODE>(p, t, d0, turn);
+  const int64_t slot = r0 + ROWS > p.q_heads ? p.slots[t] : -1;
+  const bool stored = slot >= 0 && slot < p.cache.slots_total;
+  int row = 0;
+  const int64_t tile0 = stored ? tile_of(p.cache, slot, row) : 0;
+  const float top = p.bits == 8 ? 255.f : 15.f, inv_top = p.bits == 8 ? 1.f / 255.f : 1.f / 15.f;
+  const int row_bytes = D * p.bits / 8;  // of its codes
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(mask, lo, o));
-    hi = max_nan(hi, __shfl_xor_sync(mask, hi, o));
-  }
-  constexpr float top = BITS == 8 ? 255.f : 15.f;
-  constexpr float inv_top = 1.f / top;
-  const bool finite = fabsf(lo) <= 3.402823466e38f && fabsf(hi) <= 3.402823466e38f;
-  lo = fminf(lo, 0.f);
-  hi = fmaxf(hi, 0.f);
-  const uint16_t sbits = static_cast<uint16_t>(pack16<DT>(__fsub_rn(__fmul_rn(hi, inv_top), __fmul_rn(lo, inv_top)), 0.f));
-  float s = lo16<DT>(sbits);
-  if (s < kSmallest) s = 0.f;
-  const float inv = (finite && s > 0.f) ? __frcp_rn(s) : 0.f;
-  const float z = finite ? fminf(fmaxf(rintf(__fmul_rn(-lo, inv)), 0.f), top) : 0.f;
-  uint32_t u[8];
+  for (int i = 0; i < ROWS; ++i) {
+    const int r = r0 + i;
+    if (r >= rows) break;
+    float x[8];
+    unpack8<DT>(w[i], x);
+    if (some_turn && r < turned) turn8<DT, MODE>(p, MODE == kElements ? source(r) : nullptr, d0, turn, other[MODE == kHalf ? i : 0], x);
+    if (r < p.q_heads) {
+      *reinterpret_cast<uint4 *>(p.q_out + (int64_t(t) * p.q_heads + r) * D + d0) = pack8<DT>(x);
+      continue;
+    }
+    if (!stored) continue;
+    if constexpr (MODE != kNone) {
+      const uint4 y = pack8<DT>(x);  // the key as a dtype tensor would hold it
+      unpack8<DT>(y, x);
+    }
+    const int kind = r < turned ? 0 : 1;  // keys, values
+    const int h = r - p.q_heads - kind * kv;
+    float lo = x[0], hi = x[0];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float v = finite ? __fmul_rn(x[j], inv) : 0.f;
-    u[j] = static_cast<uint32_t>(fminf(fmaxf(__fadd_rn(rintf(v), z), 0.f), top));
-  }
-  const int64_t tile = slot / kTileTokens;
-  const int row = static_cast<int>(slot % kTileTokens);
-  const int64_t page = tile / p.page_tiles;
-  uint8_t *dst = p.cache + ((page * p.kv_heads + h) * p.page_tiles + (tile - page * p.page_tiles)) * p.tile_bytes;
-  constexpr int RB = D * BITS / 8;  // bytes of a row's codes
-  uint8_t *codes = dst + kind * (kTileTokens * RB) + row * RB;
-  if constexpr (BITS == 8) {
-    const uint32_t a = u[0] | (u[1] << 8) | (u[2] << 16) | (u[3] << 24);
-    const uint32_t b = u[4] | (u[5] << 8) | (u[6] << 16) | (u[7] << 24);
-    *reinterpret_cast<uint2 *>(codes + lane * 8) = make_uint2(a, b);
-  } else {
-    uint32_t a = 0;
+    for (int j = 1; j < 8; ++j) {
+      lo = min_nan(lo, x[j]);
+      hi = max_nan(hi, x[j]);
+    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) a |= u[j] << (4 * j);
-    *reinterpret_cast<uint32_t *>(codes + lane * 4) = a;
-  }
-  if (lane == 0) {
-    const uint32_t bits16 = finite ? static_cast<uint16_t>(pack16<DT>(s, 0.f)) : 0x7FFFu;
-    *reinterpret_cast<uint32_t *>(dst + 2 * kTileTokens * RB + kind * 64 + row * 4) = bits16 | (static_cast<uint32_t>(z) << 16);
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+      lo = min_nan(lo, __shfl_xor_sync(mask, lo, o));
+      hi = max_nan(hi, __shfl_xor_sync(mask, hi, o));
+    }
+    const bool finite = fabsf(lo) <= 3.402823466e38f && fabsf(hi) <= 3.402823466e38f;
+    lo = fminf(lo, 0.f);
+    hi = fmaxf(hi, 0.f);
+    const uint16_t sbits = static_cast<uint16_t>(pack16<DT>(__fsub_rn(__fmul_rn(hi, inv_top), __fmul_rn(lo, inv_top)), 0.f));
+    float s = lo16<DT>(sbits);
+    if (s < kSmallest) s = 0.f;
+    const float inv = (finite && s > 0.f) ? __frcp_rn(s) : 0.f;
+    const float z = finite ? fminf(fmaxf(rintf(__fmul_rn(-lo, inv)), 0.f), top) : 0.f;
+    uint32_t u[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v = finite ? __fmul_rn(x[j], inv) : 0.f;
+      u[j] = static_cast<uint32_t>(fminf(fmaxf(__fadd_rn(rintf(v), z), 0.f), top));
+    }
+    uint8_t *dst = p.cache.data + (tile0 + int64_t(h) * p.cache.page_tiles) * p.cache.tile_bytes;
+    uint8_t *codes = dst + (kind * kTileTokens + row) * row_bytes;
+    if (p.bits == 8) {
+      const uint32_t a = u[0] | (u[1] << 8) | (u[2] << 16) | (u[3] << 24);
+      const uint32_t b = u[4] | (u[5] << 8) | (u[6] << 16) | (u[7] << 24);
+      *reinterpret_cast<uint2 *>(codes + lane * 8) = make_uint2(a, b);
+    } else {
+      uint32_t a = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a |= u[j] << (4 * j);
+      *reinterpret_cast<uint32_t *>(codes + lane * 4) = a;
+    }
+    if (lane == 0) {
+      const uint32_t bits16 = finite ? static_cast<uint16_t>(pack16<DT>(s, 0.f)) : 0x7FFFu;
+      *reinterpret_cast<uint32_t *>(dst + 2 * kTileTokens * row_bytes + kind * 64 + row * 4) = bits16 | (static_cast<uint32_t>(z) << 16);
+    }
   }
 }
 
 struct ReadParams {
-  const uint8_t *cache;
+  CacheView cache;
   const int64_t *slots;
   uint16_t *k_out, *v_out;
-  int64_t tokens, slots_total;
-  int kv_heads, page_tiles;
-  int64_t tile_bytes;
+  uint32_t groups;       // tokens * head_groups
+  uint32_t head_groups;  // groups of up to HEADS consecutive heads
 };
 
+// Eight values from their codes (4 bits: in w.x).
 template <class DT, int BITS>
-__device__ __forceinline__ uint4 decode8(const uint8_t *codes, int lane, uint32_t param) {
+__device__ __forceinline__ uint4 decode8(uint2 w, uint32_t param) {
   const float s = lo16<DT>(param & 0xFFFFu);
   const int z = static_cast<int>(param >> 16);
   float x[8];
-  if constexpr (BITS == 8) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(codes + lane * 8);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(static_cast<int>(((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 0xFFu) - z) * s;
-  } else {
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + lane * 4);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(static_cast<int>((w >> (4 * j)) & 0xFu) - z) * s;
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t u = BITS == 8 ? ((j < 4 ? w.x : w.y) >> (8 * (j & 3))) & 0xFFu : (w.x >> (4 * j)) & 0xFu;
+    x[j] = static_cast<float>(static_cast<int>(u) - z) * s;
   }
   return pack8<DT>(x);
 }
+template <int BITS>
+__device__ __forceinline__ uint2 load_codes(const uint8_t *codes, int lane) {
+  if constexpr (BITS == 8) return __ldg(reinterpret_cast<const uint2 *>(codes) + lane);
+  else return make_uint2(__ldg(reinterpret_cast<const uint32_t *>(codes) + lane), 0u);
+}
 
-// A (token, head) for each group of LANES lanes: its key and its value.
-template <class DT, int LANES, int BITS>
+// The keys and values of up to HEADS consecutive heads of a token for each group of LANES lanes.
+template <class DT, int LANES, int BITS, int HEADS>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const ReadParams p) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int D = LANES * 8, RB = D * BITS / 8;
-  const int64_t idx = (blockIdx.x * int64_t(kThreads) + threadIdx.x) / LANES;
+  const uint32_t idx = (blockIdx.x * kThreads + threadIdx.x) / LANES;
   const int lane = threadIdx.x % LANES;
-  const int64_t t = idx / p.kv_heads;
-  const int h = static_cast<int>(idx - t * p.kv_heads);
-  if (t >= p.tokens) return;
+  if (idx >= p.groups) return;
+  const uint32_t t = idx / p.head_groups;
+  const int h0 = static_cast<int>(idx - t * p.head_groups) * HEADS;
   const int64_t slot = p.slots[t];
-  uint4 k = make_uint4(0, 0, 0, 0), v = k;
-  if (slot >= 0 && slot < p.slots_total) {
-    const int64_t tile = slot / kTileTokens;
-    const int row = static_cast<int>(slot % kTileTokens);
-    const int64_t page = tile / p.page_tiles;
-    const uint8_t *src = p.cache + ((page * p.kv_heads + h) * p.page_tiles + (tile - page * p.page_tiles)) * p.tile_bytes;
-    const uint8_t *par = src + 2 * kTileTokens * RB + row * 4;
-    k = decode8<DT, BITS>(src + row * RB, lane, *reinterpret_cast<const uint32_t *>(par));
-    v = decode8<DT, BITS>(src + kTileTokens * RB + row * RB, lane, *reinterpret_cast<const uint32_t *>(par + 64));
+  uint2 k[HEADS], v[HEADS];
+  uint32_t pk[HEADS], pv[HEADS];
+  const bool stored = slot >= 0 && slot < p.cache.slots_total;
+  int row = 0;
+  const int64_t tile0 = stored ? tile_of(p.cache, slot, row) : 0;
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) {
+    k[i] = v[i] = make_uint2(0, 0);
+    pk[i] = pv[i] = 0;
+    if (stored && h0 + i < p.cache.kv_heads) {
+      const uint8_t *src = p.cache.data + (tile0 + int64_t(h0 + i) * p.cache.page_tiles) * p.cache.tile_bytes;
+      const uint32_t *par = reinterpret_cast<const uint32_t *>(src + 2 * kTileTokens * RB) + row;
+      k[i] = load_codes<BITS>(src + row * RB, lane);
+      v[i] = load_codes<BITS>(src + (kTileTokens + row) * RB, lane);
+      pk[i] = __ldg(par);
+      pv[i] = __ldg(par + kTileTokens);
+    }
   }
-  const int64_t at = (t * p.kv_heads + h) * D + lane * 8;
-  *reinterpret_cast<uint4 *>(p.k_out + at) = k;
-  *reinterpret_cast<uint4 *>(p.v_out + at) = v;
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) {
+    if (h0 + i >= p.cache.kv_heads) break;
+    const int64_t at = (int64_t(t) * p.cache.kv_heads + h0 + i) * D + lane * 8;
+    *reinterpret_cast<uint4 *>(p.k_out + at) = decode8<DT, BITS>(k[i], pk[i]);
+    *reinterpret_cast<uint4 *>(p.v_out + at) = decode8<DT, BITS>(v[i], pv[i]);
+  }
 }
 
 // Launch with programmatic stream serialisation (the kernels wait for their predecessor themselves).
 template <class P>
 cudaError_t launch(void (*fn)(P), int64_t threads, const P &p, cudaStream_t stream) {
   const int64_t blocks = (threads + kThreads - 1) / kThreads;
-  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -401,34 +483,87 @@ cudaError_t launch(void (*fn)(P), int64_t threads, const P &p, cudaStream_t stre
 
 bool vec_ok(const HeadsView &x) { return aligned(x.ptr, 16) && x.token_stride % 8 == 0 && x.head_stride % 8 == 0; }
 
-template <class DT>
-cudaError_t rope_for(RopeParams &p, bool vec, bool inter, cudaStream_t stream) {
-  p.units = vec ? (inter ? p.head_dim / 8 : p.rot / 16 + (p.head_dim - p.rot) / 8) : p.rot / 2 + (p.head_dim - p.rot);
-  // four heads a thread (the table's row is read once for them), fewer when there is little work
-  const int64_t full = int64_t(p.tokens) * p.units * p.heads;
-  p.head_groups = full < 148 * 2048 ? p.heads : (p.heads + 3) / 4;
-  const int64_t threads = p.tokens * p.head_groups * p.units;
-  if (vec) return launch(inter ? rope_kernel<DT, 8, true> : rope_kernel<DT, 8, false>, threads, p, stream);
-  return launch(inter ? rope_kernel<DT, 1, true> : rope_kernel<DT, 1, false>, threads, p, stream);
+// Threads of one launch (32-bit indices): calls with more run as several launches over their tokens.
+constexpr int64_t kMaxThreads = int64_t(1) << 31;
+// Threads that fill the GPU: below it a thread takes one head.
+constexpr int64_t kFill = 148 * 2048;
+
+CacheView view_of(const w4a16_kv_cache_t &c) {
+  CacheView v{static_cast<uint8_t *>(c.data), c.num_pages * c.page_size, kv_tile_bytes(c.head_dim, c.bits), c.kv_heads,
+              c.page_size / kTileTokens, -1};
+  for (int i = 0; i < 20; ++i)
+    if (v.page_tiles == 1 << i) v.page_shift = i;
+  return v;
 }
 
+template <class DT>
+cudaError_t rope_for(const RopeParams &p, bool vec, bool inter, cudaStream_t stream) {
+  if (vec) return launch(inter ? rope_kernel<DT, 8, true> : rope_kernel<DT, 8, false>, p.threads, p, stream);
+  return launch(inter ? rope_kernel<DT, 1, true> : rope_kernel<DT, 1, false>, p.threads, p, stream);
+}
+
+// Work items of a token in groups of up to `most` (1 when all of them one by one do not fill the GPU).
+int items_a_group(int64_t tokens, int items, int lanes, int most) { return tokens * items * lanes < kFill ? 1 : most; }
+
+template <class DT, int LANES, int ROWS>
+cudaError_t write_rows(const WriteParams &p, int mode, cudaStream_t stream) {
+  const int64_t threads = int64_t(p.groups) * LANES;
+  switch (mode) {
+    case kNone: return launch(kv_write_kernel<DT, LANES, kNone, ROWS>, threads, p, stream);
+    case kHalf: return launch(kv_write_kernel<DT, LANES, kHalf, ROWS>, threads, p, stream);
+    case kInterleaved: return launch(kv_write_kernel<DT, LANES, kInterleaved, ROWS>, threads, p, stream);
+    default: return launch(kv_write_kernel<DT, LANES, kElements, ROWS>, threads, p, stream);
+  }
+}
+template <class DT, int LANES>
+cudaError_t write_for(WriteParams p, int64_t tokens, int mode, cudaStream_t stream) {
+  const int rows = p.q_heads + 2 * p.cache.kv_heads;
+  const int each = items_a_group(tokens, rows, LANES, kHeads);
+  p.row_groups = static_cast<uint32_t>((rows + each - 1) / each);
+  const int64_t most = kMaxThreads / (int64_t(p.row_groups) * LANES) - 1;
+  for (int64_t done = 0; done < tokens; done += most) {
+    const int64_t n = tokens - done < most ? tokens - done : most;
+    WriteParams c = p;
+    c.groups = static_cast<uint32_t>(n * p.row_groups);
+    c.k += done * p.k_ts;
+    c.v += done * p.v_ts;
+    if (c.q) c.q += done * p.q_ts, c.q_out += done * p.q_heads * (LANES * 8);
+    c.slots += done;
+    if (c.positions) c.positions += done;
+    const cudaError_t e = each == 1 ? write_rows<DT, LANES, 1>(c, mode, stream) : write_rows<DT, LANES, kHeads>(c, mode, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+template <class DT>
+cudaError_t write_for(const WriteParams &p, int64_t tokens, int head_dim, int mode, cudaStream_t stream) {
+  if (head_dim == 64) return write_for<DT, 8>(p, tokens, mode, stream);
+  if (head_dim == 128) return write_for<DT, 16>(p, tokens, mode, stream);
+  return write_for<DT, 32>(p, tokens, mode, stream);
+}
 template <class DT, int LANES, int BITS>
-cudaError_t write_for(const WriteParams &p, bool rope, cudaStream_t stream) {
-  const int64_t threads = p.tokens * (p.q_heads + 2 * p.kv_heads) * LANES;
-  return launch(rope ? kv_write_kernel<DT, LANES, BITS, true> : kv_write_kernel<DT, LANES, BITS, false>, threads, p, stream);
+cudaError_t read_for(ReadParams p, int64_t tokens, cudaStream_t stream) {
+  const int each = items_a_group(tokens, p.cache.kv_heads, LANES, kHeads);
+  p.head_groups = static_cast<uint32_t>((p.cache.kv_heads + each - 1) / each);
+  const int64_t most = kMaxThreads / (int64_t(p.head_groups) * LANES) - 1;
+  for (int64_t done = 0; done < tokens; done += most) {
+    const int64_t n = tokens - done < most ? tokens - done : most;
+    ReadParams c = p;
+    c.groups = static_cast<uint32_t>(n * p.head_groups);
+    c.slots += done;
+    c.k_out += done * p.cache.kv_heads * (LANES * 8);
+    c.v_out += done * p.cache.kv_heads * (LANES * 8);
+    const int64_t threads = int64_t(c.groups) * LANES;
+    const cudaError_t e = launch(each == 1 ? kv_read_kernel<DT, LANES, BITS, 1> : kv_read_kernel<DT, LANES, BITS, kHeads>, threads, c, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 template <class DT, int BITS>
-cudaError_t write_for(const WriteParams &p, int head_dim, bool rope, cudaStream_t stream) {
-  if (head_dim == 64) return write_for<DT, 8, BITS>(p, rope, stream);
-  if (head_dim == 128) return write_for<DT, 16, BITS>(p, rope, stream);
-  return write_for<DT, 32, BITS>(p, rope, stream);
-}
-template <class DT, int BITS>
-cudaError_t read_for(const ReadParams &p, int head_dim, cudaStream_t stream) {
-  const int64_t threads = p.tokens * p.kv_heads * (head_dim / 8);
-  if (head_dim == 64) return launch(kv_read_kernel<DT, 8, BITS>, threads, p, stream);
-  if (head_dim == 128) return launch(kv_read_kernel<DT, 16, BITS>, threads, p, stream);
-  return launch(kv_read_kernel<DT, 32, BITS>, threads, p, stream);
+cudaError_t read_for(const ReadParams &p, int64_t tokens, int head_dim, cudaStream_t stream) {
+  if (head_dim == 64) return read_for<DT, 8, BITS>(p, tokens, stream);
+  if (head_dim == 128) return read_for<DT, 16, BITS>(p, tokens, stream);
+  return read_for<DT, 32, BITS>(p, tokens, stream);
 }
 
 }  // namespace
@@ -436,31 +571,39 @@ cudaError_t read_for(const ReadParams &p, int head_dim, cudaStream_t stream) {
 cudaError_t launch_rope(const HeadsView &x, const HeadsView &out, int64_t tokens, int heads, int head_dim, int dtype,
                         const RopeArgs &rope, cudaStream_t stream) {
   RopeParams p{};
-  p.x = static_cast<const uint16_t *>(x.ptr);
-  p.out = static_cast<uint16_t *>(const_cast<void *>(out.ptr));
   p.x_ts = x.token_stride;
   p.x_hs = x.head_stride;
   p.o_ts = out.token_stride;
   p.o_hs = out.head_stride;
-  p.positions = rope.positions;
   p.table = rope.table;
   p.table_rows = rope.table_rows;
-  p.tokens = tokens;
   p.heads = heads;
   p.head_dim = head_dim;
   p.rot = rope.rot_dim;
   p.copy_rest = x.ptr != out.ptr;
-  const bool vec = vec_ok(x) && vec_ok(out) && head_dim % 8 == 0 && rope.rot_dim % (rope.interleaved ? 8 : 16) == 0 &&
-                   aligned(rope.table, 16);
-  return dtype == W4A16_BF16 ? rope_for<BF16>(p, vec, rope.interleaved, stream)
-                             : rope_for<F16>(p, vec, rope.interleaved, stream);
+  const bool inter = rope.interleaved;
+  const bool vec = vec_ok(x) && vec_ok(out) && head_dim % 8 == 0 && rope.rot_dim % (inter ? 8 : 16) == 0 && aligned(rope.table, 16);
+  p.units = static_cast<uint32_t>(vec ? (inter ? head_dim / 8 : p.rot / 16 + (head_dim - p.rot) / 8) : p.rot / 2 + (head_dim - p.rot));
+  const int each = items_a_group(tokens, heads, static_cast<int>(p.units), kHeads);
+  p.head_groups = static_cast<uint32_t>((heads + each - 1) / each);
+  const int64_t most = kMaxThreads / (int64_t(p.units) * p.head_groups) - 1;
+  for (int64_t done = 0; done < tokens; done += most) {
+    const int64_t n = tokens - done < most ? tokens - done : most;
+    p.x = static_cast<const uint16_t *>(x.ptr) + done * x.token_stride;
+    p.out = static_cast<uint16_t *>(const_cast<void *>(out.ptr)) + done * out.token_stride;
+    p.positions = rope.positions + done;
+    p.threads = static_cast<uint32_t>(n * p.units * p.head_groups);
+    const cudaError_t e = dtype == W4A16_BF16 ? rope_for<BF16>(p, vec, inter, stream) : rope_for<F16>(p, vec, inter, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_kv_write(const w4a16_kv_cache_t &cache, const HeadsView &k, const HeadsView &v, const int64_t *slots,
                             int64_t tokens, int dtype, const RopeArgs &rope, const HeadsView &q, int q_heads, void *q_out,
                             cudaStream_t stream) {
   WriteParams p{};
-  p.cache = static_cast<uint8_t *>(cache.data);
+  p.cache = view_of(cache);
   p.k = static_cast<const uint16_t *>(k.ptr);
   p.v = static_cast<const uint16_t *>(v.ptr);
   p.q = static_cast<const uint16_t *>(q.ptr);
@@ -475,38 +618,34 @@ cudaError_t launch_kv_write(const w4a16_kv_cache_t &cache, const HeadsView &k, c
   p.positions = rope.positions;
   p.table = rope.table;
   p.table_rows = rope.table_rows;
-  p.tokens = tokens;
-  p.slots_total = cache.num_pages * cache.page_size;
   p.q_heads = q.ptr ? q_heads : 0;
-  p.kv_heads = cache.kv_heads;
   p.rot = rope.rot_dim;
-  p.page_tiles = cache.page_size / kTileTokens;
-  p.tile_bytes = kv_tile_bytes(cache.head_dim, cache.bits);
   p.interleaved = rope.interleaved;
-  p.pair_vectors = rope.rot_dim % 16 == 0 && aligned(rope.table, 16);
-  const bool turn = rope.positions != nullptr;
-  if (dtype == W4A16_BF16)
-    return cache.bits == 8 ? write_for<BF16, 8>(p, cache.head_dim, turn, stream)
-                           : write_for<BF16, 4>(p, cache.head_dim, turn, stream);
-  return cache.bits == 8 ? write_for<F16, 8>(p, cache.head_dim, turn, stream)
-                         : write_for<F16, 4>(p, cache.head_dim, turn, stream);
+  p.bits = cache.bits;
+  int mode = kNone;
+  if (rope.positions) {
+    mode = kElements;
+    if (aligned(rope.table, 16)) {
+      if (!rope.interleaved && rope.rot_dim % 16 == 0) mode = kHalf;
+      if (rope.interleaved && rope.rot_dim % 8 == 0) mode = kInterleaved;
+    }
+  }
+  return dtype == W4A16_BF16 ? write_for<BF16>(p, tokens, cache.head_dim, mode, stream)
+                             : write_for<F16>(p, tokens, cache.head_dim, mode, stream);
 }
 
 cudaError_t launch_kv_read(const w4a16_kv_cache_t &cache, const int64_t *slots, int64_t tokens, void *k_out, void *v_out,
                            int dtype, cudaStream_t stream) {
   ReadParams p{};
-  p.cache = static_cast<const uint8_t *>(cache.data);
+  p.cache = view_of(cache);
   p.slots = slots;
   p.k_out = static_cast<uint16_t *>(k_out);
   p.v_out = static_cast<uint16_t *>(v_out);
-  p.tokens = tokens;
-  p.slots_total = cache.num_pages * cache.page_size;
-  p.kv_heads = cache.kv_heads;
-  p.page_tiles = cache.page_size / kTileTokens;
-  p.tile_bytes = kv_tile_bytes(cache.head_dim, cache.bits);
   if (dtype == W4A16_BF16)
-    return cache.bits == 8 ? read_for<BF16, 8>(p, cache.head_dim, stream) : read_for<BF16, 4>(p, cache.head_dim, stream);
-  return cache.bits == 8 ? read_for<F16, 8>(p, cache.head_dim, stream) : read_for<F16, 4>(p, cache.head_dim, stream);
+    return cache.bits == 8 ? read_for<BF16, 8>(p, tokens, cache.head_dim, stream)
+                           : read_for<BF16, 4>(p, tokens, cache.head_dim, stream);
+  return cache.bits == 8 ? read_for<F16, 8>(p, tokens, cache.head_dim, stream)
+                         : read_for<F16, 4>(p, tokens, cache.head_dim, stream);
 }
 
 }  // namespace w4a16

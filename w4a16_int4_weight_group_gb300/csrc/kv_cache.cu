@@ -211,8 +211,8 @@ struct WriteParams {
   const float *table;
   int64_t table_rows;
   uint32_t groups;      // tokens * row_groups
-  uint32_t row_groups;  // groups of up to ROWS rows of a token: q heads, then k, then v
-  int q_heads, rot, bits;
+  uint32_t row_groups;  // groups of up to ROWS rows of a token: heads of q (q_groups of them), then of k and v
+  int q_groups, q_heads, rot, bits;
   bool interleaved;
 };
 
@@ -299,7 +299,8 @@ __device__ __forceinline__ void turn8(const WriteParams &p, const uint16_t *src,
   }
 }
 
-// Up to ROWS consecutive rows (q heads, k heads, v heads) of a token for each group of LANES = head_dim / 8 lanes.
+// Up to ROWS consecutive rows of a token for each group of LANES = head_dim / 8 lanes: heads of q, or of k and then
+// v. The rows' reductions go side by side (a row's alone would wait for each of its shuffles).
 template <class DT, int LANES, int MODE, int ROWS>
 __global__ void __launch_bounds__(kThreads, 3) kv_write_kernel(const WriteParams p) {
   griddep_wait();
@@ -309,76 +310,108 @@ __global__ void __launch_bounds__(kThreads, 3) kv_write_kernel(const WriteParams
   const int lane = threadIdx.x % LANES, d0 = lane * 8;
   if (idx >= p.groups) return;  // the whole group leaves together
   const uint32_t t = idx / p.row_groups;
-  const int r0 = static_cast<int>(idx - t * p.row_groups) * ROWS;
-  const int kv = p.cache.kv_heads, turned = p.q_heads + kv, rows = turned + kv;
+  const int g = static_cast<int>(idx - t * p.row_groups);
+  const int half = p.rot / 2, pair_at = d0 < half ? d0 + half : d0 - half;
+  if (MODE != kNone && g < p.q_groups) {
+    const int r0 = g * ROWS;
+    const uint16_t *src = p.q + t * p.q_ts + r0 * p.q_hs;
+    const bool turns = d0 < p.rot;
+    uint4 w[ROWS], other[MODE == kHalf ? ROWS : 1];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (r0 + i < p.q_heads) {
+        w[i] = *reinterpret_cast<const uint4 *>(src + i * p.q_hs + d0);
+        if (MODE == kHalf && turns) other[i] = *reinterpret_cast<const uint4 *>(src + i * p.q_hs + pair_at);
+      }
+    }
+    Turn turn;
+    if (turns) load_turn<MODE>(p, t, d0, turn);
+    uint16_t *dst = p.q_out + (int64_t(t) * p.q_heads + r0) * D + d0;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (r0 + i < p.q_heads) {
+        float x[8];
+        unpack8<DT>(w[i], x);
+        if (turns) turn8<DT, MODE>(p, src + i * p.q_hs, d0, turn, other[MODE == kHalf ? i : 0], x);
+        *reinterpret_cast<uint4 *>(dst + i * D) = pack8<DT>(x);
+      }
+    }
+    return;
+  }
+  const int kv = p.cache.kv_heads, r0 = (g - p.q_groups) * ROWS;
+  const int64_t slot = p.slots[t];
+  if (slot < 0 || slot >= p.cache.slots_total) return;
   const uint32_t mask = LANES == 32 ? 0xFFFFFFFFu : ((1u << (LANES & 31)) - 1u) << ((threadIdx.x & 31) / LANES * LANES);
-  const bool some_turn = MODE != kNone && d0 < p.rot && r0 < turned;
-  const int half = p.rot / 2;
+  const bool turns = MODE != kNone && d0 < p.rot && r0 < kv;
   uint4 w[ROWS], other[MODE == kHalf ? ROWS : 1];
-  auto source = [&](int r) {
-    return r < p.q_heads ? p.q + t * p.q_ts + r * p.q_hs
-                         : r < turned ? p.k + t * p.k_ts + (r - p.q_heads) * p.k_hs : p.v + t * p.v_ts + (r - turned) * p.v_hs;
-  };
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     const int r = r0 + i;
-    if (r >= rows) break;
-    const uint16_t *src = source(r);
-    w[i] = *reinterpret_cast<const uint4 *>(src + d0);
-    if (MODE == kHalf && some_turn && r < turned) other[i] = *reinterpret_cast<const uint4 *>(src + (d0 < half ? d0 + half : d0 - half));
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (r < 2 * kv) {
+      const uint16_t *src = r < kv ? p.k + t * p.k_ts + r * p.k_hs : p.v + t * p.v_ts + (r - kv) * p.v_hs;
+      w[i] = *reinterpret_cast<const uint4 *>(src + d0);
+      if (MODE == kHalf && turns && r < kv) other[i] = *reinterpret_cast<const uint4 *>(src + pair_at);
+    }
   }
-  Turn turn;
-  if (some_turn) load_turn<MODE>(p, t, d0, turn);
-  const int64_t slot = r0 + ROWS > p.q_heads ? p.slots[t] : -1;
-  const bool stored = slot >= 0 && slot < p.cache.slots_total;
+  if (turns) {
+    Turn turn;
+    load_turn<MODE>(p, t, d0, turn);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (r0 + i < kv) {
+        float x[8];
+        unpack8<DT>(w[i], x);
+        turn8<DT, MODE>(p, p.k + t * p.k_ts + (r0 + i) * p.k_hs, d0, turn, other[MODE == kHalf ? i : 0], x);
+        w[i] = pack8<DT>(x);  // the key as a dtype tensor would hold it
+      }
+    }
+  }
+  float lo[ROWS], hi[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    float x[8];
+    unpack8<DT>(w[i], x);
+    lo[i] = hi[i] = x[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) {
+      lo[i] = min_nan(lo[i], x[j]);
+      hi[i] = max_nan(hi[i], x[j]);
+    }
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      lo[i] = min_nan(lo[i], __shfl_xor_sync(mask, lo[i], o));
+      hi[i] = max_nan(hi[i], __shfl_xor_sync(mask, hi[i], o));
+    }
+  }
   int row = 0;
-  const int64_t tile0 = stored ? tile_of(p.cache, slot, row) : 0;
+  uint8_t *tile0 = p.cache.data + tile_of(p.cache, slot, row) * p.cache.tile_bytes;
   const float top = p.bits == 8 ? 255.f : 15.f, inv_top = p.bits == 8 ? 1.f / 255.f : 1.f / 15.f;
   const int row_bytes = D * p.bits / 8;  // of its codes
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     const int r = r0 + i;
-    if (r >= rows) break;
-    float x[8];
-    unpack8<DT>(w[i], x);
-    if (some_turn && r < turned) turn8<DT, MODE>(p, MODE == kElements ? source(r) : nullptr, d0, turn, other[MODE == kHalf ? i : 0], x);
-    if (r < p.q_heads) {
-      *reinterpret_cast<uint4 *>(p.q_out + (int64_t(t) * p.q_heads + r) * D + d0) = pack8<DT>(x);
-      continue;
-    }
-    if (!stored) continue;
-    if constexpr (MODE != kNone) {
-      const uint4 y = pack8<DT>(x);  // the key as a dtype tensor would hold it
-      unpack8<DT>(y, x);
-    }
-    const int kind = r < turned ? 0 : 1;  // keys, values
-    const int h = r - p.q_heads - kind * kv;
-    float lo = x[0], hi = x[0];
-#pragma unroll
-    for (int j = 1; j < 8; ++j) {
-      lo = min_nan(lo, x[j]);
-      hi = max_nan(hi, x[j]);
-    }
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) {
-      lo = min_nan(lo, __shfl_xor_sync(mask, lo, o));
-      hi = max_nan(hi, __shfl_xor_sync(mask, hi, o));
-    }
-    const bool finite = fabsf(lo) <= 3.402823466e38f && fabsf(hi) <= 3.402823466e38f;
-    lo = fminf(lo, 0.f);
-    hi = fmaxf(hi, 0.f);
-    const uint16_t sbits = static_cast<uint16_t>(pack16<DT>(__fsub_rn(__fmul_rn(hi, inv_top), __fmul_rn(lo, inv_top)), 0.f));
+    if (r >= 2 * kv) break;
+    const int kind = r < kv ? 0 : 1;  // keys, values
+    const bool finite = fabsf(lo[i]) <= 3.402823466e38f && fabsf(hi[i]) <= 3.402823466e38f;
+    const float low = fminf(lo[i], 0.f), high = fmaxf(hi[i], 0.f);
+    const uint16_t sbits = static_cast<uint16_t>(pack16<DT>(__fsub_rn(__fmul_rn(high, inv_top), __fmul_rn(low, inv_top)), 0.f));
     float s = lo16<DT>(sbits);
     if (s < kSmallest) s = 0.f;
     const float inv = (finite && s > 0.f) ? __frcp_rn(s) : 0.f;
-    const float z = finite ? fminf(fmaxf(rintf(__fmul_rn(-lo, inv)), 0.f), top) : 0.f;
+    const float z = finite ? fminf(fmaxf(rintf(__fmul_rn(-low, inv)), 0.f), top) : 0.f;
+    float x[8];
+    unpack8<DT>(w[i], x);
     uint32_t u[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float v = finite ? __fmul_rn(x[j], inv) : 0.f;
       u[j] = static_cast<uint32_t>(fminf(fmaxf(__fadd_rn(rintf(v), z), 0.f), top));
     }
-    uint8_t *dst = p.cache.data + (tile0 + int64_t(h) * p.cache.page_tiles) * p.cache.tile_bytes;
+    uint8_t *dst = tile0 + int64_t(r - kind * kv) * p.cache.page_tiles * p.cache.tile_bytes;
     uint8_t *codes = dst + (kind * kTileTokens + row) * row_bytes;
     if (p.bits == 8) {
       const uint32_t a = u[0] | (u[1] << 8) | (u[2] << 16) | (u[3] << 24);
@@ -519,7 +552,8 @@ template <class DT, int LANES>
 cudaError_t write_for(WriteParams p, int64_t tokens, int mode, cudaStream_t stream) {
   const int rows = p.q_heads + 2 * p.cache.kv_heads;
   const int each = items_a_group(tokens, rows, LANES, kHeads);
-  p.row_groups = static_cast<uint32_t>((rows + each - 1) / each);
+  p.q_groups = (p.q_heads + each - 1) / each;
+  p.row_groups = static_cast<uint32_t>(p.q_groups + (2 * p.cache.kv_heads + each - 1) / each);
   const int64_t most = kMaxThreads / (int64_t(p.row_groups) * LANES) - 1;
   for (int64_t done = 0; done < tokens; done += most) {
     const int64_t n = tokens - done < most ? tokens - done : most;

@@ -17,8 +17,8 @@
 // parameters), so that the attention fetches a tile with one bulk copy.
 //
 // All three kernels are bound by memory: a lane handles 8 elements (16 bytes), so that the lanes of a
-// row are 8, 16 or 32 neighbours and its minimum and maximum are a few shuffles. A thread takes up to four heads of
-// one token: their loads are in flight together, and the token's cosines and sines (four times the bytes of a
+// row are 8, 16 or 32 neighbours and its minimum and maximum are a few shuffles. A thread takes up to four heads (the
+// write: two) of one token: their loads are in flight together, and the token's cosines and sines (four times the bytes of a
 // 16-bit vector), its slot and its place in the cache are fetched once for them. With little work it takes one.
 #include "common.cuh"
 #include "internal.h"
@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kHeads = 4;  // heads whose loads a thread has in flight together
+constexpr int kRows = 2;   // rows of the cache write (6 CTAs of 40 registers an SM: 57 us for 8192 tokens; 4 rows at 64 registers: 59)
 constexpr float kSmallest = 1.17549435e-38f;  // smallest normal fp32 number
 
 template <class DT>
@@ -302,7 +303,7 @@ __device__ __forceinline__ void turn8(const WriteParams &p, const uint16_t *src,
 // Up to ROWS consecutive rows of a token for each group of LANES = head_dim / 8 lanes: heads of q, or of k and then
 // v. The rows' reductions go side by side (a row's alone would wait for each of its shuffles).
 template <class DT, int LANES, int MODE, int ROWS>
-__global__ void __launch_bounds__(kThreads, 3) kv_write_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(kThreads, 6) kv_write_kernel(const WriteParams p) {
   griddep_wait();
   griddep_launch_dependents();
   constexpr int D = LANES * 8;
@@ -551,7 +552,7 @@ cudaError_t write_rows(const WriteParams &p, int mode, cudaStream_t stream) {
 template <class DT, int LANES>
 cudaError_t write_for(WriteParams p, int64_t tokens, int mode, cudaStream_t stream) {
   const int rows = p.q_heads + 2 * p.cache.kv_heads;
-  const int each = items_a_group(tokens, rows, LANES, kHeads);
+  const int each = items_a_group(tokens, rows, LANES, kRows);
   p.q_groups = (p.q_heads + each - 1) / each;
   p.row_groups = static_cast<uint32_t>(p.q_groups + (2 * p.cache.kv_heads + each - 1) / each);
   const int64_t most = kMaxThreads / (int64_t(p.row_groups) * LANES) - 1;
@@ -564,7 +565,7 @@ cudaError_t write_for(WriteParams p, int64_t tokens, int mode, cudaStream_t stre
     if (c.q) c.q += done * p.q_ts, c.q_out += done * p.q_heads * (LANES * 8);
     c.slots += done;
     if (c.positions) c.positions += done;
-    const cudaError_t e = each == 1 ? write_rows<DT, LANES, 1>(c, mode, stream) : write_rows<DT, LANES, kHeads>(c, mode, stream);
+    const cudaError_t e = each == 1 ? write_rows<DT, LANES, 1>(c, mode, stream) : write_rows<DT, LANES, kRows>(c, mode, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

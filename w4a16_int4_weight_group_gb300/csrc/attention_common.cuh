@@ -31,7 +31,26 @@ struct Queries {
   int n, first;  // query tokens, cache position of the first of them
 };
 
-__device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+// a / b of numbers that are not negative, in 32 bits where they fit (a 64-bit division takes hundreds of cycles).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
+// The list of `total` units cut into `ctas` contiguous shares, the first `extra` of them one unit longer.
+struct Shares {
+  int64_t total, ctas, each, extra;
+  __device__ __forceinline__ int64_t begin(int64_t c) const { return c * each + (c < extra ? c : extra); }
+  // the CTA whose share holds unit u
+  __device__ __forceinline__ int64_t owner(int64_t u) const {
+    const int64_t longer = extra * (each + 1);
+    return u < longer ? quotient(u, each + 1) : extra + quotient(u - longer, each);
+  }
+};
+__device__ __forceinline__ unsigned int add_acq_rel(unsigned int *p, unsigned int v) {
+  unsigned int old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
 
 __device__ __forceinline__ int length_of(const Params &p, int b) {
   const int64_t cap = p.max_pages * p.page_tiles * 16;
@@ -78,15 +97,15 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 // Writes a finished value group of four elements of a row.
-__device__ __forceinline__ void store_out4(const Params &p, int64_t at, float4 v) {
+__device__ __forceinline__ void store_out4(uint16_t *out, bool bf16, int64_t at, float4 v) {
   uint2 w;
-  if (p.bf16) {
+  if (bf16) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
     w = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
   } else {
     w = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
   }
-  *reinterpret_cast<uint2 *>(p.out + at) = w;
+  *reinterpret_cast<uint2 *>(out + at) = w;
 }
 
 // ... of eight elements (16 bytes).
@@ -133,13 +152,12 @@ __device__ __forceinline__ void query_unit(const Params &p, float top, float &up
   unit = fabsf(p.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
-// This CTA's share of the units: an equal part of the list over all sequences (total units over ctas CTAs; it
-// starts at cur, has `units` units and ends before unit u1). False when there is nothing for it. Without a
-// workspace the share is the segments that start in that part, whole. Called by all threads; scan_s has a
-// word for each of the W warps, share_s two words.
+// This CTA's share of the units: an equal part of the list over all sequences (it starts at cur, has `units` units
+// and ends before unit u1). False when there is nothing for it. Without a workspace the share is the segments that
+// start in that part, whole. Called by all threads; scan_s has a word for each of the W warps, share_s two words.
 template <class L, int W>
-__device__ __forceinline__ bool share_of(const Params &p, int64_t *scan_s, volatile int64_t *share_s, Cursor &cur, int64_t &u1,
-                                         int64_t &total, int64_t &ctas, int64_t &units) {
+__device__ __forceinline__ bool share_of(const Params &p, int64_t *scan_s, volatile int64_t *share_s, Cursor &cur, Shares &sh,
+                                         int64_t &u1, int64_t &units) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slice = (p.batch + 32 * W - 1) / (32 * W);
   int64_t mine = 0;
@@ -153,16 +171,20 @@ __device__ __forceinline__ bool share_of(const Params &p, int64_t *scan_s, volat
   if (lane == 31) scan_s[warp] = upto;
   __syncthreads();
   int64_t before = upto - mine;
-  total = 0;
+  sh.total = 0;
+#pragma unroll
   for (int w = 0; w < W; ++w) {
-    if (w < warp) before += scan_s[w];
-    total += scan_s[w];
+    const int64_t v = scan_s[w];
+    if (w < warp) before += v;
+    sh.total += v;
   }
-  ctas = total < gridDim.x ? total : gridDim.x;
+  sh.ctas = sh.total < gridDim.x ? sh.total : gridDim.x;
   const int64_t cta = blockIdx.x;
-  if (cta >= ctas) return false;
-  const int64_t u0 = cta * total / ctas;
-  u1 = (cta + 1) * total / ctas;
+  if (cta >= sh.ctas) return false;
+  sh.each = quotient(sh.total, sh.ctas);
+  sh.extra = sh.total - sh.each * sh.ctas;
+  const int64_t u0 = sh.begin(cta);
+  u1 = sh.begin(cta + 1);
   if (u0 >= before && u0 < before + mine) {
     int64_t at = u0 - before;
     for (int b = tid * slice;; ++b) {
@@ -179,9 +201,9 @@ __device__ __forceinline__ bool share_of(const Params &p, int64_t *scan_s, volat
   load_sequence<L>(p, static_cast<int>(share_s[0]), cur);
   {
     int64_t at = share_s[1];
-    cur.h = static_cast<int>(at / (int64_t(cur.nb) * cur.nrt));
+    cur.h = static_cast<int>(quotient(at, int64_t(cur.nb) * cur.nrt));
     at -= int64_t(cur.h) * cur.nb * cur.nrt;
-    cur.rt = static_cast<int>(at / cur.nb);
+    cur.rt = static_cast<int>(quotient(at, cur.nb));
     cur.blk = static_cast<int>(at - int64_t(cur.rt) * cur.nb);
   }
   units = u1 - u0;
@@ -204,19 +226,90 @@ __device__ __forceinline__ bool share_of(const Params &p, int64_t *scan_s, volat
   return true;
 }
 
-// Adds the parts of a split segment and writes its rows: THREADS threads, the parts in the order of the CTAs.
-// The maxima first, side by side (the parts of one long sequence are many), then CHUNK parts at a time their
-// weights and their weighted sums. scratch: THREADS + CHUNK * R floats.
-template <int R, int D, int THREADS, int CHUNK, class Slot, class Sync>
-__device__ __forceinline__ void join_parts(const Params &p, const Cursor &seg, const Queries &qu, int rows, int parts, Slot slot_of,
-                                           float *scratch, int tid, Sync sync) {
+// Barrier of THREADS threads: the CTA's own (BAR 0) or a named one.
+template <int BAR, int THREADS>
+__device__ __forceinline__ void sync_threads() {
+  if constexpr (BAR == 0) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"n"(BAR), "n"(THREADS) : "memory");
+}
+
+// A split segment's parts and where its rows go.
+struct Parts {
+  const float *slot0, *slot1;  // of the first part and of the second; those after it are two slots apart each
+  int count;
+  int rows;              // of the row tile in use
+  int first_row;         // of the row tile among the cache head's
+  int group, q_heads, head0;  // query heads of a cache head, of all, and the first of this cache head
+  int64_t q0;            // row of the sequence's first query token
+  uint16_t *out;
+  float *lse;
+  bool bf16;
+  float *scratch;        // THREADS + CHUNK * R floats
+};
+__device__ __forceinline__ Parts parts_of(const Params &p, const Cursor &seg, const Queries &qu, int rows, int height, int64_t c0, int count,
+                                          int64_t slot_floats, float *scratch) {
+  return Parts{p.partials + (2 * c0 + 1) * slot_floats, p.partials + 2 * (c0 + 1) * slot_floats, count, rows, seg.rt * height, p.group,
+               p.q_heads, seg.h * p.group, qu.q0, p.out, p.lse, p.bf16 != 0, scratch};
+}
+
+// The split segments that this CTA was the last to finish: at most two (the share's first and last). They are joined
+// after the share: inside it the joining's registers would push the loops over the cache into local memory.
+struct Pending {
+  Parts parts[2];
+  int count;
+};
+// Counts this CTA's part of a segment (units seg_u .. seg_u + nb - 1 of the list) in, its partial result being
+// written by the threads that `sync` joins; the last one to come is to join them.
+template <int BAR, int THREADS>
+__device__ __forceinline__ void count_in(const Params &p, const Shares &sh, const Cursor &seg, const Queries &qu, int rows, int height,
+                                         int64_t seg_u, int64_t slot_floats, float *scratch, Pending *pending, int tid) {
+  sync_threads<BAR, THREADS>();
+  if (tid == 0) {
+    const int64_t c0 = sh.owner(seg_u);
+    const int parts = static_cast<int>(sh.owner(seg_u + seg.nb - 1) - c0) + 1;
+    if (add_acq_rel(p.flags + c0, 1u) == static_cast<unsigned int>(parts - 1)) {
+      p.flags[c0] = 0u;
+      pending->parts[pending->count++] = parts_of(p, seg, qu, rows, height, c0, parts, slot_floats, scratch);
+    }
+  }
+}
+
+// Adds the parts of a split segment and writes its rows: THREADS threads, the parts in the order of the CTAs. The
+// maxima and denominators first, side by side (the parts of one long sequence are many), then the weighted sums with
+// many loads in flight: with one part after the other this took 11000 of the 36000 cycles of a call over 8192 tokens.
+template <int R, int D, int THREADS, int CHUNK, int BAR>
+__device__ __forceinline__ void join_parts(const Parts &g, const int tid) {
+  auto sync = [] { sync_threads<BAR, THREADS>(); };
+  const int parts = g.count, rows = g.rows;
+  float *scratch = g.scratch;
+  __threadfence();  // the other CTAs' parts, which the counter said are there
   float *red = scratch;            // [THREADS / R][R]
   float *wgt = scratch + THREADS;  // [CHUNK][R]
   constexpr int kLanes = THREADS / R;
   const int row_t = tid % R, lane_t = tid / R;
-  float top = -INFINITY;
-#pragma unroll 4
-  for (int c = lane_t; c < parts; c += kLanes) top = fmaxf(top, __ldcg(slot_of(c) + R * D + row_t));
+  constexpr int kFloats = R * (D + 2);
+  auto slot = [&](int c) { return c == 0 ? g.slot0 : g.slot1 + int64_t(c - 1) * (2 * kFloats); };
+  auto place = [&](int row) {  // of a row among all query heads of all tokens
+    const int gr = g.first_row + row, qi = gr / g.group;
+    return (g.q0 + qi) * g.q_heads + g.head0 + (gr - qi * g.group);
+  };
+  // the first parts' maxima and denominators, kept for the weights
+  constexpr int kKeep = 4;
+  float mc[kKeep], lc[kKeep], top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) {
+    const int c = lane_t + i * kLanes;
+    mc[i] = -INFINITY;
+    lc[i] = 0.f;
+    if (c < parts) {
+      const float *s = slot(c);
+      mc[i] = __ldcg(s + R * D + row_t);
+      lc[i] = __ldcg(s + R * (D + 1) + row_t);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i) top = fmaxf(top, mc[i]);
+  for (int c = lane_t + kKeep * kLanes; c < parts; c += kLanes) top = fmaxf(top, __ldcg(slot(c) + R * D + row_t));
   red[tid] = top;
   sync();
 #pragma unroll
@@ -224,7 +317,9 @@ __device__ __forceinline__ void join_parts(const Params &p, const Cursor &seg, c
   sync();
   constexpr int kPer = (R * D / 4 + THREADS - 1) / THREADS;  // groups of four elements of a thread
   constexpr int kPass = kPer < 4 ? kPer : 4;                 // of them at a time
+  constexpr int kFlight = kPass == 1 ? 16 : kPass == 2 ? 8 : 4;  // parts whose loads are in flight
   const bool works = R * D / 4 >= THREADS || tid < R * D / 4;
+  auto weight = [&](float m, float l) { return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2_approx(m - top); };
   float sum = 0.f;
 #pragma unroll 1
   for (int x0 = 0; x0 < kPer; x0 += kPass) {
@@ -234,22 +329,47 @@ __device__ __forceinline__ void join_parts(const Params &p, const Cursor &seg, c
 #pragma unroll 1
     for (int cc = 0; cc < parts; cc += CHUNK) {
       const int now = min(CHUNK, parts - cc);
-      for (int c = lane_t; c < now; c += kLanes) {
-        const float mc = __ldcg(slot_of(cc + c) + R * D + row_t), lc = __ldcg(slot_of(cc + c) + R * (D + 1) + row_t);
-        const float f = mc == -INFINITY ? (lc == 0.f ? 0.f : 1.f) : exp2_approx(mc - top);
-        wgt[c * R + row_t] = f;
-        if (x0 == 0) sum += lc * f;
+#pragma unroll
+      for (int i = 0; i < kKeep; ++i) {
+        const int c = lane_t + i * kLanes;
+        if (c < parts && c >= cc && c < cc + now) {
+          const float f = weight(mc[i], lc[i]);
+          wgt[(c - cc) * R + row_t] = f;
+          if (x0 == 0) sum += lc[i] * f;
+        }
+      }
+      // (parts past the kept ones: the same threads, read again)
+      for (int c = lane_t + kKeep * kLanes; c < cc + now; c += kLanes) {
+        if (c < cc) continue;
+        const float m = __ldcg(slot(c) + R * D + row_t), l = __ldcg(slot(c) + R * (D + 1) + row_t);
+        const float f = weight(m, l);
+        wgt[(c - cc) * R + row_t] = f;
+        if (x0 == 0) sum += l * f;
       }
       sync();
-#pragma unroll 4
-      for (int c = 0; c < now; ++c) {
-        const float4 *src = reinterpret_cast<const float4 *>(slot_of(cc + c)) + tid + x0 * THREADS;
+      if (works) {
+#pragma unroll 1
+        for (int c = 0; c < now; c += kFlight) {
+          float4 y[kFlight][kPass];
 #pragma unroll
-        for (int x = 0; x < kPass; ++x) {
-          if (!works) continue;
-          const float4 y = __ldcg(src + x * THREADS);
-          const float f = wgt[c * R + (tid + (x0 + x) * THREADS) / (D / 4)];
-          v[x] = make_float4(fmaf(y.x, f, v[x].x), fmaf(y.y, f, v[x].y), fmaf(y.z, f, v[x].z), fmaf(y.w, f, v[x].w));
+          for (int f = 0; f < kFlight; ++f) {
+            if (c + f < now) {
+              const float4 *src = reinterpret_cast<const float4 *>(slot(cc + c + f)) + tid + x0 * THREADS;
+#pragma unroll
+              for (int x = 0; x < kPass; ++x) y[f][x] = __ldcg(src + x * THREADS);
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < kFlight; ++f) {
+            if (c + f < now) {
+#pragma unroll
+              for (int x = 0; x < kPass; ++x) {
+                const float k = wgt[(c + f) * R + (tid + (x0 + x) * THREADS) / (D / 4)];
+                v[x] = make_float4(fmaf(y[f][x].x, k, v[x].x), fmaf(y[f][x].y, k, v[x].y), fmaf(y[f][x].z, k, v[x].z),
+                                   fmaf(y[f][x].w, k, v[x].w));
+              }
+            }
+          }
         }
       }
       sync();
@@ -265,24 +385,20 @@ __device__ __forceinline__ void join_parts(const Params &p, const Cursor &seg, c
         float s = 0.f;
 #pragma unroll
         for (int y = 0; y < kLanes; ++y) s += red[y * R + row];
-        const int gr = seg.rt * R + row, qi = gr / p.group;
-        const int64_t at = (qu.q0 + qi) * p.q_heads + seg.h * p.group + (gr - qi * p.group);
         const float inv = s == 0.f ? 0.f : 1.f / s;
-        store_out4(p, at * D + d, make_float4(v[x].x * inv, v[x].y * inv, v[x].z * inv, v[x].w * inv));
+        store_out4(g.out, g.bf16, place(row) * D + d, make_float4(v[x].x * inv, v[x].y * inv, v[x].z * inv, v[x].w * inv));
       }
     }
   }
-  if (p.lse) {
+  if (g.lse) {
     if (lane_t == 0) wgt[row_t] = top;
     sync();
     if (tid < rows) {
       float s = 0.f;
 #pragma unroll
       for (int y = 0; y < kLanes; ++y) s += red[y * R + tid];
-      const int gr = seg.rt * R + tid, qi = gr / p.group;
-      const int64_t at = (qu.q0 + qi) * p.q_heads + seg.h * p.group + (gr - qi * p.group);
       const float t = wgt[tid];
-      p.lse[at] = s == 0.f ? -INFINITY : (t == -INFINITY ? s : (t + log2f(s)) * kLn2);
+      g.lse[place(tid)] = s == 0.f ? -INFINITY : (t == -INFINITY ? s : (t + log2f(s)) * kLn2);
     }
   }
   sync();

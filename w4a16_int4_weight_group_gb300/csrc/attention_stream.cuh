@@ -55,7 +55,7 @@ struct StreamLayout {
   static constexpr bool kQSmem = NT * D >= 256; // Q's operands stay in shared memory, not in registers
   static constexpr int kCtas = NT * D >= 512 && D < 256 ? 1 : 2;  // on an SM
   static constexpr int kQBytes = R * D * 2;
-  static constexpr int kFixed = kQBytes + MB * R * kPad * 4 + R * (8 + 4) + 2 * W * R * 4 + 512;
+  static constexpr int kFixed = kQBytes + MB * R * kPad * 4 + R * (8 + 4) + 2 * W * R * 4 + 768;
   static constexpr int kBudget = (kCtas == 2 ? 113 : 226) * 1024;
   static constexpr int kFit = (kBudget - kFixed) / (W * kStage);
   static constexpr int S = kFit > 4 ? 4 : kFit;  // stages of a warp's ring
@@ -66,10 +66,11 @@ struct StreamLayout {
   static constexpr int kOffQs = kOffMask + R * 8;             // float a row: score unit
   static constexpr int kOffM = kOffQs + R * 4;                // [W][R] maxima, then denominators
   static constexpr int kOffBar = (kOffM + 2 * W * R * 4 + 7) / 8 * 8;
-  static constexpr int kOffMisc = kOffBar + 8 * (W * S + 1);  // abort flag, last flag, start, scan
-  static constexpr int kSmem = kOffMisc + 32 + 8 * W;
+  static constexpr int kOffMisc = kOffBar + 8 * (W * S + 1);  // abort flag, start, scan, split segments to join
+  static constexpr int kSmem = kOffMisc + 32 + 8 * W + sizeof(Pending);
   static_assert(S >= 2, "a ring of two stages at least");
   static_assert(kSmem <= kBudget, "shared memory");
+  static_assert(MB * R * kPad >= kThreads + 64 * R, "scratch of the joining of parts");
   static_assert(kOffRing % 128 == 0 && kOffO % 16 == 0 && kTile % 128 == 0, "alignment");
 };
 
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
   const uint32_t bars = base + L::kOffBar + 8u * S * warp;  // this warp's ring
   const uint32_t stall_bar = base + L::kOffBar + 8u * S * W;
   const uint32_t abort_flag = base + L::kOffMisc;
-  volatile uint32_t *last_s = reinterpret_cast<volatile uint32_t *>(smem + L::kOffMisc + 4);
+  Pending *pending = reinterpret_cast<Pending *>(smem + L::kOffMisc + 32 + 8 * W);
   volatile int64_t *share_s = reinterpret_cast<volatile int64_t *>(smem + L::kOffMisc + 8);
   int64_t *scan_s = reinterpret_cast<int64_t *>(smem + L::kOffMisc + 32);
   const uint32_t ring = base + L::kOffRing + static_cast<uint32_t>(warp * S * L::kStage);
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
   if (tid == 0) {
     mbar_init(stall_bar, 1);
     st_flag(abort_flag, 0u);
+    pending->count = 0;
   }
   mbar_init_fence();
   griddep_wait();
@@ -148,8 +150,9 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
   unsigned int *error = &p.control->error;
 
   Cursor cur;
-  int64_t u1, total, ctas, units;
-  if (!share_of<L, W>(p, scan_s, share_s, cur, u1, total, ctas, units)) return;  // nothing for this CTA
+  Shares sh;
+  int64_t u1, units;
+  if (!share_of<L, W>(p, scan_s, share_s, cur, sh, u1, units)) return;  // nothing for this CTA
   const int64_t cta = blockIdx.x;
 
   // ---- the ring: copies are issued S steps ahead, across segments
@@ -617,7 +620,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
             const int gr = seg.rt * R + row, qi = gr / p.group;
             const int64_t at = (qu.q0 + qi) * p.q_heads + seg.h * p.group + (gr - qi * p.group);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            store_out4(p, at * D + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+            store_out4(p.out, L::BF, at * D + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
             if (p.lse && d == 0) p.lse[at] = sum == 0.f ? -INFINITY : (top == -INFINITY ? sum : (top + log2f(sum)) * kLn2);
           }
         } else {
@@ -628,27 +631,11 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
           }
         }
       }
-      if (!is_whole) {
-        const int64_t c0 = ceil_div((seg_u + 1) * ctas, total) - 1;
-        const int64_t c1 = ceil_div((seg_u + seg.nb) * ctas, total) - 1;
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-          const unsigned int had = atomicAdd(p.flags + c0, 1u);
-          *last_s = had == static_cast<unsigned int>(c1 - c0);
-          if (*last_s) p.flags[c0] = 0u;
-        }
-        __syncthreads();
-        if (*last_s) {
-          __threadfence();
-          const int parts = static_cast<int>(c1 - c0) + 1;
-          auto slot_of = [&](int c) { return p.partials + (2 * (c0 + c) + (c == 0 ? 1 : 0)) * int64_t(R) * (D + 2); };
-          join_parts<R, D, L::kThreads, 32>(p, seg, qu, rows, parts, slot_of, o_s, tid, [] { __syncthreads(); });
-        }
-      }
+      if (!is_whole) count_in<0, L::kThreads>(p, sh, seg, qu, rows, R, seg_u, int64_t(R) * (D + 2), o_s, pending, tid);
     }
     __syncthreads();  // o_s, m_s, Q and the masks are free again
   }
+  for (int i = 0; i < pending->count; ++i) join_parts<R, D, L::kThreads, 64, 0>(pending->parts[i], tid);
   if (ld_flag(abort_flag) != 0) {
     // let this warp's own copies land before the shared memory is released
     for (int s = 0; s < S; ++s)

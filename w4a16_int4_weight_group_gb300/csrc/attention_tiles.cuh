@@ -60,7 +60,7 @@ struct TileLayout {
   static constexpr int kOffBar = kOffQs + 128 * 4;
   static constexpr int kBars = 2 + 2 + 2 + 2 + 4 + 2 + 2 + 2 + 4;
   static constexpr int kOffMisc = kOffBar + 8 * kBars;
-  static constexpr int kSmem = kOffMisc + 64 + kThreads / 4 + 1024;  // + slack to align the base to 1024 bytes
+  static constexpr int kSmem = kOffMisc + 64 + kThreads / 4 + sizeof(Pending) + 1024;  // + slack to align the base to 1024 bytes
   static constexpr uint32_t kTmemCols = 512;  // S of the groups at 0 and 128, O at 256 and 384
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) tiles_kernel(const Params p) {
   auto pv_done = [&](int g) { return bar0 + 8u * (16 + g); };
   const uint32_t q_full = bar0 + 8u * 18, all_done = bar0 + 8u * 19, stall_bar = bar0 + 8u * 20, pv_all_done = bar0 + 8u * 21;
   const uint32_t abort_flag = base + L::kOffMisc, tmem_slot = abort_flag + 4;
-  volatile uint32_t *last_s = reinterpret_cast<volatile uint32_t *>(smem + L::kOffMisc + 8);
+  Pending *pending = reinterpret_cast<Pending *>(smem + L::kOffMisc + 64 + L::kThreads / 4);
   volatile int64_t *share_s = reinterpret_cast<volatile int64_t *>(smem + L::kOffMisc + 32);
   int64_t *scan_s = reinterpret_cast<int64_t *>(smem + L::kOffMisc + 64);
 
@@ -303,6 +303,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) tiles_kernel(const Params p) {
     mbar_init(pv_all_done, 1);
     mbar_init(stall_bar, 1);
     st_flag(abort_flag, 0u);
+    pending->count = 0;
     mbar_init_fence();
   }
   griddep_wait();
@@ -312,8 +313,9 @@ __global__ void __launch_bounds__(L::kThreads, 1) tiles_kernel(const Params p) {
   unsigned int *error = &p.control->error;
 
   Cursor cur;
-  int64_t u1, total, ctas, units;
-  if (!share_of<L, W>(p, scan_s, share_s, cur, u1, total, ctas, units)) return;  // nothing for this CTA
+  Shares sh;
+  int64_t u1, units;
+  if (!share_of<L, W>(p, scan_s, share_s, cur, sh, u1, units)) return;  // nothing for this CTA
   const int64_t cta = blockIdx.x;
   if (warp == 16) tmem_alloc(tmem_slot, L::kTmemCols);
   tc_fence_before();
@@ -786,31 +788,15 @@ __global__ void __launch_bounds__(L::kThreads, 1) tiles_kernel(const Params p) {
             slot[R * (D + 1) + row] = sum;
           }
         }
-        if (!is_whole) {
-          const int64_t c0 = ceil_div((seg_u + 1) * ctas, total) - 1;
-          const int64_t c1 = ceil_div((seg_u + seg.nb) * ctas, total) - 1;
-          __threadfence();
-          bar_sync<1, 256>();
-          if (tid == 0) {
-            const unsigned int had = atomicAdd(p.flags + c0, 1u);
-            *last_s = had == static_cast<unsigned int>(c1 - c0);
-            if (*last_s) p.flags[c0] = 0u;
-          }
-          bar_sync<1, 256>();
-          if (*last_s) {
-            __threadfence();
-            // a thread: one row, half of the elements; the parts in the order of the CTAs
-            const int parts = static_cast<int>(c1 - c0) + 1;
-            auto slot_of = [&](int c) { return p.partials + (2 * (c0 + c) + (c == 0 ? 1 : 0)) * int64_t(R) * (D + 2); };
-            join_parts<R, D, 256, 8>(p, seg, qu, rows, parts, slot_of, reinterpret_cast<float *>(smem + L::kOffQ), tid, bar_sync<1, 256>);
-          }
-        }
+        if (!is_whole)
+          count_in<1, 256>(p, sh, seg, qu, rows, R, seg_u, int64_t(R) * (D + 2), reinterpret_cast<float *>(smem + L::kOffQ), pending, tid);
       }
       tc_fence_before();
       bar_sync<1, 256>();  // the sums and row_s have been read, Q may be written
       t0 += count;
       if (t0 < units) next_segment<L>(p, cur);
     }
+    for (int i = 0; i < pending->count; ++i) join_parts<R, D, 256, 8, 1>(pending->parts[i], tid);
   }
   tc_fence_before();
   __syncthreads();

@@ -159,53 +159,74 @@ template <class L, int W>
 __device__ __forceinline__ bool share_of(const Params &p, int64_t *scan_s, volatile int64_t *share_s, Cursor &cur, Shares &sh,
                                          int64_t &u1, int64_t &units) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int slice = (p.batch + 32 * W - 1) / (32 * W);
-  int64_t mine = 0;
-  for (int b = tid * slice; b < min(p.batch, (tid + 1) * slice); ++b) mine += load_sequence<L>(p, b, cur);
-  int64_t upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  if (lane == 31) scan_s[warp] = upto;
-  __syncthreads();
-  int64_t before = upto - mine;
-  sh.total = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    const int64_t v = scan_s[w];
-    if (w < warp) before += v;
-    sh.total += v;
-  }
-  sh.ctas = sh.total < gridDim.x ? sh.total : gridDim.x;
   const int64_t cta = blockIdx.x;
-  if (cta >= sh.ctas) return false;
-  sh.each = quotient(sh.total, sh.ctas);
-  sh.extra = sh.total - sh.each * sh.ctas;
-  const int64_t u0 = sh.begin(cta);
-  u1 = sh.begin(cta + 1);
-  if (u0 >= before && u0 < before + mine) {
-    int64_t at = u0 - before;
-    for (int b = tid * slice;; ++b) {
-      const int64_t n = load_sequence<L>(p, b, cur);
-      if (at < n) {
-        share_s[0] = b;
-        share_s[1] = at;
-        break;
-      }
-      at -= n;
+  auto scan = [&](int64_t x) {  // over the warp's lanes, this one's included
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += v;
     }
+    return x;
+  };
+  auto cut = [&](int64_t total) {
+    sh.total = total;
+    sh.ctas = total < gridDim.x ? total : gridDim.x;
+    if (cta >= sh.ctas) return false;
+    sh.each = quotient(total, sh.ctas);
+    sh.extra = total - sh.each * sh.ctas;
+    u1 = sh.begin(cta + 1);
+    return true;
+  };
+  int64_t u0, at;  // the share's first unit, among all and in its sequence
+  if (p.batch <= 32) {
+    // a lane for each sequence, every warp for itself: no barrier, and no second look at the lengths
+    int64_t mine = 0;
+    if (lane < p.batch) mine = load_sequence<L>(p, lane, cur);
+    const int64_t upto = scan(mine);
+    if (!cut(__shfl_sync(0xFFFFFFFFu, upto, 31))) return false;
+    u0 = sh.begin(cta);
+    const int b = __popc(__ballot_sync(0xFFFFFFFFu, upto <= u0));
+    at = u0 - __shfl_sync(0xFFFFFFFFu, upto - mine, b);
+    cur.b = b;
+    cur.nb = __shfl_sync(0xFFFFFFFFu, cur.nb, b);
+    cur.nrt = __shfl_sync(0xFFFFFFFFu, cur.nrt, b);
+    cur.len = __shfl_sync(0xFFFFFFFFu, cur.len, b);
+  } else {
+    const int slice = (p.batch + 32 * W - 1) / (32 * W);
+    int64_t mine = 0;
+    for (int b = tid * slice; b < min(p.batch, (tid + 1) * slice); ++b) mine += load_sequence<L>(p, b, cur);
+    const int64_t upto = scan(mine);
+    if (lane == 31) scan_s[warp] = upto;
+    __syncthreads();
+    int64_t before = upto - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const int64_t v = scan_s[w];
+      if (w < warp) before += v;
+      total += v;
+    }
+    if (!cut(total)) return false;
+    u0 = sh.begin(cta);
+    if (u0 >= before && u0 < before + mine) {
+      int64_t rest = u0 - before;
+      for (int b = tid * slice;; ++b) {
+        const int64_t n = load_sequence<L>(p, b, cur);
+        if (rest < n) {
+          share_s[0] = b;
+          share_s[1] = rest;
+          break;
+        }
+        rest -= n;
+      }
+    }
+    __syncthreads();
+    load_sequence<L>(p, static_cast<int>(share_s[0]), cur);
+    at = share_s[1];
   }
-  __syncthreads();
-  load_sequence<L>(p, static_cast<int>(share_s[0]), cur);
-  {
-    int64_t at = share_s[1];
-    cur.h = static_cast<int>(quotient(at, int64_t(cur.nb) * cur.nrt));
-    at -= int64_t(cur.h) * cur.nb * cur.nrt;
-    cur.rt = static_cast<int>(quotient(at, cur.nb));
-    cur.blk = static_cast<int>(at - int64_t(cur.rt) * cur.nb);
-  }
+  cur.h = static_cast<int>(quotient(at, int64_t(cur.nb) * cur.nrt));
+  at -= int64_t(cur.h) * cur.nb * cur.nrt;
+  cur.rt = static_cast<int>(quotient(at, cur.nb));
+  cur.blk = static_cast<int>(at - int64_t(cur.rt) * cur.nb);
   units = u1 - u0;
   if (!p.flags) {
     if (cur.blk != 0) {
@@ -282,7 +303,6 @@ __device__ __forceinline__ void join_parts(const Parts &g, const int tid) {
   auto sync = [] { sync_threads<BAR, THREADS>(); };
   const int parts = g.count, rows = g.rows;
   float *scratch = g.scratch;
-  __threadfence();  // the other CTAs' parts, which the counter said are there
   float *red = scratch;            // [THREADS / R][R]
   float *wgt = scratch + THREADS;  // [CHUNK][R]
   constexpr int kLanes = THREADS / R;
@@ -293,6 +313,23 @@ __device__ __forceinline__ void join_parts(const Parts &g, const int tid) {
     const int gr = g.first_row + row, qi = gr / g.group;
     return (g.q0 + qi) * g.q_heads + g.head0 + (gr - qi * g.group);
   };
+  constexpr int kPer = (R * D / 4 + THREADS - 1) / THREADS;  // groups of four elements of a thread
+  constexpr int kPass = kPer < 4 ? kPer : 4;                 // of them at a time
+  constexpr int kFlight = kPass == 1 ? 16 : kPass == 2 ? 8 : 4;  // parts whose loads are in flight
+  auto mine = [&](int x) { return R * D / 4 % THREADS == 0 || tid + x * THREADS < R * D / 4; };  // this thread has group x
+  float4 y[kFlight][kPass];
+  auto fetch = [&](int c0, int end, int x0) {
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      if (c0 + f < end) {
+        const float4 *src = reinterpret_cast<const float4 *>(slot(c0 + f)) + tid + x0 * THREADS;
+#pragma unroll
+        for (int x = 0; x < kPass; ++x)
+          if (mine(x0 + x)) y[f][x] = __ldcg(src + x * THREADS);
+      }
+    }
+  };
+  fetch(0, min(parts, CHUNK), 0);  // (in flight while the weights are made)
   // the first parts' maxima and denominators, kept for the weights
   constexpr int kKeep = 4;
   float mc[kKeep], lc[kKeep], top = -INFINITY;
@@ -315,10 +352,6 @@ __device__ __forceinline__ void join_parts(const Parts &g, const int tid) {
 #pragma unroll
   for (int x = 0; x < kLanes; ++x) top = fmaxf(top, red[x * R + row_t]);
   sync();
-  constexpr int kPer = (R * D / 4 + THREADS - 1) / THREADS;  // groups of four elements of a thread
-  constexpr int kPass = kPer < 4 ? kPer : 4;                 // of them at a time
-  constexpr int kFlight = kPass == 1 ? 16 : kPass == 2 ? 8 : 4;  // parts whose loads are in flight
-  const bool works = R * D / 4 >= THREADS || tid < R * D / 4;
   auto weight = [&](float m, float l) { return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2_approx(m - top); };
   float sum = 0.f;
 #pragma unroll 1
@@ -347,23 +380,16 @@ __device__ __forceinline__ void join_parts(const Parts &g, const int tid) {
         if (x0 == 0) sum += l * f;
       }
       sync();
-      if (works) {
+      {
 #pragma unroll 1
         for (int c = 0; c < now; c += kFlight) {
-          float4 y[kFlight][kPass];
-#pragma unroll
-          for (int f = 0; f < kFlight; ++f) {
-            if (c + f < now) {
-              const float4 *src = reinterpret_cast<const float4 *>(slot(cc + c + f)) + tid + x0 * THREADS;
-#pragma unroll
-              for (int x = 0; x < kPass; ++x) y[f][x] = __ldcg(src + x * THREADS);
-            }
-          }
+          if (c + cc + x0 > 0) fetch(cc + c, cc + now, x0);
 #pragma unroll
           for (int f = 0; f < kFlight; ++f) {
             if (c + f < now) {
 #pragma unroll
               for (int x = 0; x < kPass; ++x) {
+                if (!mine(x0 + x)) continue;
                 const float k = wgt[(c + f) * R + (tid + (x0 + x) * THREADS) / (D / 4)];
                 v[x] = make_float4(fmaf(y[f][x].x, k, v[x].x), fmaf(y[f][x].y, k, v[x].y), fmaf(y[f][x].z, k, v[x].z),
                                    fmaf(y[f][x].w, k, v[x].w));
@@ -381,7 +407,7 @@ __device__ __forceinline__ void join_parts(const Parts &g, const int tid) {
 #pragma unroll
     for (int x = 0; x < kPass; ++x) {
       const int i = tid + (x0 + x) * THREADS, row = i / (D / 4), d = (i % (D / 4)) * 4;
-      if (works && row < rows) {
+      if (mine(x0 + x) && row < rows) {
         float s = 0.f;
 #pragma unroll
         for (int y = 0; y < kLanes; ++y) s += red[y * R + row];

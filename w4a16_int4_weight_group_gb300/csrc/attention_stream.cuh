@@ -46,14 +46,14 @@ struct StreamLayout {
   static constexpr int RB = D * BITS / 8;       // bytes of a token's codes
   static constexpr int kTile = 16 * (2 * RB + 8);
   static constexpr int TPS = kTile <= 2176 && NT < 4 ? 2 : 1;  // tiles of a warp's step
-  static constexpr int W = D == 256 ? 4 : 8;         // warps
+  static constexpr int W = D == 256 ? 4 : NT * D == 256 ? 12 : 8;  // warps
   static constexpr int kThreads = 32 * W;
   static constexpr int kStage = TPS * kTile;
   static constexpr int kUnit = W * TPS * 16;    // tokens of a unit
   static constexpr int MB = W / 2;              // sums kept in shared memory when the warps join
   static constexpr int kPad = D + 4;            // floats of a row of them
   static constexpr bool kQSmem = NT * D >= 256; // Q's operands stay in shared memory, not in registers
-  static constexpr int kCtas = NT * D >= 512 && D < 256 ? 1 : 2;  // on an SM
+  static constexpr int kCtas = NT * D >= 256 && D < 256 ? 1 : 2;  // on an SM (one: more registers, none spilled in the loop)
   static constexpr int kQBytes = R * D * 2;
   static constexpr int kFixed = kQBytes + MB * R * kPad * 4 + R * (8 + 4) + 2 * W * R * 4 + 768;
   static constexpr int kBudget = (kCtas == 2 ? 113 : 226) * 1024;
@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
     pending->count = 0;
   }
   mbar_init_fence();
+  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
   const uint64_t lim = p.control->limit_ns;

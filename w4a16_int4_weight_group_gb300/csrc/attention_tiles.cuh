@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) tiles_kernel(const Params p) {
     pending->count = 0;
     mbar_init_fence();
   }
+  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
   const uint64_t lim = p.control->limit_ns;

@@ -45,7 +45,7 @@ struct StreamLayout {
   static constexpr int R = 8 * NT;              // query rows of a row tile
   static constexpr int RB = D * BITS / 8;       // bytes of a token's codes
   static constexpr int kTile = 16 * (2 * RB + 8);
-  static constexpr int TPS = kTile <= 2176 && NT < 4 ? 2 : 1;  // tiles of a warp's step
+  static constexpr int TPS = kTile <= 2176 && NT == 1 ? 2 : 1;  // tiles of a warp's step
   static constexpr int W = D == 256 ? 4 : NT * D == 256 ? 12 : 8;  // warps
   static constexpr int kThreads = 32 * W;
   static constexpr int kStage = TPS * kTile;

@@ -43,7 +43,6 @@ cudaError_t launch_tree_attention(const AttentionArgs &a, const DeviceInfo &dev)
   p.page_table = a.page_table;
   p.max_pages = a.max_pages;
   p.num_pages = a.cache.num_pages;
-  p.tile_bytes = kv_tile_bytes(a.cache.head_dim, a.cache.bits);
   p.tree_mask = a.tree_mask;
   p.scale = a.scale;
   p.out = static_cast<uint16_t *>(a.out);

@@ -297,7 +297,8 @@ __device__ __forceinline__ void count_in(const Params &p, const Shares &sh, cons
 
 // Adds the parts of a split segment and writes its rows: THREADS threads, the parts in the order of the CTAs. The
 // maxima and denominators first, side by side (the parts of one long sequence are many), then the weighted sums with
-// many loads in flight: with one part after the other this took 11000 of the 36000 cycles of a call over 8192 tokens.
+// many loads in flight: with one part after the other this took 11000 of the 36000 cycles of a call over 8192 tokens
+// (131073 tokens 76.5 us, joined this way 67.7).
 template <int R, int D, int THREADS, int CHUNK, int BAR>
 __device__ __forceinline__ void join_parts(const Parts &g, const int tid) {
   auto sync = [] { sync_threads<BAR, THREADS>(); };

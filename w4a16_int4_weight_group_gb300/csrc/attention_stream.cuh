@@ -7,7 +7,7 @@
 // Bound by the cache's bytes ((2 D bits / 8 + 8) a token and cache head) and, with 4-bit codes, nearly as
 // much by the instructions that turn codes into operands. So:
 //
-//  * Work split. The units are (sequence, cache head, row tile, 256 tokens), in this order; every CTA of a
+//  * Work split. The units are (sequence, cache head, row tile, 64 to 256 tokens), in this order; every CTA of a
 //    resident grid takes an equal, contiguous share of them, whatever the lengths are. A CTA that holds all of
 //    a segment (sequence, head, row tile) writes its result; otherwise it leaves its sums in the workspace
 //    and the last one to finish adds them in the order of the CTAs (so results do not depend on timing).
@@ -29,6 +29,15 @@
 //    that every probability counts with 11 bits over the range of fp32.
 //  * The running maximum is raised only when a score exceeds it by more than 3 (in powers of two), so most
 //    steps need neither the reduction across lanes nor the rescaling of the sums.
+//
+// Measured (HBM: share of the device's 6782 GB/s copy rate):
+//  * 131073 tokens of 8 heads of 128 elements, 8 bits, 5 rows a head: 65 us = 4.2 TB/s, 0.62 of it. Each further
+//    131072 tokens take 45 us (0.90): about 15 us are the call's start, first loads and the joining of the parts.
+//  * 48 sequences of up to 6001 tokens, 4 bits: 76 us = 2.2 TB/s (0.32). A 4-bit code costs the instructions of an
+//    8-bit one for half of the bytes; the schedulers issue in half of the cycles.
+//  * 12 sequences of up to 8200 tokens, heads of 256 elements, 8 bits, 13 drafted tokens: 77 us. 26 rows are two row
+//    tiles, so every code is decoded twice, by eight warps on an SM (255 registers a thread).
+//  * 517 tokens of one sequence: 12 us a call, which is what the host takes to issue it.
 #pragma once
 
 #include "attention.h"

@@ -9,15 +9,16 @@
 //    maximum, denominator and sums, so that the tensor cores work on one group's tile while the other's is in
 //    the softmax; the groups are joined at the end of a segment. A thread has one row: no reduction
 //    across threads.
-//  * warps 8-15: the codes, four warps for the keys and four for the values. Loaded straight into registers one tile ahead (16 contiguous bytes a thread and
+//  * warps 8-15: the codes, four warps for the keys and four for the values (on four warps for both 393 us
+//    where this takes 356). Loaded straight into registers one tile ahead (16 contiguous bytes a thread and
 //    load; the cache tiles are brought into L2 three tiles ahead), turned into exact integers u - z by a
 //    byte permutation or LOP3 and a subtraction, and stored as the operands' 128-byte-swizzled tiles: K-major
 //    keys (fp16), MN-major values (bf16); a token's elements stay together in both, so nothing is transposed.
 //    Inside a group of 8, 4-bit elements are stored in the order 0 4 1 5 2 6 3 7; Q uses the same order and
 //    the epilogue undoes it. They also leave the tokens' scales as floats.
-//  * warp 16 (it allocates tensor memory too) and warp 17: one thread each issues the MMAs, S = Q K^T (M 128, N 128)
-//    and O += P V, P read from tensor memory, where it overwrites S. (One thread for both spent as long on its
-//    waits and commits between them as on the MMAs.)
+//  * warp 16 (it allocates tensor memory too) and warp 17: one thread each issues the MMAs, S = Q K^T (M 128,
+//    N 128) and O += P V, P read from tensor memory, where it overwrites S. (One thread for both spent as long
+//    on its waits and commits between them as on the MMAs.)
 //
 // Keys' scales multiply the fp32 scores, values' scales the probabilities. A probability times its scale is the
 // sum of two bf16 numbers (upper half of the fp32 number, then the rest rounded), two products for each tile:
@@ -27,6 +28,15 @@
 // slack has some row raise in nearly every tile (measured: 2600 of 5960 cycles a tile with fp16 and half a power).
 // The work split over CTAs, the workspace and the bounded waits are those of the streaming kernel
 // (attention_stream.cuh).
+//
+// Measured: 6 sequences of 20000 tokens, 64 drafted tokens, 8 heads of 128 elements at 4 bits, 320 rows a head (157
+// GFLOP): 355 us = 442 TFLOP/s, 0.23 of the library's dense bf16 rate; about 4600 cycles for a tile of 128 rows x
+// 128 tokens. What sets the pace is the chain of a group's tile, QK (700 cycles), largest score (1000), exponentials
+// (3500 to 4000), PV (1390), and the signals between them: the two groups' chains overlap, a group's own tiles do
+// not (a third S would need the columns of the second group's sums). Two threads a row (sixteen softmax warps of 72
+// registers) took 356 us: shorter steps, but more warps on the same pipes and spilled registers. Parts of that
+// variant left out for timing: without the exponentials and maxima 263 us (the codes' warps are then the longest),
+// without the codes 337, with the products alone 180. 24 more registers a softmax thread (setmaxnreg): 377 -> 356.
 #pragma once
 
 #include "attention.h"
@@ -139,13 +149,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&x)[4]) {
@@ -166,15 +169,6 @@ __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.
 template <int ID, int THREADS>
 __device__ __forceinline__ void bar_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
-}
-__device__ __forceinline__ bool bar_or(int id, int threads, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"(x ? 1u : 0u)
-      : "memory");
-  return r != 0;
 }
 
 // Eight 4-bit codes as fp16 integers u - z in the order 0 4, 1 5, 2 6, 3 7 (lo = 1024 + z, hi = 64 + z, twice).

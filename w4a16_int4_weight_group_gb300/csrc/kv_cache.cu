@@ -20,6 +20,14 @@
 // row are 8, 16 or 32 neighbours and its minimum and maximum are a few shuffles. A thread takes up to four heads (the
 // write: two) of one token: their loads are in flight together, and the token's cosines and sines (four times the bytes of a
 // 16-bit vector), its slot and its place in the cache are fetched once for them. With little work it takes one.
+//
+// Measured (share of the device's 6782 GB/s copy rate):
+//  * rotation of 8191 tokens x 48 heads of 128, 64 rotated: 36.5 us for 203 MB, 5.6 TB/s (0.82; one head a thread: 44)
+//  * write with rotation of 8192 tokens, 40 q and 8 cached heads, 8 bits: 57 us with the
+//    read of the same tokens after it, 274 MB in all, 4.8 TB/s (0.71); in the write (50 us with a cold cache) the
+//    schedulers issue in 73 % of the cycles (the reductions and conversions of each row)
+//  * read of 50001 tokens of 8 heads, 4 bits: 41 us for 260 MB, 6.3 TB/s (0.93)
+//  * 5 or 16 tokens: 7.5 and 10 us a call, which is the host's time to issue it
 #include "common.cuh"
 #include "internal.h"
 

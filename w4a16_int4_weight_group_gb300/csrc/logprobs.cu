@@ -17,6 +17,11 @@
 // by (value, lower index), a total order, so equal logits, and masked rows in which most elements are the
 // same, neither overflow the list nor make the result depend on timing. A row that rises along its length
 // can overflow it; it is then read again k times.
+//
+// Measured: 1024 rows of 128007 bf16 logits, 20 alternatives: 72 us for 262 MB, 3.6 TB/s, 0.54 of the device's copy
+// rate. 1024 rows are 1.7 waves of four CTAs on an SM; in them the schedulers issue in 64 % of the cycles
+// (conversion, subtraction, exponential, two sums and the comparison with the bound for each element).
+// 5 rows of 32003: 12.5 us a call, which is the host's time to issue it (four output tensors).
 #include "common.cuh"
 #include "internal.h"
 
@@ -499,7 +504,9 @@ cudaError_t launch_token_logprobs(const LogprobArgs &a, const DeviceInfo &dev) {
   p.entropy = a.entropy;
   p.top_ids = a.top_ids;
   p.top_logprobs = a.top_logprobs;
-  // few rows: up to eight CTAs (one cluster) share a row, while each keeps at least 4096 elements
+  // Few rows: up to eight CTAs (one cluster) share a row, while each keeps at least 4096 elements and all are resident
+  // at once. 256 x 128007 with 20 alternatives: clusters of two 29 us (one CTA a row about as long, its times from 27 to
+  // 68 between 160 and 400 rows); 1024 rows, past the residency: one CTA 73 us, two 90, four 121.
   int c = 1;
   while (c < 8 && a.rows * c * 2 <= kCtas * dev.num_sms && a.vocab / (c * 2) >= 4096) c *= 2;
   p.csize = c;

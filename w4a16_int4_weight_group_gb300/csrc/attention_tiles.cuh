@@ -32,11 +32,13 @@
 // Measured: 6 sequences of 20000 tokens, 64 drafted tokens, 8 heads of 128 elements at 4 bits, 320 rows a head (157
 // GFLOP): 355 us = 442 TFLOP/s, 0.23 of the library's dense bf16 rate; about 4600 cycles for a tile of 128 rows x
 // 128 tokens. A group's tile goes through QK (700 cycles), largest score (1000), exponentials (3500 to 4000) and PV
-// (1390, two products), while the other group is somewhere in the same steps. No counter is near its limit (schedulers 54 %,
-// tensor pipe 34 %), and the time is not one step's: two threads a row (sixteen softmax warps of 72 registers) took 356
-// us, P handed to its product in two or four pieces 356. In the former, parts left out for timing: codes 337,
-// exponentials 279, both 224, the maxima too 180. These add up as if products and softmax hardly overlapped,
-// which would be so if the two groups ran in step; this has not been shown. 24 more registers a softmax thread (setmaxnreg): 377 -> 356.
+// (1390, two products). The softmax sets the pace: with the groups made to take turns in it, so that one tile's
+// products lie under the other's softmax, a call takes 381 us, so one tile's maxima and exponentials alone take about
+// as long as a tile in all, and not less on more warps: two threads a row (sixteen warps of 72 registers) took 356
+// us, 370 in turns. P handed to its product in two or four pieces: 356. Parts left out for timing, with two
+// threads a row: codes 337, exponentials 279, both 224, the maxima too 180. No counter is near its limit
+// (schedulers 54 %, shared memory's pipe 39 % without the tensor cores' reads, tensor pipe 34 %).
+// 24 more registers a softmax thread (setmaxnreg): 377 -> 356.
 #pragma once
 
 #include "attention.h"

@@ -356,8 +356,10 @@ w4a16_status w4a16_kv_read(const w4a16_kv_cache_t *cache, const int64_t *slots, 
  * that no sequence owns, are not written. Scores, softmax statistics and sums are fp32; the probabilities are
  * rounded to 11 significant bits for the product with the values' codes.
  *   workspace   device memory, 256-byte aligned, w4a16_tree_attention_workspace_size bytes, as for w4a16_gemm_ws: its
- *               first 4 KiB zero before first use (every call leaves them zero; the same buffer may serve both
- *               functions on one stream). NULL or a smaller one: a sequence's tokens are not split over CTAs.
+ *               first 4 KiB zero before first use (every call that completes leaves them zero, one that gives up a
+ *               bounded wait may not; the same buffer may serve both functions on one stream, and a captured
+ *               call needs it for as long as its graph is replayed). NULL or a smaller one: a sequence's tokens are
+ *               not split over CTAs.
  * Errors: INVALID_ARG, UNSUPPORTED (dtype, bits, head_dim, max_q), MISALIGNED, CUDA. A kernel that gives up a
  * bounded wait is reported by w4a16_get_device_error.
  */
@@ -409,6 +411,13 @@ const char *w4a16_last_error(void);
  * released its resources), W4A16_OK otherwise. Synchronises the current device.
  */
 w4a16_status w4a16_get_device_error(void);
+
+/*
+ * w4a16_stream_capture_id - a number (not zero, and another one for every capture) while the stream is being captured
+ * into a CUDA graph, 0 otherwise. For bindings that keep workspaces: a captured call keeps its workspace's address, so
+ * the graph needs one of its own, zeroed by a node of its own. Neither synchronises nor disturbs a capture.
+ */
+uint64_t w4a16_stream_capture_id(w4a16_stream_t stream);
 
 /* Path w4a16_gemm would choose for these sizes on the current device (a w4a16_path value), or -1. */
 int w4a16_debug_selected_path(int64_t m, int64_t k, int64_t n, int group_size);

@@ -70,6 +70,7 @@ SIGNATURES = [
     ("w4a16_plan", _c_int, [_c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_int, _c_int, ctypes.POINTER(Plan)]),
     ("w4a16_last_error", ctypes.c_char_p, []),
     ("w4a16_get_device_error", _c_int, []),
+    ("w4a16_stream_capture_id", ctypes.c_uint64, [_vp]),
     ("w4a16_debug_selected_path", _c_int, [_c_i64, _c_i64, _c_i64, _c_int]),
     ("w4a16_debug_force_path", _c_int, [_c_int]),
     ("w4a16_debug_decode_override", _c_int, [_c_int, _c_int, _c_int]),
@@ -224,6 +225,24 @@ def w4a16_dequant(b_q: torch.Tensor, scales: torch.Tensor, qzeros: Optional[torc
 
 
 _workspaces = {}
+_captured = {}  # (device, stream) -> (number of the stream's last capture, its workspace)
+_capture_fn = None
+
+
+def _capture_id(stream: int) -> int:
+    """Number (not zero) of the capture that the stream takes part in, 0 when there is none."""
+    global _capture_fn
+    if not stream:
+        return 0  # the legacy default stream cannot be captured
+    if _capture_fn is None:
+        L = lib()
+        try:
+            from . import _w4a16_call as m
+            m.bind_capture(ctypes.cast(L.w4a16_stream_capture_id, _vp).value)
+            _capture_fn = m.capture_id
+        except (ImportError, AttributeError):
+            _capture_fn = L.w4a16_stream_capture_id
+    return _capture_fn(stream)
 
 
 # workspace bytes per (device, m, k, n, group_size, dtype): a pure function of the shape and the device
@@ -235,8 +254,22 @@ def workspace_for(device: torch.device, stream, nbytes: int) -> torch.Tensor:
 
     It is zero-filled when (re)allocated; the library leaves its flag area (the first 4 KiB) zero
     after every call and needs nothing else of the rest between calls.
+
+    A graph keeps the addresses of its calls. So while the stream is being captured, the buffer is one of the
+    capture's own: allocated in it (torch.cuda.graph: from the graph's memory pool, which lives as long as the
+    graph), its flag area zeroed by a node of the graph, used by no eager call and no other graph. The buffers
+    of eager calls never get into a graph, and may be replaced. (A stream captured by other means than torch has no
+    such pool: calls under it take a workspace of the caller's, or none.)
     """
     key = (device.index, int(stream))
+    capture = _capture_id(key[1])
+    if capture:
+        of, buf = _captured.get(key, (0, None))
+        if of != capture or buf.numel() < nbytes:
+            buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+            buf[:4096].zero_()
+            _captured[key] = (capture, buf)
+        return buf
     buf = _workspaces.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)

@@ -686,6 +686,17 @@ int w4a16_debug_selected_path(int64_t m, int64_t k, int64_t n, int group_size) {
   return p.path;
 }
 
+uint64_t w4a16_stream_capture_id(w4a16_stream_t stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(reinterpret_cast<cudaStream_t>(stream), &status, &id) != cudaSuccess) {
+    // (the legacy stream while another one is captured: it is not itself captured, and the error is not sticky)
+    cudaGetLastError();
+    return 0;
+  }
+  return status == cudaStreamCaptureStatusActive ? static_cast<uint64_t>(id) + 1 : 0;
+}
+
 w4a16_status w4a16_get_device_error(void) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "synchronise");

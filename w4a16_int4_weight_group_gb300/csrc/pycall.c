@@ -11,6 +11,8 @@
  *     layer, a, out, ws, stream: integers (addresses; None or 0 for a null pointer);
  *     m: int64; ws_bytes: size_t. The GIL is released around the call.
  *
+ *   bind_capture(address), capture_id(stream) -> int  w4a16_stream_capture_id
+ *
  *   bind_serving(rope, kv_write, kv_read, tree_attention, token_logprobs)   addresses of the five
  *   rope, kv_write, kv_read, tree_attention, token_logprobs -> status (int): flat arguments, the fields of
  *     w4a16_rope_t (positions, table, table_rows, rot_dim, interleaved; positions 0: no rope) and of
@@ -66,6 +68,29 @@ static PyObject *layer_gemm(PyObject *self, PyObject *const *args, Py_ssize_t na
   st = g_layer_gemm(layer, a, out, (int64_t)m, ws, ws_bytes, stream);
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(st);
+}
+
+static uint64_t (*g_capture_id)(w4a16_stream_t) = NULL;
+
+static PyObject *bind_capture(PyObject *self, PyObject *arg) {
+  (void)self;
+  void *p = PyLong_AsVoidPtr(arg);
+  if (p == NULL) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind_capture: null function address");
+    return NULL;
+  }
+  *(void **)&g_capture_id = p;
+  Py_RETURN_NONE;
+}
+static PyObject *capture_id(PyObject *self, PyObject *arg) {
+  (void)self;
+  if (g_capture_id == NULL) {
+    PyErr_SetString(PyExc_RuntimeError, "capture_id: bind_capture() was not called");
+    return NULL;
+  }
+  void *stream = as_ptr(arg);
+  if (PyErr_Occurred()) return NULL;
+  return PyLong_FromUnsignedLongLong(g_capture_id((w4a16_stream_t)stream));
 }
 
 /* Integer arguments (None counts as 0) of a call that takes `want` of them; argument `f` (if not negative)
@@ -180,6 +205,8 @@ static PyMethodDef kMethods[] = {
     {"bind", (PyCFunction)bind, METH_O, "bind(address of w4a16_layer_gemm)"},
     {"layer_gemm", (PyCFunction)(void (*)(void))layer_gemm, METH_FASTCALL,
      "layer_gemm(layer, a, out, m, ws, ws_bytes, stream) -> status"},
+    {"bind_capture", (PyCFunction)bind_capture, METH_O, "bind_capture(address of w4a16_stream_capture_id)"},
+    {"capture_id", (PyCFunction)capture_id, METH_O, "capture_id(stream) -> number of its capture, 0 for none"},
     {"bind_serving", FAST(bind_serving), "bind_serving(rope, kv_write, kv_read, tree_attention, token_logprobs)"},
     {"rope", FAST(rope), "w4a16_rope, flat arguments -> status"},
     {"kv_write", FAST(kv_write), "w4a16_kv_write, flat arguments -> status"},

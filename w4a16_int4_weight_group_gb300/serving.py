@@ -319,10 +319,16 @@ def w4a16_kv_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype
 _attention_ws: dict = {}  # workspace bytes: a pure function of the sizes and the device
 
 
+def w4a16_tree_attention_workspace_size(max_q: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of the workspace that a call of w4a16_tree_attention with these sizes uses on the current device."""
+    return int(lib().w4a16_tree_attention_workspace_size(max_q, q_heads, kv_heads, head_dim))
+
+
 def w4a16_tree_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
                          q_start: Optional[torch.Tensor] = None, tree_mask: Optional[torch.Tensor] = None,
                          softmax_scale: Optional[float] = None, max_q: Optional[int] = None,
-                         out: Optional[torch.Tensor] = None, return_lse: bool = False):
+                         out: Optional[torch.Tensor] = None, return_lse: bool = False,
+                         workspace: Optional[torch.Tensor] = None):
     """softmax(scale q k^T) v of each sequence's query tokens over its cached tokens, the query tokens among them.
 
     q [total_q, q_heads, head_dim]; page_table int32 [batch, max_pages]; kv_lens int32 [batch]; q_start int32
@@ -330,6 +336,10 @@ def w4a16_tree_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch
     its own sequence; None: a chain); softmax_scale: head_dim ** -0.5 unless given; max_q: the most query tokens of
     a sequence, at most 64 (unless given: min(total_q, 64), 1 without q_start). Returns out, or (out, lse) with lse
     float32 [total_q, q_heads]. A query that sees nothing gives zeros and -inf.
+
+    workspace: contiguous uint8 [bytes] of the caller's own, its first 4 KiB zero before its first use, for calls of
+    one stream (or one graph) at a time; with fewer bytes than w4a16_tree_attention_workspace_size no sequence is split
+    over CTAs. Unless given, the binding keeps one for each stream, and one for each capture by torch.cuda.graph.
     """
     shape = _three(q, "q")
     dev = _device(q)
@@ -360,14 +370,18 @@ def w4a16_tree_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch
         lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
         sep = lse.data_ptr()
     stream = _current_stream(dev)
-    key = (dev, max_q, Hq, c[2], D)
-    need = _attention_ws.get(key)
-    if need is None:
-        need = _attention_ws[key] = int(lib().w4a16_tree_attention_workspace_size(max_q, Hq, c[2], D))
     wp = wb = 0
-    if need:
-        ws = workspace_for(q.device, stream, need)
-        wp, wb = ws.data_ptr(), ws.numel()
+    if workspace is not None:
+        wb = workspace.numel()
+        wp = _index(workspace, "workspace", torch.uint8, (wb,), dev)
+    else:
+        key = (dev, max_q, Hq, c[2], D)
+        need = _attention_ws.get(key)
+        if need is None:
+            need = _attention_ws[key] = w4a16_tree_attention_workspace_size(max_q, Hq, c[2], D)
+        if need:
+            ws = workspace_for(q.device, stream, need)
+            wp, wb = ws.data_ptr(), ws.numel()
     st = (_calls or _bind()).tree_attention(*c, *qa, Hq, total, sp, B, max_q, lp, pp, cols, mp, softmax_scale, op, sep, code, wp, wb,
                                             stream)
     if st:
@@ -410,4 +424,4 @@ def w4a16_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = 
 
 
 __all__ = ["w4a16_rope_table", "w4a16_rope", "w4a16_kv_cache", "w4a16_kv_write", "w4a16_kv_read", "w4a16_tree_attention",
-           "w4a16_token_logprobs"]
+           "w4a16_tree_attention_workspace_size", "w4a16_token_logprobs"]

@@ -172,6 +172,17 @@ template <int ID, int THREADS>
 __device__ __forceinline__ void bar_sync() {
   asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
 }
+// The same barrier with a vote: whether any of its threads says so, one answer for all of them.
+template <int ID, int THREADS>
+__device__ __forceinline__ bool bar_any(bool vote) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(static_cast<uint32_t>(vote)), "n"(ID), "n"(THREADS)
+      : "memory");
+  return any != 0;
+}
 
 // Eight 4-bit codes as fp16 integers u - z in the order 0 4, 1 5, 2 6, 3 7 (lo = 1024 + z, hi = 64 + z, twice).
 __device__ __forceinline__ void decode4(uint32_t w, uint32_t lo, uint32_t hi, uint32_t (&x)[4]) {
@@ -734,9 +745,10 @@ __global__ void __launch_bounds__(L::kThreads, 1) tiles_kernel(const Params p) {
       tc_fence_after();
       row_s[grp * 128 + row] = m;
       row_s[256 + grp * 128 + row] = begun ? l : -1.f;  // (no tile: no sums either)
-      bar_sync<1, 256>();
+      // One answer for all threads of the softmax: the warps of the codes and of the MMAs, already at the next segment, may
+      // set the flag at any moment, and the barriers and tensor memory loads below are for all of these threads or for none.
+      const bool given_up = bar_any<1, 256>(!ok || ld_flag(abort_flag) != 0);
       tc_fence_after();
-      const bool given_up = ld_flag(abort_flag) != 0;
       if (given_up) ok = false;
       const float m0 = row_s[row], m1 = row_s[128 + row];
       const bool has0 = row_s[256 + row] != -1.f, has1 = row_s[384 + row] != -1.f;

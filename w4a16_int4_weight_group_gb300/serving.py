@@ -154,7 +154,9 @@ class _Ctypes:
 
 
 # The checks below use the cheapest tensor queries and read each once: the smallest calls take a few
-# microseconds, of which these are a part.
+# microseconds, of which these are a part. The library launches on the current device and looks its size and control
+# words up, so each function runs with its tensors' device as the current one.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _codes = {torch.float16: 0, torch.bfloat16: 1}
 _bits = {(4 * d * b + 128, d): b for d in (64, 128, 256) for b in (4, 8)}
 
@@ -232,6 +234,9 @@ def w4a16_rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, in
     """x [tokens, heads, head_dim] with its heads turned to `positions` (int64 [tokens]); `out` may be x itself."""
     shape = _three(x, "x")
     dev = _device(x)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return w4a16_rope(x, positions, table, interleaved, out)
     dtype = x.dtype
     code = _code(dtype)
     T, H, D = shape
@@ -256,6 +261,9 @@ def w4a16_kv_write(k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots:
     table, k turns first, and q [tokens, q_heads, head_dim], when given, is turned into the returned q_out."""
     shape = _three(k, "k")
     dev = _device(k)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return w4a16_kv_write(k, v, cache, slots, q, positions, table, interleaved, q_out)
     dtype = k.dtype
     code = _code(dtype)
     T, Hk, D = shape
@@ -293,6 +301,9 @@ def w4a16_kv_read(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype
                   v_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Keys and values [tokens, kv_heads, head_dim] of the given slots, dequantised to dtype (the one written)."""
     dev = _device(cache)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return w4a16_kv_read(cache, slots, head_dim, dtype, k_out, v_out)
     c = _cache_fields(cache, head_dim, dev)
     code = _code(dtype)
     if slots.dim() != 1:
@@ -343,6 +354,10 @@ def w4a16_tree_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch
     """
     shape = _three(q, "q")
     dev = _device(q)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return w4a16_tree_attention(q, cache, page_table, kv_lens, q_start, tree_mask, softmax_scale, max_q, out,
+                                        return_lse, workspace)
     dtype = q.dtype
     code = _code(dtype)
     total, Hq, D = shape
@@ -402,6 +417,9 @@ def w4a16_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor] = 
     if es != 1 and vocab > 1:
         raise ValueError("logits must be [rows, vocab] with contiguous rows")
     dev = _device(logits)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return w4a16_token_logprobs(logits, tokens, top_k)
     device = logits.device
     code = 2 if logits.dtype is torch.float32 else _code(logits.dtype)
     if tokens is None:

@@ -368,6 +368,13 @@ w4a16_status w4a16_tree_attention(const w4a16_kv_cache_t *cache, const void *q, 
                                   const int32_t *kv_lens, const int32_t *page_table, int64_t max_pages,
                                   const uint64_t *tree_mask, float softmax_scale, void *out, float *lse, w4a16_dtype dtype,
                                   void *workspace, size_t workspace_bytes, w4a16_stream_t stream);
+/* The same with NaN in the rows that w4a16_tree_attention does not write (query tokens past max_q of a sequence, rows that no
+ * sequence owns; q_start ascending): fill 1: of out, 2: of lse, 3: of both, 0: none. */
+w4a16_status w4a16_tree_attention_fill(const w4a16_kv_cache_t *cache, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                       int q_heads, int64_t total_q, const int32_t *q_start, int64_t batch, int max_q,
+                                       const int32_t *kv_lens, const int32_t *page_table, int64_t max_pages,
+                                       const uint64_t *tree_mask, float softmax_scale, void *out, float *lse, int fill, w4a16_dtype dtype,
+                                       void *workspace, size_t workspace_bytes, w4a16_stream_t stream);
 /* Bytes of workspace w4a16_tree_attention uses for these sizes on the current device. */
 size_t w4a16_tree_attention_workspace_size(int max_q, int q_heads, int kv_heads, int head_dim);
 

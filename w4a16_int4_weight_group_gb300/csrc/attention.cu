@@ -47,6 +47,7 @@ cudaError_t launch_tree_attention(const AttentionArgs &a, const DeviceInfo &dev)
   p.scale = a.scale;
   p.out = static_cast<uint16_t *>(a.out);
   p.lse = a.lse;
+  p.fill = a.q_start ? a.fill : 0;  // without q_start every row is a sequence's
   p.total_q = a.total_q;
   p.batch = static_cast<int>(a.batch);
   p.q_heads = a.q_heads;

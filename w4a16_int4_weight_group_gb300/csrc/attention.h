@@ -23,6 +23,7 @@ struct Params {
   float scale;
   uint16_t *out;
   float *lse;
+  int fill;  // outputs (1: out, 2: lse) whose rows that are not computed get NaN
   int64_t total_q;
   int batch, q_heads, kv_heads, group, page_tiles, max_q;
   int page_shift;  // log2 of page_tiles, or -1

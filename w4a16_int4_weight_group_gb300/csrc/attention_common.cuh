@@ -247,6 +247,36 @@ __device__ __forceinline__ bool share_of(const Params &p, int64_t *scan_s, volat
   return true;
 }
 
+// NaN into the rows that are not computed, where the caller asks for it: those of a sequence past its first max_q (a CTA
+// for each sequence, from the last one on: in small calls these have no share), those before the first sequence and after
+// the last, and those of a sequence whose ends are no rows of q. One look at two words a sequence where there are none.
+// (At the start: behind the loops over the cache it adds up to 70 bytes of spills to those.)
+template <int D, int THREADS>
+__device__ __forceinline__ void fill_unowned(const Params &p, int tid) {
+  if (!p.fill) return;
+  auto nan_rows = [&](int64_t from, int64_t to) {
+    from = from > 0 ? from : 0;
+    to = to < p.total_q ? to : p.total_q;
+    if (from >= to) return;
+    const int64_t each = int64_t(p.q_heads) * (D / 8);  // 16-byte vectors of a row
+    if (p.fill & 1)
+      for (int64_t i = from * each + tid; i < to * each; i += THREADS)
+        reinterpret_cast<uint4 *>(p.out)[i] = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+    if ((p.fill & 2) && p.lse)
+      for (int64_t i = from * p.q_heads + tid; i < to * p.q_heads; i += THREADS) p.lse[i] = __int_as_float(0x7FFFFFFF);
+  };
+  for (int64_t b = gridDim.x - 1 - blockIdx.x; b <= p.batch; b += gridDim.x) {
+    if (b == p.batch) {
+      nan_rows(0, p.q_start[0]);
+      nan_rows(p.q_start[b], p.total_q);
+    } else {
+      const int64_t q0 = p.q_start[b], q1 = p.q_start[b + 1];
+      const bool valid = q0 >= 0 && q0 <= q1 && q1 <= p.total_q;
+      nan_rows(valid ? q0 + (q1 - q0 < p.max_q ? q1 - q0 : p.max_q) : q0, q1);
+    }
+  }
+}
+
 // Barrier of THREADS threads: the CTA's own (BAR 0) or a named one.
 template <int BAR, int THREADS>
 __device__ __forceinline__ void sync_threads() {

@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
   const uint64_t limit_ns = lim ? lim : kDefaultWaitNs;
   unsigned int *error = &p.control->error;
 
+  fill_unowned<D, L::kThreads>(p, tid);
   Cursor cur;
   Shares sh;
   int64_t u1, units;

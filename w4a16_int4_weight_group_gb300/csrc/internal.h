@@ -172,6 +172,7 @@ struct AttentionArgs {
   float scale;
   void *out;   // [total_q, q_heads, head_dim]
   float *lse;  // [total_q, q_heads] or null
+  int fill;    // 1 (out), 2 (lse): NaN for the rows that are not computed
   int dtype;
   void *workspace;
   size_t workspace_bytes;

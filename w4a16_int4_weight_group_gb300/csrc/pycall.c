@@ -13,7 +13,7 @@
  *
  *   bind_capture(address), capture_id(stream) -> int  w4a16_stream_capture_id
  *
- *   bind_serving(rope, kv_write, kv_read, tree_attention, token_logprobs)   addresses of the five
+ *   bind_serving(rope, kv_write, kv_read, tree_attention_fill, token_logprobs)   addresses of the five
  *   rope, kv_write, kv_read, tree_attention, token_logprobs -> status (int): flat arguments, the fields of
  *     w4a16_rope_t (positions, table, table_rows, rot_dim, interleaved; positions 0: no rope) and of
  *     w4a16_kv_cache_t (data, num_pages, kv_heads, head_dim, page_size, bits) in the place of the structures.
@@ -117,7 +117,7 @@ static w4a16_status (*g_kv_write)(const w4a16_kv_cache_t *, const void *, int64_
 static w4a16_status (*g_kv_read)(const w4a16_kv_cache_t *, const int64_t *, int64_t, void *, void *, w4a16_dtype, w4a16_stream_t);
 static w4a16_status (*g_tree_attention)(const w4a16_kv_cache_t *, const void *, int64_t, int64_t, int, int64_t, const int32_t *, int64_t,
                                         int, const int32_t *, const int32_t *, int64_t, const uint64_t *, float, void *, float *,
-                                        w4a16_dtype, void *, size_t, w4a16_stream_t);
+                                        int, w4a16_dtype, void *, size_t, w4a16_stream_t);
 static w4a16_status (*g_token_logprobs)(const void *, int64_t, int64_t, int64_t, w4a16_dtype, const int64_t *, int, int, float *,
                                         float *, int64_t *, float *, w4a16_stream_t);
 
@@ -179,15 +179,15 @@ static PyObject *kv_read(PyObject *self, PyObject *const *args, Py_ssize_t nargs
   return PyLong_FromLong(g_kv_read(&c, PTR(6), v[7], PTR(8), PTR(9), (w4a16_dtype)v[10], PTR(11)));
 }
 /* cache[6], q, strides[2], q_heads, total_q, q_start, batch, max_q, kv_lens, page_table, max_pages, tree_mask, scale, out,
- * lse, dtype, workspace, bytes, stream */
+ * lse, fill, dtype, workspace, bytes, stream */
 static PyObject *tree_attention(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
   (void)self;
-  int64_t v[25];
+  int64_t v[26];
   double scale = 0.0;
-  if (unbound(*(void **)&g_tree_attention) || take("tree_attention", args, nargs, 25, 18, v, &scale)) return NULL;
+  if (unbound(*(void **)&g_tree_attention) || take("tree_attention", args, nargs, 26, 18, v, &scale)) return NULL;
   const w4a16_kv_cache_t c = cache_at(v);
   const int st = g_tree_attention(&c, PTR(6), v[7], v[8], I32(9), v[10], PTR(11), v[12], I32(13), PTR(14), PTR(15), v[16], PTR(17),
-                                  (float)scale, PTR(19), PTR(20), (w4a16_dtype)v[21], PTR(22), (size_t)v[23], PTR(24));
+                                  (float)scale, PTR(19), PTR(20), I32(21), (w4a16_dtype)v[22], PTR(23), (size_t)v[24], PTR(25));
   return PyLong_FromLong(st);
 }
 /* logits, row_stride, rows, vocab, dtype, tokens, n_tokens, top_k, logprobs, entropy, top_ids, top_logprobs, stream */
@@ -207,11 +207,11 @@ static PyMethodDef kMethods[] = {
      "layer_gemm(layer, a, out, m, ws, ws_bytes, stream) -> status"},
     {"bind_capture", (PyCFunction)bind_capture, METH_O, "bind_capture(address of w4a16_stream_capture_id)"},
     {"capture_id", (PyCFunction)capture_id, METH_O, "capture_id(stream) -> number of its capture, 0 for none"},
-    {"bind_serving", FAST(bind_serving), "bind_serving(rope, kv_write, kv_read, tree_attention, token_logprobs)"},
+    {"bind_serving", FAST(bind_serving), "bind_serving(rope, kv_write, kv_read, tree_attention_fill, token_logprobs)"},
     {"rope", FAST(rope), "w4a16_rope, flat arguments -> status"},
     {"kv_write", FAST(kv_write), "w4a16_kv_write, flat arguments -> status"},
     {"kv_read", FAST(kv_read), "w4a16_kv_read, flat arguments -> status"},
-    {"tree_attention", FAST(tree_attention), "w4a16_tree_attention, flat arguments -> status"},
+    {"tree_attention", FAST(tree_attention), "w4a16_tree_attention_fill, flat arguments -> status"},
     {"token_logprobs", FAST(token_logprobs), "w4a16_token_logprobs, flat arguments -> status"},
     {NULL, NULL, 0, NULL},
 };

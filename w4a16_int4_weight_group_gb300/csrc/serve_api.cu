@@ -172,6 +172,15 @@ w4a16_status w4a16_tree_attention(const w4a16_kv_cache_t *cache, const void *q, 
                                   const int32_t *kv_lens, const int32_t *page_table, int64_t max_pages,
                                   const uint64_t *tree_mask, float softmax_scale, void *out, float *lse, w4a16_dtype dtype,
                                   void *workspace, size_t workspace_bytes, w4a16_stream_t stream) {
+  return w4a16_tree_attention_fill(cache, q, q_token_stride, q_head_stride, q_heads, total_q, q_start, batch, max_q, kv_lens, page_table,
+                                   max_pages, tree_mask, softmax_scale, out, lse, 0, dtype, workspace, workspace_bytes, stream);
+}
+
+w4a16_status w4a16_tree_attention_fill(const w4a16_kv_cache_t *cache, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                       int q_heads, int64_t total_q, const int32_t *q_start, int64_t batch, int max_q,
+                                       const int32_t *kv_lens, const int32_t *page_table, int64_t max_pages,
+                                       const uint64_t *tree_mask, float softmax_scale, void *out, float *lse, int fill, w4a16_dtype dtype,
+                                       void *workspace, size_t workspace_bytes, w4a16_stream_t stream) {
   w4a16_status st = check_cache(cache, dtype);
   if (st != W4A16_OK) return st;
   if (batch < 0 || batch > (1 << 20) || total_q < 0 || total_q >= kMaxTokens)
@@ -187,7 +196,15 @@ w4a16_status w4a16_tree_attention(const w4a16_kv_cache_t *cache, const void *q, 
   if (!q_start && total_q != batch)
     return fail(W4A16_ERR_INVALID_ARG, "without q_start there is one query token for each sequence: total_q (%lld), batch (%lld)",
                 (long long)total_q, (long long)batch);
-  if (batch == 0 || total_q == 0) return ok();
+  if (fill < 0 || fill > 3) return fail(W4A16_ERR_INVALID_ARG, "fill (%d) must be in [0, 3]", fill);
+  if (total_q == 0) return ok();
+  if (batch == 0) {  // no row is a sequence's: all bits set are a NaN of every dtype
+    cudaError_t e = cudaSuccess;
+    if ((fill & 1) && out) e = cudaMemsetAsync(out, 0xFF, static_cast<size_t>(total_q) * q_heads * cache->head_dim * 2, reinterpret_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess && (fill & 2) && lse)
+      e = cudaMemsetAsync(lse, 0xFF, static_cast<size_t>(total_q) * q_heads * 4, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ok() : cuda_fail(e, "w4a16_tree_attention fill");
+  }
   if (!kv_lens || (!page_table && max_pages > 0) || !out)
     return fail(W4A16_ERR_INVALID_ARG, "kv_lens, page_table and out must not be NULL");
   const int D = cache->head_dim;
@@ -212,7 +229,7 @@ w4a16_status w4a16_tree_attention(const w4a16_kv_cache_t *cache, const void *q, 
   cudaError_t e = current_device_info(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "device query");
   AttentionArgs a{*cache, qv, q_heads, total_q, q_start, batch, max_q, kv_lens, page_table, max_pages, tree_mask, softmax_scale,
-                  out, lse, static_cast<int>(dtype), workspace, workspace ? workspace_bytes : 0,
+                  out, lse, fill, static_cast<int>(dtype), workspace, workspace ? workspace_bytes : 0,
                   reinterpret_cast<cudaStream_t>(stream)};
   e = launch_tree_attention(a, dev);
   if (e != cudaSuccess) return cuda_fail(e, "w4a16_tree_attention launch");

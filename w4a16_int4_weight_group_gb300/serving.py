@@ -46,6 +46,8 @@ SIGNATURES = [
     ("w4a16_kv_read", ctypes.c_int, [_pc, _vp, _i64, _vp, _vp, ctypes.c_int, _vp]),
     ("w4a16_tree_attention", ctypes.c_int, [_pc, _vp, _i64, _i64, ctypes.c_int, _i64, _vp, _i64, ctypes.c_int, _vp, _vp,
                                             _i64, _vp, _f32, _vp, _vp, ctypes.c_int, _vp, ctypes.c_size_t, _vp]),
+    ("w4a16_tree_attention_fill", ctypes.c_int, [_pc, _vp, _i64, _i64, ctypes.c_int, _i64, _vp, _i64, ctypes.c_int, _vp, _vp,
+                                                 _i64, _vp, _f32, _vp, _vp, ctypes.c_int, ctypes.c_int, _vp, ctypes.c_size_t, _vp]),
     ("w4a16_tree_attention_workspace_size", ctypes.c_size_t, [ctypes.c_int] * 4),
     ("w4a16_token_logprobs", ctypes.c_int, [_vp, _i64, _i64, _i64, ctypes.c_int, _vp, ctypes.c_int, ctypes.c_int, _vp, _vp,
                                             _vp, _vp, _vp]),
@@ -121,7 +123,7 @@ def _bind():
         m = None
     if m is not None and hasattr(m, "bind_serving"):
         m.bind_serving(*(ctypes.cast(getattr(L, "w4a16_" + n), _vp).value
-                         for n in ("rope", "kv_write", "kv_read", "tree_attention", "token_logprobs")))
+                         for n in ("rope", "kv_write", "kv_read", "tree_attention_fill", "token_logprobs")))
         _calls = m
     else:
         _calls = _Ctypes()
@@ -146,7 +148,7 @@ class _Ctypes:
 
     @staticmethod
     def tree_attention(*a):
-        return lib().w4a16_tree_attention(ctypes.byref(KVCache(*a[:6])), *a[6:])
+        return lib().w4a16_tree_attention_fill(ctypes.byref(KVCache(*a[:6])), *a[6:])
 
     @staticmethod
     def token_logprobs(*a):
@@ -346,7 +348,9 @@ def w4a16_tree_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch
     [batch + 1] (None: one query token for each sequence); tree_mask int64 [total_q] (bit j: sees query token j of
     its own sequence; None: a chain); softmax_scale: head_dim ** -0.5 unless given; max_q: the most query tokens of
     a sequence, at most 64 (unless given: min(total_q, 64), 1 without q_start). Returns out, or (out, lse) with lse
-    float32 [total_q, q_heads]. A query that sees nothing gives zeros and -inf.
+    float32 [total_q, q_heads]. A query that sees nothing gives zeros and -inf. Query tokens of a sequence past its first
+    max_q, and rows that no sequence owns (before q_start[0], from q_start[batch] on), are not computed: NaN in the tensors that this
+    call makes, unchanged in a given `out`.
 
     workspace: contiguous uint8 [bytes] of the caller's own, its first 4 KiB zero before its first use, for calls of
     one stream (or one graph) at a time; with fewer bytes than w4a16_tree_attention_workspace_size no sequence is split
@@ -375,15 +379,18 @@ def w4a16_tree_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch
         max_q = 1 if q_start is None else max(1, min(total, 64))
     if softmax_scale is None:
         softmax_scale = D ** -0.5
+    fill = 0  # outputs made here have no row that holds whatever was in the memory before
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=q.device)
         op = out.data_ptr()
+        fill = 1
     else:
         op = _index(out, "out", dtype, shape, dev)
     lse, sep = None, 0
     if return_lse:
         lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
         sep = lse.data_ptr()
+        fill |= 2
     stream = _current_stream(dev)
     wp = wb = 0
     if workspace is not None:
@@ -397,8 +404,8 @@ def w4a16_tree_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch
         if need:
             ws = workspace_for(q.device, stream, need)
             wp, wb = ws.data_ptr(), ws.numel()
-    st = (_calls or _bind()).tree_attention(*c, *qa, Hq, total, sp, B, max_q, lp, pp, cols, mp, softmax_scale, op, sep, code, wp, wb,
-                                            stream)
+    st = (_calls or _bind()).tree_attention(*c, *qa, Hq, total, sp, B, max_q, lp, pp, cols, mp, softmax_scale, op, sep, fill,
+                                            code, wp, wb, stream)
     if st:
         _check(st)
     return (out, lse) if return_lse else out

@@ -52,6 +52,7 @@ __device__ __forceinline__ unsigned int add_acq_rel(unsigned int *p, unsigned in
   return old;
 }
 
+// Cached tokens of a sequence: its length, at least zero, at most what its row of the page table holds.
 __device__ __forceinline__ int length_of(const Params &p, int b) {
   const int64_t cap = p.max_pages * p.page_tiles * 16;
   const int len = p.kv_lens[b];

@@ -345,9 +345,10 @@ def w4a16_tree_attention(q: torch.Tensor, cache: torch.Tensor, page_table: torch
     """softmax(scale q k^T) v of each sequence's query tokens over its cached tokens, the query tokens among them.
 
     q [total_q, q_heads, head_dim]; page_table int32 [batch, max_pages]; kv_lens int32 [batch]; q_start int32
-    [batch + 1] (None: one query token for each sequence); tree_mask int64 [total_q] (bit j: sees query token j of
+    [batch + 1], ascending (None: one query token for each sequence); tree_mask int64 [total_q] (bit j: sees query token j of
     its own sequence; None: a chain); softmax_scale: head_dim ** -0.5 unless given; max_q: the most query tokens of
-    a sequence, at most 64 (unless given: min(total_q, 64), 1 without q_start). Returns out, or (out, lse) with lse
+    a sequence, at most 64 (unless given: min(total_q, 64), 1 without q_start). A length in kv_lens that is past the
+    page table counts as the table's end: the query tokens are then its last tokens. Returns out, or (out, lse) with lse
     float32 [total_q, q_heads]. A query that sees nothing gives zeros and -inf. Query tokens of a sequence past its first
     max_q, and rows that no sequence owns (before q_start[0], from q_start[batch] on), are not computed: NaN in the tensors that this
     call makes, unchanged in a given `out`.

@@ -346,7 +346,7 @@ w4a16_status w4a16_kv_read(const w4a16_kv_cache_t *cache, const int64_t *slots, 
  *               max_q (<= 64) of them; NULL: one for each sequence (total_q == batch)
  *   kv_lens     int32 [batch]: cached tokens of each sequence, its query tokens (already written) the last of them. A
  *               negative length counts as zero, one past max_pages pages as max_pages * page_size (the query tokens are
- *               then the last ones of these pages)
+ *               then the last ones of these pages), one past 2^31 - 256 as that
  *   page_table  int32 [batch, max_pages]: pages of each sequence; tokens of a page outside the cache are not seen
  *   tree_mask   uint64 [total_q]: bit j of a query token's word: it sees the j-th query token of its own
  *               sequence (set its own bit too); NULL: a chain (it sees those up to itself). Cached tokens before

@@ -52,11 +52,13 @@ __device__ __forceinline__ unsigned int add_acq_rel(unsigned int *p, unsigned in
   return old;
 }
 
-// Cached tokens of a sequence: its length, at least zero, at most what its row of the page table holds.
+// Cached tokens of a sequence: its length, at least zero, at most what its row of the page table holds, and at most
+// 2^31 - 256, so that the positions of its last unit (64 to 256 tokens) are still 32-bit numbers.
+constexpr int kMaxLength = 0x7FFFFF00;
 __device__ __forceinline__ int length_of(const Params &p, int b) {
-  const int64_t cap = p.max_pages * p.page_tiles * 16;
+  const int64_t pages = p.max_pages * p.page_tiles * 16;
   const int len = p.kv_lens[b];
-  return len < 0 ? 0 : static_cast<int>(min(int64_t(len), cap));
+  return len < 0 ? 0 : static_cast<int>(min(int64_t(min(len, kMaxLength)), pages));
 }
 __device__ __forceinline__ Queries queries_of(const Params &p, int b, int len) {
   const int64_t q0 = p.q_start ? p.q_start[b] : b, q1 = p.q_start ? p.q_start[b + 1] : b + 1;

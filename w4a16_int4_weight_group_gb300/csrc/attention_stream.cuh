@@ -78,6 +78,7 @@ struct StreamLayout {
   static constexpr int kOffMisc = kOffBar + 8 * (W * S + 1);  // abort flag, start, scan, split segments to join
   static constexpr int kSmem = kOffMisc + 32 + 8 * W + sizeof(Pending);
   static_assert(S >= 2, "a ring of two stages at least");
+  static_assert(kUnit <= 256, "positions past the longest sequence's end");
   static_assert(kSmem <= kBudget, "shared memory");
   static_assert(MB * R * kPad >= kThreads + 64 * R, "scratch of the joining of parts");
   static_assert(kOffRing % 128 == 0 && kOffO % 16 == 0 && kTile % 128 == 0, "alignment");

@@ -268,7 +268,8 @@ w4a16_status w4a16_layer_destroy(w4a16_layer_t layer);
  * Serving operators next to the linear layer: what a model's step runs between its W4A16 projections
  * and after its last one, with one to 64 drafted tokens for each sequence (one: plain decoding).
  *
- * Strides are in elements; the last dimension of a strided tensor is contiguous. All of them are
+ * Strides are in elements (the stride of a dimension of one element does not count); the last dimension of a
+ * strided tensor is contiguous. All of them are
  * stream-ordered, allocate nothing, do not synchronise and can be captured; validation happens before any
  * launch. Index tensors are read on the device: an index out of range never leads to an access out of
  * range, each function says what it does instead.

@@ -35,3 +35,37 @@ def test_fill_of_the_attention(w, s):
     assert call(-1) == 1
     assert call(3, total=0) == 0 and call(0, B=0) == 0 and call(2, B=0) == 0  # nothing to fill
     assert w.w4a16_debug_launch_count() == before
+
+
+def test_strides_of_single_tokens_and_heads_do_not_count(w, s):
+    """Calls that pass these checks are stopped by a later one (an overlap, a NULL), so that nothing is launched."""
+    L, before = w.lib(), w.w4a16_debug_launch_count()
+    r = s.Rope(0x1000, 0x2000, 100, 128, 0)
+
+    def rope(T, H, xt, xh, ot=128, oh=128):  # the table lies inside of out: refused last
+        return L.w4a16_rope(ctypes.byref(r), vp(0x100000), xt, xh, vp(0x1F00), ot, oh, T, H, 128, 1, None)
+
+    for strides in ((3, 128), (0, 128), (-5, 128), (128, 7), (128, 0), (128, -7)):
+        T, H = (1, 2) if strides[1] == 128 else (2, 1)
+        assert rope(T, H, *strides) == 1 and "the table" in w.last_error(), strides
+        assert rope(T, H, 256, 128, *strides) == 1 and "the table" in w.last_error(), strides
+    assert rope(1, 2, 256, 7) == 1 and "do not hold" in w.last_error()
+    assert rope(2, 1, -1, 128) == 1 and "do not hold" in w.last_error()
+    c1 = s.KVCache(0x10000000, 4, 1, 128, 16, 4)
+
+    def write(T, kt, kh, vt, vh, qt, qh, Hq):  # q_out NULL: refused last
+        return L.w4a16_kv_write(ctypes.byref(c1), vp(0x100000), kt, kh, vp(0x200000), vt, vh, vp(0x3000), T, ctypes.byref(r), vp(0x400000), qt, qh,
+                                Hq, None, 1, None)
+
+    assert write(4, 128, 129, 128, 3, 128, 5, 1) == 1 and "q_out must not be NULL" in w.last_error()
+    assert write(1, 129, 128, 3, -1, 257, 128, 2) == 1 and "q_out must not be NULL" in w.last_error()
+    assert write(4, 129, 128, 128, 128, 128, 128, 1) == 3 and write(4, 128, 128, 128, 128, 256, 129, 2) == 3
+
+    def attend(total, qt, qh, Hq):  # out overlaps q: refused last
+        return L.w4a16_tree_attention(ctypes.byref(c1), vp(0x100000), qt, qh, Hq, total, vp(0x9000), 2, 2, vp(0xA000), vp(0xB000), 5, None, 0.1,
+                                      vp(0x100000), None, 1, None, 0, None)
+
+    assert attend(3, 128, 33, 1) == 1 and "overlaps" in w.last_error()
+    assert attend(1, 33, 128, 2) == 1 and "overlaps" in w.last_error()
+    assert attend(3, 33, 128, 2) == 3 and attend(3, 256, 129, 2) == 3
+    assert w.w4a16_debug_launch_count() == before

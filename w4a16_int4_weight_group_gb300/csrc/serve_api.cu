@@ -46,6 +46,11 @@ Range view_range(const HeadsView &v, int64_t tokens, int heads, int head_dim) {
   return range(v.ptr, last * 2);
 }
 
+// A strided tensor as the kernels get it: a dimension of one element has no stride that counts.
+HeadsView view(const void *ptr, int64_t token_stride, int64_t head_stride, int64_t tokens, int heads) {
+  return HeadsView{ptr, tokens == 1 ? 0 : token_stride, heads == 1 ? 0 : head_stride};
+}
+
 w4a16_status check_view(const HeadsView &v, int64_t tokens, int heads, int head_dim, const char *name, bool vectors) {
   if (!v.ptr) return fail(W4A16_ERR_INVALID_ARG, "%s must not be NULL", name);
   if ((heads > 1 && v.head_stride < head_dim) || (tokens > 1 && v.token_stride < 1) || v.head_stride < 0 || v.token_stride < 0)
@@ -90,10 +95,10 @@ w4a16_status w4a16_rope(const w4a16_rope_t *rope, const void *x, int64_t x_token
   if (tokens == 0 || heads == 0) return ok();
   RopeArgs ra;
   if ((st = check_rope(rope, head_dim, &ra)) != W4A16_OK) return st;
-  const HeadsView xv{x, x_token_stride, x_head_stride}, ov{out, out_token_stride, out_head_stride};
+  const HeadsView xv = view(x, x_token_stride, x_head_stride, tokens, heads), ov = view(out, out_token_stride, out_head_stride, tokens, heads);
   if ((st = check_view(xv, tokens, heads, head_dim, "x", false)) != W4A16_OK) return st;
   if ((st = check_view(ov, tokens, heads, head_dim, "out", false)) != W4A16_OK) return st;
-  if (x == out ? (x_token_stride != out_token_stride || x_head_stride != out_head_stride)
+  if (x == out ? (xv.token_stride != ov.token_stride || xv.head_stride != ov.head_stride)
                : overlaps(view_range(xv, tokens, heads, head_dim), view_range(ov, tokens, heads, head_dim)))
     return fail(W4A16_ERR_INVALID_ARG, "out overlaps x (in place: the same pointer and strides)");
   const Range o = view_range(ov, tokens, heads, head_dim);
@@ -115,7 +120,8 @@ w4a16_status w4a16_kv_write(const w4a16_kv_cache_t *cache, const void *k, int64_
   const int D = cache->head_dim;
   if (!slots) return fail(W4A16_ERR_INVALID_ARG, "slots must not be NULL");
   if (!aligned(slots, 8)) return fail(W4A16_ERR_MISALIGNED, "slots must be 8-byte aligned");
-  const HeadsView kv{k, k_token_stride, k_head_stride}, vv{v, v_token_stride, v_head_stride};
+  const HeadsView kv = view(k, k_token_stride, k_head_stride, tokens, cache->kv_heads);
+  const HeadsView vv = view(v, v_token_stride, v_head_stride, tokens, cache->kv_heads);
   HeadsView qv{nullptr, 0, 0};
   if ((st = check_view(kv, tokens, cache->kv_heads, D, "k", true)) != W4A16_OK) return st;
   if ((st = check_view(vv, tokens, cache->kv_heads, D, "v", true)) != W4A16_OK) return st;
@@ -131,7 +137,7 @@ w4a16_status w4a16_kv_write(const w4a16_kv_cache_t *cache, const void *k, int64_
   if (q) {
     if (!rope) return fail(W4A16_ERR_INVALID_ARG, "q is only taken with rope (it is turned, not cached)");
     if (q_heads <= 0 || q_heads > kMaxHeads) return fail(W4A16_ERR_INVALID_ARG, "q_heads (%d) must be in [1, %d]", q_heads, kMaxHeads);
-    qv = HeadsView{q, q_token_stride, q_head_stride};
+    qv = view(q, q_token_stride, q_head_stride, tokens, q_heads);
     if ((st = check_view(qv, tokens, q_heads, D, "q", true)) != W4A16_OK) return st;
     const HeadsView qo{q_out, int64_t(q_heads) * D, D};
     if ((st = check_view(qo, tokens, q_heads, D, "q_out", true)) != W4A16_OK) return st;
@@ -208,7 +214,7 @@ w4a16_status w4a16_tree_attention_fill(const w4a16_kv_cache_t *cache, const void
   if (!kv_lens || (!page_table && max_pages > 0) || !out)
     return fail(W4A16_ERR_INVALID_ARG, "kv_lens, page_table and out must not be NULL");
   const int D = cache->head_dim;
-  const HeadsView qv{q, q_token_stride, q_head_stride};
+  const HeadsView qv = view(q, q_token_stride, q_head_stride, total_q, q_heads);
   if ((st = check_view(qv, total_q, q_heads, D, "q", true)) != W4A16_OK) return st;
   if (!aligned(kv_lens, 4) || !aligned(page_table, 4) || !aligned(q_start, 4) || !aligned(tree_mask, 8) || !aligned(lse, 4) ||
       !aligned(out, 16))

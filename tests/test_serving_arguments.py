@@ -1,5 +1,9 @@
 """Host-side checks of the serving operators' arguments, past those of test_serving_cpu.py (no GPU)."""
 import ctypes
+import shutil
+import subprocess
+import threading
+import time
 
 import pytest
 
@@ -69,3 +73,33 @@ def test_strides_of_single_tokens_and_heads_do_not_count(w, s):
     assert attend(1, 33, 128, 2) == 1 and "overlaps" in w.last_error()
     assert attend(3, 33, 128, 2) == 3 and attend(3, 256, 129, 2) == 3
     assert w.w4a16_debug_launch_count() == before
+
+
+@pytest.mark.parametrize("name,count", [("rope", 16), ("kv_write", 26), ("kv_read", 12), ("tree_attention", 26), ("token_logprobs", 13)])
+def test_calls_leave_the_gil_to_other_threads(w, s, tmp_path, name, count):
+    """The marshalling module's calls of a function that takes a third of a second, while another thread counts."""
+    mod = pytest.importorskip("w4a16_int4_weight_group_gb300._w4a16_call")
+    cc = shutil.which("cc") or shutil.which("gcc")
+    if not cc:
+        pytest.skip("no C compiler")
+    (tmp_path / "slow.c").write_text("#include <time.h>\nint slow(void) { struct timespec t = {0, 300000000}; return nanosleep(&t, 0); }\n")
+    subprocess.run([cc, "-shared", "-fPIC", str(tmp_path / "slow.c"), "-o", str(tmp_path / "slow.so")], check=True)
+    slow = ctypes.cast(ctypes.CDLL(str(tmp_path / "slow.so")).slow, ctypes.c_void_p).value
+    ticks, stop = [], threading.Event()
+
+    def tick():
+        while not stop.wait(0.01):
+            ticks.append(time.monotonic())
+
+    thread = threading.Thread(target=tick)
+    mod.bind_serving(*[slow] * 5)
+    try:
+        thread.start()
+        t0 = time.monotonic()
+        assert getattr(mod, name)(*[0] * count) == 0
+        t1 = time.monotonic()
+    finally:
+        stop.set()
+        thread.join()
+        s._bind()  # the library's own functions again
+    assert t1 - t0 >= 0.29 and sum(t0 + 0.02 < t < t1 - 0.02 for t in ticks) >= 5

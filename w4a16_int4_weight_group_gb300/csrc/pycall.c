@@ -16,7 +16,8 @@
  *   bind_serving(rope, kv_write, kv_read, tree_attention_fill, token_logprobs)   addresses of the five
  *   rope, kv_write, kv_read, tree_attention, token_logprobs -> status (int): flat arguments, the fields of
  *     w4a16_rope_t (positions, table, table_rows, rot_dim, interleaved; positions 0: no rope) and of
- *     w4a16_kv_cache_t (data, num_pages, kv_heads, head_dim, page_size, bits) in the place of the structures.
+ *     w4a16_kv_cache_t (data, num_pages, kv_heads, head_dim, page_size, bits) in the place of the structures. The GIL is
+ *     released around each: a launch waits while the stream's queue is full.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -156,7 +157,10 @@ static PyObject *rope(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
   int64_t v[16];
   if (unbound(*(void **)&g_rope) || take("rope", args, nargs, 16, -1, v, NULL)) return NULL;
   const w4a16_rope_t r = rope_at(v);
-  const int st = g_rope(&r, PTR(5), v[6], v[7], PTR(8), v[9], v[10], v[11], I32(12), I32(13), (w4a16_dtype)v[14], PTR(15));
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g_rope(&r, PTR(5), v[6], v[7], PTR(8), v[9], v[10], v[11], I32(12), I32(13), (w4a16_dtype)v[14], PTR(15));
+  Py_END_ALLOW_THREADS
   return PyLong_FromLong(st);
 }
 /* cache[6], k, strides[2], v, strides[2], slots, tokens, rope[5], q, strides[2], q_heads, q_out, dtype, stream */
@@ -166,8 +170,11 @@ static PyObject *kv_write(PyObject *self, PyObject *const *args, Py_ssize_t narg
   if (unbound(*(void **)&g_kv_write) || take("kv_write", args, nargs, 26, -1, v, NULL)) return NULL;
   const w4a16_kv_cache_t c = cache_at(v);
   const w4a16_rope_t r = rope_at(v + 14);
-  const int st = g_kv_write(&c, PTR(6), v[7], v[8], PTR(9), v[10], v[11], PTR(12), v[13], v[14] ? &r : NULL, PTR(19), v[20], v[21],
-                            I32(22), PTR(23), (w4a16_dtype)v[24], PTR(25));
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g_kv_write(&c, PTR(6), v[7], v[8], PTR(9), v[10], v[11], PTR(12), v[13], v[14] ? &r : NULL, PTR(19), v[20], v[21], I32(22),
+                  PTR(23), (w4a16_dtype)v[24], PTR(25));
+  Py_END_ALLOW_THREADS
   return PyLong_FromLong(st);
 }
 /* cache[6], slots, tokens, k_out, v_out, dtype, stream */
@@ -176,7 +183,11 @@ static PyObject *kv_read(PyObject *self, PyObject *const *args, Py_ssize_t nargs
   int64_t v[12];
   if (unbound(*(void **)&g_kv_read) || take("kv_read", args, nargs, 12, -1, v, NULL)) return NULL;
   const w4a16_kv_cache_t c = cache_at(v);
-  return PyLong_FromLong(g_kv_read(&c, PTR(6), v[7], PTR(8), PTR(9), (w4a16_dtype)v[10], PTR(11)));
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g_kv_read(&c, PTR(6), v[7], PTR(8), PTR(9), (w4a16_dtype)v[10], PTR(11));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
 }
 /* cache[6], q, strides[2], q_heads, total_q, q_start, batch, max_q, kv_lens, page_table, max_pages, tree_mask, scale, out,
  * lse, fill, dtype, workspace, bytes, stream */
@@ -186,8 +197,11 @@ static PyObject *tree_attention(PyObject *self, PyObject *const *args, Py_ssize_
   double scale = 0.0;
   if (unbound(*(void **)&g_tree_attention) || take("tree_attention", args, nargs, 26, 18, v, &scale)) return NULL;
   const w4a16_kv_cache_t c = cache_at(v);
-  const int st = g_tree_attention(&c, PTR(6), v[7], v[8], I32(9), v[10], PTR(11), v[12], I32(13), PTR(14), PTR(15), v[16], PTR(17),
-                                  (float)scale, PTR(19), PTR(20), I32(21), (w4a16_dtype)v[22], PTR(23), (size_t)v[24], PTR(25));
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g_tree_attention(&c, PTR(6), v[7], v[8], I32(9), v[10], PTR(11), v[12], I32(13), PTR(14), PTR(15), v[16], PTR(17), (float)scale,
+                        PTR(19), PTR(20), I32(21), (w4a16_dtype)v[22], PTR(23), (size_t)v[24], PTR(25));
+  Py_END_ALLOW_THREADS
   return PyLong_FromLong(st);
 }
 /* logits, row_stride, rows, vocab, dtype, tokens, n_tokens, top_k, logprobs, entropy, top_ids, top_logprobs, stream */
@@ -195,8 +209,10 @@ static PyObject *token_logprobs(PyObject *self, PyObject *const *args, Py_ssize_
   (void)self;
   int64_t v[13];
   if (unbound(*(void **)&g_token_logprobs) || take("token_logprobs", args, nargs, 13, -1, v, NULL)) return NULL;
-  const int st = g_token_logprobs(PTR(0), v[1], v[2], v[3], (w4a16_dtype)v[4], PTR(5), I32(6), I32(7), PTR(8), PTR(9), PTR(10), PTR(11),
-                                  PTR(12));
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g_token_logprobs(PTR(0), v[1], v[2], v[3], (w4a16_dtype)v[4], PTR(5), I32(6), I32(7), PTR(8), PTR(9), PTR(10), PTR(11), PTR(12));
+  Py_END_ALLOW_THREADS
   return PyLong_FromLong(st);
 }
 

@@ -103,3 +103,35 @@ def test_calls_leave_the_gil_to_other_threads(w, s, tmp_path, name, count):
         thread.join()
         s._bind()  # the library's own functions again
     assert t1 - t0 >= 0.29 and sum(t0 + 0.02 < t < t1 - 0.02 for t in ticks) >= 5
+
+
+@pytest.mark.parametrize("through", ["module", "ctypes"])
+def test_sizes_past_32_bits_are_refused_not_cut(w, s, through):
+    """2^32 + n is not n: every size that is a C int, with otherwise valid arguments that only an overlap would refuse."""
+    if through == "module":
+        pytest.importorskip("w4a16_int4_weight_group_gb300._w4a16_call")
+        calls = s._bind()
+    else:
+        calls = s._Ctypes()
+    before, big = w.w4a16_debug_launch_count(), 1 << 32
+    cache = [0x10000000, 4, 2, 128, 16, 4]
+    # arguments, the places of C ints, and what the call says when only the overlap is wrong
+    cases = {
+        "rope": ([0x1000, 0x1F00, 100, 128, 0, 0x100000, 256, 128, 0x1F00, 256, 128, 4, 2, 128, 1, 0], (3, 12, 13, 14), "the table"),
+        "kv_write": (cache + [0x10000000, 256, 128, 0x200000, 256, 128, 0x3000, 4, 0x1000, 0x2000, 100, 128, 0, 0, 0, 0, 0, 0, 1, 0],
+                     (2, 3, 4, 5, 17, 24), "the cache overlaps"),
+        "kv_read": (cache + [0x3000, 4, 0x10000000, 0x200000, 1, 0], (2, 3, 4, 5, 10), "overlap"),
+        "tree_attention": (cache + [0x100000, 512, 128, 4, 3, 0x9000, 2, 2, 0xA000, 0xB000, 5, 0, 0.1, 0x100000, 0, 0, 1, 0, 0, 0],
+                           (2, 3, 4, 5, 9, 13, 21, 22), "overlaps"),
+        "token_logprobs": ([0x100000, 1000, 2, 1000, 0, 0x1000, 1, 4, 0x100000, 0x3000, 0x4000, 0x5000, 0], (4, 6, 7), "overlaps"),
+    }
+    for name, (args, ints, says) in cases.items():
+        fn = getattr(calls, name)
+        assert fn(*args) == 1 and says in w.last_error(), name
+        for i in ints:
+            for shift in (big, -big):
+                wrong = list(args)
+                wrong[i] += shift
+                assert fn(*wrong) != 0 and says not in w.last_error(), (name, i)
+    assert w.w4a16_debug_launch_count() == before
+    s._bind()

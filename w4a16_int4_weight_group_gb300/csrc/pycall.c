@@ -21,6 +21,7 @@
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <limits.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -107,8 +108,11 @@ static int take(const char *name, PyObject *const *args, Py_ssize_t nargs, int w
   }
   return PyErr_Occurred() ? -1 : 0;
 }
+/* An argument of the C type int: one outside its range becomes the nearest end, which the library's checks refuse (cut to
+ * 32 bits it could be another, valid number). */
+static int to_int(int64_t x) { return x > INT_MAX ? INT_MAX : x < INT_MIN ? INT_MIN : (int)x; }
 #define PTR(i) ((void *)(uintptr_t)v[i])
-#define I32(i) ((int)v[i])
+#define I32(i) to_int(v[i])
 
 static w4a16_status (*g_rope)(const w4a16_rope_t *, const void *, int64_t, int64_t, void *, int64_t, int64_t, int64_t, int, int,
                               w4a16_dtype, w4a16_stream_t);
@@ -143,11 +147,11 @@ static int unbound(const void *fn) {
   return fn == NULL;
 }
 static w4a16_rope_t rope_at(const int64_t *v) {
-  const w4a16_rope_t r = {(const int64_t *)(uintptr_t)v[0], (const float *)(uintptr_t)v[1], v[2], (int32_t)v[3], (int32_t)v[4]};
+  const w4a16_rope_t r = {(const int64_t *)(uintptr_t)v[0], (const float *)(uintptr_t)v[1], v[2], I32(3), I32(4)};
   return r;
 }
 static w4a16_kv_cache_t cache_at(const int64_t *v) {
-  const w4a16_kv_cache_t c = {(void *)(uintptr_t)v[0], v[1], (int32_t)v[2], (int32_t)v[3], (int32_t)v[4], (int32_t)v[5]};
+  const w4a16_kv_cache_t c = {(void *)(uintptr_t)v[0], v[1], I32(2), I32(3), I32(4), I32(5)};
   return c;
 }
 
@@ -159,7 +163,7 @@ static PyObject *rope(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
   const w4a16_rope_t r = rope_at(v);
   int st;
   Py_BEGIN_ALLOW_THREADS
-  st = g_rope(&r, PTR(5), v[6], v[7], PTR(8), v[9], v[10], v[11], I32(12), I32(13), (w4a16_dtype)v[14], PTR(15));
+  st = g_rope(&r, PTR(5), v[6], v[7], PTR(8), v[9], v[10], v[11], I32(12), I32(13), (w4a16_dtype)I32(14), PTR(15));
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(st);
 }
@@ -173,7 +177,7 @@ static PyObject *kv_write(PyObject *self, PyObject *const *args, Py_ssize_t narg
   int st;
   Py_BEGIN_ALLOW_THREADS
   st = g_kv_write(&c, PTR(6), v[7], v[8], PTR(9), v[10], v[11], PTR(12), v[13], v[14] ? &r : NULL, PTR(19), v[20], v[21], I32(22),
-                  PTR(23), (w4a16_dtype)v[24], PTR(25));
+                  PTR(23), (w4a16_dtype)I32(24), PTR(25));
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(st);
 }
@@ -185,7 +189,7 @@ static PyObject *kv_read(PyObject *self, PyObject *const *args, Py_ssize_t nargs
   const w4a16_kv_cache_t c = cache_at(v);
   int st;
   Py_BEGIN_ALLOW_THREADS
-  st = g_kv_read(&c, PTR(6), v[7], PTR(8), PTR(9), (w4a16_dtype)v[10], PTR(11));
+  st = g_kv_read(&c, PTR(6), v[7], PTR(8), PTR(9), (w4a16_dtype)I32(10), PTR(11));
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(st);
 }
@@ -200,7 +204,7 @@ static PyObject *tree_attention(PyObject *self, PyObject *const *args, Py_ssize_
   int st;
   Py_BEGIN_ALLOW_THREADS
   st = g_tree_attention(&c, PTR(6), v[7], v[8], I32(9), v[10], PTR(11), v[12], I32(13), PTR(14), PTR(15), v[16], PTR(17), (float)scale,
-                        PTR(19), PTR(20), I32(21), (w4a16_dtype)v[22], PTR(23), (size_t)v[24], PTR(25));
+                        PTR(19), PTR(20), I32(21), (w4a16_dtype)I32(22), PTR(23), (size_t)v[24], PTR(25));
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(st);
 }
@@ -211,7 +215,7 @@ static PyObject *token_logprobs(PyObject *self, PyObject *const *args, Py_ssize_
   if (unbound(*(void **)&g_token_logprobs) || take("token_logprobs", args, nargs, 13, -1, v, NULL)) return NULL;
   int st;
   Py_BEGIN_ALLOW_THREADS
-  st = g_token_logprobs(PTR(0), v[1], v[2], v[3], (w4a16_dtype)v[4], PTR(5), I32(6), I32(7), PTR(8), PTR(9), PTR(10), PTR(11), PTR(12));
+  st = g_token_logprobs(PTR(0), v[1], v[2], v[3], (w4a16_dtype)I32(4), PTR(5), I32(6), I32(7), PTR(8), PTR(9), PTR(10), PTR(11), PTR(12));
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(st);
 }

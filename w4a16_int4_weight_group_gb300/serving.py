@@ -130,29 +130,39 @@ def _bind():
     return _calls
 
 
+def _ints(args, at):
+    """The arguments with those that are C ints (their places in `at`) brought into an int's range: past it the nearest end,
+    which the library's checks refuse (ctypes would cut them to 32 bits)."""
+    return [max(-2 ** 31, min(2 ** 31 - 1, int(x))) if i in at else x for i, x in enumerate(args)]
+
+
 class _Ctypes:
     """The flat calls of the marshalling module through ctypes."""
 
     @staticmethod
     def rope(*a):
+        a = _ints(a, (3, 4, 12, 13, 14))
         return lib().w4a16_rope(ctypes.byref(Rope(*a[:5])), *a[5:])
 
     @staticmethod
     def kv_write(*a):
+        a = _ints(a, (2, 3, 4, 5, 17, 18, 22, 24))
         rope = ctypes.byref(Rope(*a[14:19])) if a[14] else None
         return lib().w4a16_kv_write(ctypes.byref(KVCache(*a[:6])), *a[6:14], rope, *a[19:])
 
     @staticmethod
     def kv_read(*a):
+        a = _ints(a, (2, 3, 4, 5, 10))
         return lib().w4a16_kv_read(ctypes.byref(KVCache(*a[:6])), *a[6:])
 
     @staticmethod
     def tree_attention(*a):
+        a = _ints(a, (2, 3, 4, 5, 9, 13, 21, 22))
         return lib().w4a16_tree_attention_fill(ctypes.byref(KVCache(*a[:6])), *a[6:])
 
     @staticmethod
     def token_logprobs(*a):
-        return lib().w4a16_token_logprobs(*a)
+        return lib().w4a16_token_logprobs(*_ints(a, (4, 6, 7)))
 
 
 # The checks below use the cheapest tensor queries and read each once: the smallest calls take a few

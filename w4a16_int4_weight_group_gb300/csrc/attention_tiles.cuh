@@ -315,7 +315,6 @@ __global__ void __launch_bounds__(L::kThreads, 1) tiles_kernel(const Params p) {
   }
   __syncthreads();
   griddep_wait();
-  griddep_launch_dependents();
   const uint64_t lim = p.control->limit_ns;
   const uint64_t limit_ns = lim ? lim : kDefaultWaitNs;
   unsigned int *error = &p.control->error;
@@ -331,6 +330,9 @@ __global__ void __launch_bounds__(L::kThreads, 1) tiles_kernel(const Params p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kOffMisc + 4);
+  // The next kernel may start from here on (CTAs without a share are gone): one that allocates tensor memory before it waits
+  // for this one, as the layer's does, must not find it free while a CTA here has yet to take it, and then wait for that CTA.
+  griddep_launch_dependents();
 
   if (warp >= 8 && warp < 16) {
     // ---------------------------------------------------------------------------------- the codes

@@ -86,3 +86,10 @@ def test_without_q_start_every_row_is_computed(w):
     dev = inputs(w, [20, 40, 60], [1, 1, 1], 3, [0, 1, 2, 3])
     dev["q_start"], dev["max_q"] = None, None
     run(w, dev, range(3))
+
+
+@pytest.mark.parametrize("max_q", [2, 64])
+def test_a_prompt_that_is_far_too_long(w, max_q):
+    dev = inputs(w, [20000], [1], 20000, [0, 20000])
+    dev["max_q"] = max_q
+    run(w, dev, range(max_q))

@@ -319,11 +319,13 @@ __global__ void __launch_bounds__(L::kThreads, 1) tiles_kernel(const Params p) {
   const uint64_t limit_ns = lim ? lim : kDefaultWaitNs;
   unsigned int *error = &p.control->error;
 
-  fill_unowned<D, L::kThreads>(p, tid);
   Cursor cur;
   Shares sh;
   int64_t u1, units;
-  if (!share_of<L, W>(p, scan_s, share_s, cur, sh, u1, units)) return;  // nothing for this CTA
+  if (!share_of<L, W>(p, scan_s, share_s, cur, sh, u1, units)) {  // nothing for this CTA
+    fill_unowned<D, L::kThreads>(p, tid);
+    return;
+  }
   const int64_t cta = blockIdx.x;
   if (warp == 16) tmem_alloc(tmem_slot, L::kTmemCols);
   tc_fence_before();
@@ -750,7 +752,8 @@ __global__ void __launch_bounds__(L::kThreads, 1) tiles_kernel(const Params p) {
       row_s[256 + grp * 128 + row] = begun ? l : -1.f;  // (no tile: no sums either)
       // One answer for all threads of the softmax: the warps of the codes and of the MMAs, already at the next segment, may
       // set the flag at any moment, and the barriers and tensor memory loads below are for all of these threads or for none.
-      const bool given_up = bar_any<1, 256>(!ok || ld_flag(abort_flag) != 0);
+      // (A wait of these threads that ran out has set it too.)
+      const bool given_up = bar_any<1, 256>(ld_flag(abort_flag) != 0);
       tc_fence_after();
       if (given_up) ok = false;
       const float m0 = row_s[row], m1 = row_s[128 + row];
@@ -814,6 +817,7 @@ __global__ void __launch_bounds__(L::kThreads, 1) tiles_kernel(const Params p) {
   __syncthreads();
   tc_fence_after();
   if (warp == 16) tmem_dealloc(tmem, L::kTmemCols);
+  fill_unowned<D, L::kThreads>(p, tid);
 }
 
 template <int D>

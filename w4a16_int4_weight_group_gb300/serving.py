@@ -11,6 +11,8 @@ A model's step between two W4A16 projections:
     q = w4a16_kv_write(k, v, cache, slots, q=q, positions=positions, table=table)
     y = w4a16_tree_attention(q, cache, page_table, kv_lens, q_start=q_start, tree_mask=mask, max_q=n)
     logprobs, entropy, ids, alternatives = w4a16_token_logprobs(lm_head(h), drafted, top_k=5)
+
+For compiled models the module `ops` has them as torch.library ops.
 """
 from __future__ import annotations
 

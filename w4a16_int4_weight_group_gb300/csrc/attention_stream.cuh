@@ -62,7 +62,7 @@ struct StreamLayout {
   static constexpr int MB = W / 2;              // sums kept in shared memory when the warps join
   static constexpr int kPad = D + 4;            // floats of a row of them
   static constexpr bool kQSmem = NT * D >= 256; // Q's operands stay in shared memory, not in registers
-  static constexpr int kCtas = NT * D >= 256 && D < 256 ? 1 : 2;  // on an SM (one: more registers, none spilled in the loop)
+  static constexpr int kCtas = NT * D >= 256 && D < 256 ? 1 : 2;  // on an SM (one: 168 or 255 registers a thread, not 128)
   static constexpr int kQBytes = R * D * 2;
   static constexpr int kFixed = kQBytes + MB * R * kPad * 4 + R * (8 + 4) + 2 * W * R * 4 + 768;
   static constexpr int kBudget = (kCtas == 2 ? 113 : 226) * 1024;
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
           o[i][nt][2 + x] *= BITS == 4 ? f * 0.0625f : f;
         }
       }
-    // the upper warps' sums through shared memory, then those of the four that are left
+    // the upper half of the warps' sums through shared memory, then those of the lower half
     auto put = [&](int slot, bool add) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -596,13 +596,9 @@ __global__ void __launch_bounds__(L::kThreads, L::kCtas) stream_kernel(const Par
           }
         }
     };
-    if constexpr (W > L::MB) {
-      if (warp >= L::MB) put(warp - L::MB, false);
-      __syncthreads();
-      if (warp < L::MB) put(warp, true);
-    } else {
-      put(warp, false);
-    }
+    if (warp >= L::MB) put(warp - L::MB, false);
+    __syncthreads();
+    if (warp < L::MB) put(warp, true);
     __syncthreads();
     const bool given_up = ld_flag(abort_flag) != 0;
     if (given_up) ok = false;

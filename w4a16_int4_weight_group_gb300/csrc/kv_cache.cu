@@ -93,7 +93,7 @@ struct RopeParams {
   const float *table;
   int64_t table_rows;
   uint32_t threads;  // tokens * head_groups * units
-  int heads, head_dim, rot;
+  int heads, rot;
   uint32_t units;        // pieces of a row that one thread each handles
   uint32_t head_groups;  // threads that share a (token, unit): each takes every head_groups-th head
   bool copy_rest;   // out is not x: elements from rot on are copied
@@ -527,8 +527,11 @@ bool vec_ok(const HeadsView &x) { return aligned(x.ptr, 16) && x.token_stride % 
 
 // Threads of one launch (32-bit indices): calls with more run as several launches over their tokens.
 constexpr int64_t kMaxThreads = int64_t(1) << 31;
-// Threads that fill the GPU: below it a thread takes one head.
-constexpr int64_t kFill = 148 * 2048;
+// Threads of a call, one head each, below which a thread takes one head. One tuned value for the three kernels (heads
+// of 128, 152 SMs, replayed; one / several heads a thread): rotation of 48 heads, 128 tokens 2.0 / 2.3 us, 512 tokens 4.4 / 3.2, 4096
+// tokens 42 / 19; write of 40 + 2 x 8 heads with the read after it, 128 tokens 3.9 / 4.9, 512 tokens 7.0 / 7.4, 1024 tokens
+// 10.6 / 10.0, 4096 tokens 39 / 31; read of 8 heads at 4 bits, 512 tokens 1.75 / 2.05, 1024 tokens 2.3 / 2.1.
+constexpr int64_t kFill = 303104;
 
 CacheView view_of(const w4a16_kv_cache_t &c) {
   CacheView v{static_cast<uint8_t *>(c.data), c.num_pages * c.page_size, kv_tile_bytes(c.head_dim, c.bits), c.kv_heads,
@@ -544,7 +547,7 @@ cudaError_t rope_for(const RopeParams &p, bool vec, bool inter, cudaStream_t str
   return launch(inter ? rope_kernel<DT, 1, true> : rope_kernel<DT, 1, false>, p.threads, p, stream);
 }
 
-// Work items of a token in groups of up to `most` (1 when all of them one by one do not fill the GPU).
+// Work items of a token in groups of up to `most` (1 when all of them one by one are fewer than kFill).
 int items_a_group(int64_t tokens, int items, int lanes, int most) { return tokens * items * lanes < kFill ? 1 : most; }
 
 template <class DT, int LANES, int ROWS>
@@ -621,7 +624,6 @@ cudaError_t launch_rope(const HeadsView &x, const HeadsView &out, int64_t tokens
   p.table = rope.table;
   p.table_rows = rope.table_rows;
   p.heads = heads;
-  p.head_dim = head_dim;
   p.rot = rope.rot_dim;
   p.copy_rest = x.ptr != out.ptr;
   const bool inter = rope.interleaved;

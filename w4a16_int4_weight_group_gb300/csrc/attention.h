@@ -48,7 +48,8 @@ inline int stream_rows(int max_rows, int head_dim) { return max_rows <= 8 ? 8 : 
 // Past 32 rows the streaming kernel would go over the cache once more for every 32. One sequence of 131072 tokens, 8
 // cache heads of 128 (64) elements: 30 rows on the streaming kernel 161 us at 4 bits, 176 at 8 (144, 148), 35 to 125
 // rows on the other 172 to 179 and 224 to 230 (132 to 144). Heads of 256 elements leave no room for two stages of
-// operands of 128 tokens beside Q: they stay on the streaming kernel (35 rows 448 us, 125 rows 1174).
+// operands of 128 tokens beside Q (tiles of fewer tokens were not tried): they stay on the streaming kernel (35 rows 448 us, 125
+// rows 1174 to 1207).
 constexpr int kTileRows = 128;
 inline bool use_tiles(int max_rows, int head_dim) { return max_rows > 32 && head_dim <= 128; }
 

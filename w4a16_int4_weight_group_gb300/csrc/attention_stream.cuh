@@ -31,13 +31,19 @@
 //    steps need neither the reduction across lanes nor the rescaling of the sums.
 //
 // Measured (HBM: share of the device's 6782 GB/s copy rate):
-//  * 131073 tokens of 8 heads of 128 elements, 8 bits, 5 rows a head: 65 us = 4.2 TB/s, 0.62 of it. Each further
+//  * 131073 tokens of 8 heads of 128 elements, 8 bits, 5 rows a head: 64 to 71 us = 4.1 TB/s, 0.60 of it. Each further
 //    131072 tokens take 45 us (0.90): about 15 us are the call's start, first loads and the joining of the parts.
-//  * 48 sequences of up to 6001 tokens, 4 bits: 76 us = 2.2 TB/s (0.32). A 4-bit code costs the instructions of an
+//  * 48 sequences of up to 6001 tokens, 4 bits: 75 to 82 us = 2.1 TB/s (0.31). A 4-bit code costs the instructions of an
 //    8-bit one for half of the bytes; the schedulers issue in half of the cycles.
 //  * 12 sequences of up to 8200 tokens, heads of 256 elements, 8 bits, 13 drafted tokens: 77 us. 26 rows are two row
 //    tiles, so every code is decoded twice, by eight warps on an SM (255 registers a thread).
-//  * 517 tokens of one sequence: 12 us a call, which is what the host takes to issue it.
+//  * 517 tokens of one sequence: 12 to 15 us a call; 10.3 replayed from a graph, for 0.36 MB: fixed time (the search for
+//    the share, the first copies and the joining of the parts, one after the other), not bytes.
+//  * One token over 131073 tokens of 64 elements at 8 bits 55 us, of 128 at 4 bits 70 us, over 65537 of 256 elements 71 (8 bits)
+//    and 68 us (4 bits).
+// Registers: all but the 8-row layouts for 256 elements spill (bytes stored and loaded a thread): 8 rows of 128 elements at 4 bits
+// 316 and 368 (128 registers), of 64 and of 128 at 8 bits 40 to 124 and 56 to 160; 16 rows 24 to 120 and 24 to 168; 32 rows of
+// 64 elements 180 and 244, of 128 64 to 72 and 100 to 116.
 #pragma once
 
 #include "attention.h"

@@ -30,7 +30,7 @@
 // (attention_stream.cuh).
 //
 // Measured: 6 sequences of 20000 tokens, 64 drafted tokens, 8 heads of 128 elements at 4 bits, 320 rows a head (157
-// GFLOP): 355 us = 442 TFLOP/s, 0.23 of the library's dense bf16 rate; about 4600 cycles for a tile of 128 rows x
+// GFLOP): 352 us = 446 TFLOP/s, 0.23 of the library's dense bf16 rate; about 4600 cycles for a tile of 128 rows x
 // 128 tokens. A group's tile goes through QK (700 cycles), largest score (1000), exponentials (3500 to 4000) and PV
 // (1390, two products). The softmax sets the pace: with the groups made to take turns in it, so that one tile's
 // products lie under the other's softmax, a call takes 381 us, so one tile's maxima and exponentials alone take about
@@ -38,7 +38,8 @@
 // us, 370 in turns. P handed to its product in two or four pieces: 356. Parts left out for timing, with two
 // threads a row: codes 337, exponentials 279, both 224, the maxima too 180. No counter is near its limit
 // (schedulers 54 %, shared memory's pipe 39 % without the tensor cores' reads, tensor pipe 34 %).
-// 24 more registers a softmax thread (setmaxnreg): 377 -> 356.
+// 24 more registers a softmax thread (setmaxnreg): 377 -> 356. At its 96 registers the kernel spills (bytes stored and
+// loaded a thread) 356 and 384 for heads of 128 at 4 bits, 456 and 440 at 8; where it spills, and what that costs, was not measured.
 #pragma once
 
 #include "attention.h"

@@ -22,12 +22,16 @@
 // 16-bit vector), its slot and its place in the cache are fetched once for them. With little work it takes one.
 //
 // Measured (share of the device's 6782 GB/s copy rate):
-//  * rotation of 8191 tokens x 48 heads of 128, 64 rotated: 36.5 us for 203 MB, 5.6 TB/s (0.82; one head a thread: 44)
+//  * rotation of 8191 tokens x 48 heads of 128, 64 rotated, interleaved: 36.5 us for 203 MB, 5.6 TB/s (0.82; one head a
+//    thread: 44), 128 rotated 38; half layout (92 to 94 registers, where the other has 52) 41 with 128 rotated, 52 with 64.
+//    Parts that do not divide into 16-byte vectors go element by element: 40 of 128 rotated 132 us, 20 of 80 90 us for 127 MB
 //  * write with rotation of 8192 tokens, 40 q and 8 cached heads, 8 bits: 57 us with the
 //    read of the same tokens after it, 274 MB in all, 4.8 TB/s (0.71); in the write (50 us with a cold cache) the
-//    schedulers issue in 73 % of the cycles (the reductions and conversions of each row)
-//  * read of 50001 tokens of 8 heads, 4 bits: 41 us for 260 MB, 6.3 TB/s (0.93)
-//  * 5 or 16 tokens: 7.5 and 10 us a call, which is the host's time to issue it
+//    schedulers issue in 73 % of the cycles (the reductions and conversions of each row); interleaved 54, 4 bits 59 for
+//    257 MB; 40 of 128 rotated, element by element, 99 (that kernel spills 380 bytes a thread at its 40 registers)
+//  * read of 50001 tokens of 8 heads, 4 bits: 41 us for 260 MB, 6.3 TB/s (0.93); 8 bits 49 for 311 MB (0.93)
+//  * 5 tokens turned, 16 tokens written and read: 7.5 to 10 and 20 to 24 us, the host's time to issue one and two calls;
+//    replayed from a graph 1.6 and 3.5
 #include "common.cuh"
 #include "internal.h"
 

@@ -124,3 +124,43 @@ def test_a_workspace_of_the_caller(w, n):
         assert (ws[:4096] == 0).all()
     with pytest.raises(ValueError, match="workspace"):
         w.w4a16_tree_attention(workspace=ws.view(torch.int32), **dev)
+
+
+FRESH = """
+import sys
+import torch
+import w4a16_int4_weight_group_gb300 as w
+T, HQ, HK, D = 5, 8, 2, {D}
+g = torch.Generator().manual_seed(0)
+qkv = torch.randn(T, HQ + 2 * HK, D, generator=g).to(torch.bfloat16).cuda()
+q, k, v = qkv.split([HQ, HK, HK], 1)
+cache = w.w4a16_kv_cache(8, HK, D, 64, 4)
+slots, pos, table = torch.arange(T, device="cuda") + 400, torch.arange(T, device="cuda"), w.w4a16_rope_table(16, D)
+pages = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+lens, start = torch.tensor([405], dtype=torch.int32, device="cuda"), torch.tensor([0, T], dtype=torch.int32, device="cuda")
+logits = torch.randn(T, 5000, generator=g).cuda()
+def step():
+    x = w.w4a16_rope(q, pos, table)
+    y = w.w4a16_kv_write(k, v, cache, slots, q=q, positions=pos, table=table)
+    a, l = w.w4a16_tree_attention(y, cache, pages, lens, q_start=start, max_q={max_q}, return_lse=True)
+    return [x, y, a, l, *w.w4a16_kv_read(cache, slots, D, torch.bfloat16), *w.w4a16_token_logprobs(logits, pos, 3)]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+kept, want = cache.clone(), step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(kept, cache) and w.w4a16_get_device_error() == 0
+print("equal")
+"""
+
+
+@pytest.mark.parametrize("D,max_q", [(64, 5), (128, 5), (256, 5), (64, 40), (128, 40)])
+def test_the_first_calls_of_a_process_may_be_captured(w, D, max_q):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FRESH.format(D=D, max_q=max_q)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "equal" in r.stdout, r.stdout + r.stderr

@@ -306,7 +306,7 @@ size_t w4a16_kv_tile_bytes(int head_dim, int bits);
 
 /*
  * w4a16_rope - out = x with its heads turned to their tokens' positions, products and sums in fp32, one rounding.
- *   x, out: [tokens, heads, head_dim] of dtype; out may be x itself (same pointer and strides).
+ *   x, out: [tokens, heads, head_dim] of dtype; out may be x itself (same pointer and strides). Rows of out share no elements.
  *   16-byte aligned pointers, strides in multiples of 8 elements and rot_dim in multiples of 16 (8
  *   interleaved) run with vector accesses, anything else element by element.
  * Errors: INVALID_ARG (sizes, nulls, overlap), UNSUPPORTED (dtype), MISALIGNED (natural alignment).

@@ -135,3 +135,18 @@ def test_sizes_past_32_bits_are_refused_not_cut(w, s, through):
                 assert fn(*wrong) != 0 and says not in w.last_error(), (name, i)
     assert w.w4a16_debug_launch_count() == before
     s._bind()
+
+
+def test_rows_of_the_rotation_s_output_are_apart(w, s):
+    """Every pair of strides against a count of shared elements; calls that pass are stopped by the check after it."""
+    L, before, D = w.lib(), w.w4a16_debug_launch_count(), 6
+    r = s.Rope(0x1000, 0x2000, 100, 4, 0)
+    for T, H in ((1, 3), (2, 2), (3, 4), (4, 3), (5, 1)):
+        for ts in (1, 5, 6, 7, 11, 12, 13, 18, 24, 25, 30, 60):
+            for hs in (6, 7, 8, 12, 13, 18, 20, 24, 60):
+                at = [t * ts + h * hs + d for t in range(T) for h in range(H) for d in range(D)]
+                shared = len(set(at)) < len(at)
+                # x one element before out: overlaps it, unless out is refused first
+                st = L.w4a16_rope(ctypes.byref(r), vp(0x100000 - 2), 100, 20, vp(0x100000), ts, hs, T, H, D, 1, None)
+                assert st == 1 and ("share elements" if shared else "overlaps x") in w.last_error(), (T, H, ts, hs, w.last_error())
+    assert w.w4a16_debug_launch_count() == before

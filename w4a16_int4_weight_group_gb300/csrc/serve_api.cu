@@ -62,6 +62,19 @@ w4a16_status check_view(const HeadsView &v, int64_t tokens, int heads, int head_
   return W4A16_OK;
 }
 
+// Whether two rows (token, head) of a checked view share elements: |dt token_stride - dh head_stride| < head_dim for some dt and
+// dh that are not both zero. (Both signs of dh: only equal ones can come near, since strides are not negative.)
+bool rows_overlap(const HeadsView &v, int64_t tokens, int heads, int head_dim) {
+  if (tokens == 1) return false;  // (the heads of a token are apart: check_view)
+  if (v.token_stride < head_dim) return true;
+  if (v.token_stride >= int64_t(heads - 1) * v.head_stride + head_dim) return false;
+  for (int64_t dh = 1; dh < heads; ++dh) {
+    const int64_t at = dh * v.head_stride, dt = at / v.token_stride;  // the tokens before and after that offset
+    if ((dt < tokens && at - dt * v.token_stride < head_dim) || (dt + 1 < tokens && (dt + 1) * v.token_stride - at < head_dim)) return true;
+  }
+  return false;
+}
+
 w4a16_status check_rope(const w4a16_rope_t *r, int head_dim, RopeArgs *out) {
   if (!r->positions || !r->table) return fail(W4A16_ERR_INVALID_ARG, "positions and table must not be NULL");
   if (!aligned(r->positions, 8) || !aligned(r->table, 4))
@@ -98,6 +111,7 @@ w4a16_status w4a16_rope(const w4a16_rope_t *rope, const void *x, int64_t x_token
   const HeadsView xv = view(x, x_token_stride, x_head_stride, tokens, heads), ov = view(out, out_token_stride, out_head_stride, tokens, heads);
   if ((st = check_view(xv, tokens, heads, head_dim, "x", false)) != W4A16_OK) return st;
   if ((st = check_view(ov, tokens, heads, head_dim, "out", false)) != W4A16_OK) return st;
+  if (rows_overlap(ov, tokens, heads, head_dim)) return fail(W4A16_ERR_INVALID_ARG, "out: rows of different tokens or heads share elements");
   if (x == out ? (xv.token_stride != ov.token_stride || xv.head_stride != ov.head_stride)
                : overlaps(view_range(xv, tokens, heads, head_dim), view_range(ov, tokens, heads, head_dim)))
     return fail(W4A16_ERR_INVALID_ARG, "out overlaps x (in place: the same pointer and strides)");

@@ -396,6 +396,109 @@ w4a16_status w4a16_token_logprobs(const void *logits, int64_t row_stride, int64_
                                   int64_t *top_ids, float *top_logprobs, w4a16_stream_t stream);
 
 /*
+ * Operators around a step of many users: low-rank adapters beside the layer, which drafted tokens stand, and the pages of the
+ * cache. As above: stream-ordered, no allocation, no synchronisation, captured as they are; index tensors are read on the
+ * device, and an index out of range never leads to an access out of range.
+ */
+
+/*
+ * w4a16_lora - out = base + scales[i] * (x a_i^T) b_i^T, i = ids[t] for token t: low-rank adapters of many requests beside
+ * what a shared projection gives.
+ *   x       [tokens, k], base and out [tokens, n], rows x_stride, base_stride and out_stride elements apart (16-byte aligned,
+ *           multiples of 8; the stride of a single row does not count); out may be base itself (same pointer and stride)
+ *   a       [adapters, rank, k], b [adapters, n, rank], contiguous, 16-byte aligned
+ *   ids     int32 [tokens]; a token whose id is not in [0, adapters) has no adapter: its row of out is base's
+ *   scales  float32 [adapters] or NULL (1)
+ *   k, n: multiples of 8; rank: a multiple of 8, at most 128; adapters: at most 8191
+ * Sums are fp32; x a_i^T keeps 16 (BF16) or, below the token's largest, 22 bits (F16) for the second product; out is rounded
+ * once. A token's result does not depend on the other tokens of the call, apart from how its sums are split.
+ *   workspace  device memory, 256-byte aligned, w4a16_lora_workspace_size bytes (0 for 256 tokens and fewer: NULL will do); its
+ *              first 4 KiB are not touched, so that a stream's buffer for the layer and the attention serves here too.
+ * Errors: INVALID_ARG (sizes, nulls, overlap, workspace), UNSUPPORTED (dtype, k, n, rank, adapters), MISALIGNED, CUDA.
+ */
+w4a16_status w4a16_lora(const void *x, int64_t x_stride, const void *a, const void *b, const int32_t *ids, const float *scales,
+                        const void *base, int64_t base_stride, void *out, int64_t out_stride, int64_t tokens, int64_t k, int64_t n,
+                        int rank, int64_t adapters, w4a16_dtype dtype, void *workspace, size_t workspace_bytes, w4a16_stream_t stream);
+/* Bytes of workspace w4a16_lora needs for these sizes (0: none). */
+size_t w4a16_lora_workspace_size(int64_t tokens, int rank, int64_t adapters);
+
+/*
+ * w4a16_verify_drafts - which of each sequence's drafted tokens stand, and the token after them, from given random numbers:
+ * what comes out has the distribution of the target's own samples.
+ *   logits       [total, vocab], rows row_stride elements apart, F16, BF16 or F32: row i is the target's, after token i
+ *   tokens       int64 [total]: of each sequence its last token (the root, which is not judged), then the drafted ones
+ *   q_start      int32 [batch + 1]: sequence b has the tokens q_start[b] .. q_start[b + 1] - 1, the first max_q (<= 64) of which
+ *                count; NULL: one for each sequence (total == batch), which is plain sampling
+ *   tree_mask    uint64 [total], as for w4a16_tree_attention: a token's parent is the highest bit below its own (a token
+ *                without one cannot stand); NULL: chains
+ *   uniforms     float32 [total], in [0, 1): token i's own
+ *   noise        float32 [batch, vocab], rows noise_stride elements apart, positive: exponential numbers
+ *   draft_probs  float32 [total, vocab], rows draft_stride elements apart, or NULL; only without tree_mask: row i is the
+ *                distribution that the token after token i was drawn from
+ *   temperature  float32 [batch] or NULL (1): 0 (all probability on the largest logit, the lowest index of equal ones) or positive
+ * p = softmax(row / temperature). With draft_probs q, token d stands if u q(d) < p(d); the first that does not is replaced by a
+ * draw from max(p - q, 0). Without, the children of a token are judged in ascending order: child d stands if u Z < p(d), Z being 1 minus the
+ * p of the ones rejected at that token so far (p(d) counts as 0 for a token rejected there before); when none stands, the draw is from p
+ * without them. A draw from weights r takes the j with the largest r_j / noise_j (the lowest of equal ones); where
+ * no weight is left it is from p. A drafted token outside the vocabulary does not stand, and takes nothing from p.
+ *   accepted     int32 [batch]: drafted tokens that stand
+ *   path         int32 [batch, max_q]: indices (within the sequence) of the root and the accepted tokens, then -1
+ *   out_tokens   int64 [batch, max_q]: the accepted tokens and the one after them, then -1
+ *   out_probs    float32 [batch, max_q]: the target's probability of each, then 0
+ * A row with a NaN or +infinity, or without a finite logit, has no probabilities: none of its children stands, and the token after it is
+ * -1, with probability NaN. A sequence without tokens gives accepted 0 and path and out_tokens of -1.
+ *   workspace    device memory, 256-byte aligned, w4a16_verify_drafts_workspace_size bytes; its first 4 KiB are not touched.
+ * Errors: INVALID_ARG, UNSUPPORTED (dtype, max_q, draft_probs with tree_mask), MISALIGNED, CUDA.
+ */
+w4a16_status w4a16_verify_drafts(const void *logits, int64_t row_stride, int64_t total, int64_t vocab, w4a16_dtype dtype,
+                                 const int64_t *tokens, const int32_t *q_start, int64_t batch, int max_q, const uint64_t *tree_mask,
+                                 const float *uniforms, const float *noise, int64_t noise_stride, const float *draft_probs,
+                                 int64_t draft_stride, const float *temperature, int32_t *accepted, int32_t *path, int64_t *out_tokens,
+                                 float *out_probs, void *workspace, size_t workspace_bytes, w4a16_stream_t stream);
+/* Bytes of workspace w4a16_verify_drafts needs for these sizes on the current device. */
+size_t w4a16_verify_drafts_workspace_size(int64_t total, int64_t vocab);
+
+/*
+ * Pages of a cache. refs: int32 [num_pages], the sequences that hold each page (0: free); page_table: int32 [batch, max_pages]; a
+ * sequence of n tokens holds the first ceil(n / page_size) pages of its row. Entries outside [0, num_pages) hold nothing. Calls on the same refs
+ * go to one stream. Results do not depend on timing.
+ *
+ * w4a16_kv_fork - new sequences that share their parents' pages: row i of new_table [rows, max_pages] is the held part of row
+ *   parents[i] (int32 [rows]) of page_table, then -1; new_lens[i] is its length; refs of the pages grow by one for each new holder. A
+ *   parent outside [0, batch) gives an empty sequence.
+ * w4a16_kv_reserve - room for the tokens up to new_lens (int32 [batch], batch <= 4096). A sequence that grows and whose last page is
+ *   partly filled and held by others too gets a page of its own in its place, of which copies[b] (int32 [batch, 2]) says {from,
+ *   to}; else copies[b] is {-1, -1}. (The last holder among the call's sequences keeps the page, if no one else holds it.) Then new pages up
+ *   to new_lens. Pages are the free ones in ascending order, for the sequences in ascending order; each gets
+ *   refs 1. held[b]: the tokens that the sequence has room for: new_lens[b], less where pages (or the table's row) ran
+ *   out (no room for a copy: kv_lens[b]), and kv_lens[b] where it does not grow. Entries of pages that it did not get stay as they are.
+ * w4a16_kv_copy - copies of whole pages, copies int32 [n, 2] {from, to}, in all layers; pairs with a page outside the cache are
+ *   skipped. No page is written twice, or read and written, in one call.
+ * w4a16_kv_free - the pages of the tokens from keep (int32 [batch], NULL: 0) on are given back: refs shrink by one (not
+ *   below 0), and their entries become -1.
+ * w4a16_kv_compact - a verified tree's tokens put together: the tokens path[b][0], path[b][1], .. (int32 [batch, max_q], indices among the
+ *   sequence's drafted tokens, ended by the first negative one) of each sequence, whose drafted tokens are the last
+ *   q_start[b + 1] - q_start[b] of its kv_lens (NULL: 1), move to the first drafted places, in all heads and layers, whatever
+ *   their order; new_lens[b] is the sequence's length then. kv_lens past the table's end counts as its end. Indices past the drafted tokens and
+ *   places on pages outside the cache are not moved. No page of moved tokens belongs to two sequences.
+ *
+ * layers: how many caches of this form lie one after another from cache->data (1 to 65535).
+ * Errors: INVALID_ARG, UNSUPPORTED (bits, head_dim, max_q, batch of reserve), MISALIGNED, CUDA.
+ */
+w4a16_status w4a16_kv_fork(int32_t *refs, int64_t num_pages, int page_size, const int32_t *page_table, int64_t max_pages,
+                           const int32_t *kv_lens, int64_t batch, const int32_t *parents, int64_t rows, int32_t *new_table, int32_t *new_lens,
+                           w4a16_stream_t stream);
+w4a16_status w4a16_kv_reserve(int32_t *refs, int64_t num_pages, int page_size, int32_t *page_table, int64_t max_pages,
+                              const int32_t *kv_lens, const int32_t *new_lens, int64_t batch, int32_t *held, int32_t *copies,
+                              w4a16_stream_t stream);
+w4a16_status w4a16_kv_free(int32_t *refs, int64_t num_pages, int page_size, int32_t *page_table, int64_t max_pages, const int32_t *kv_lens,
+                           const int32_t *keep, int64_t batch, w4a16_stream_t stream);
+w4a16_status w4a16_kv_copy(const w4a16_kv_cache_t *cache, int64_t layers, const int32_t *copies, int64_t n, w4a16_stream_t stream);
+w4a16_status w4a16_kv_compact(const w4a16_kv_cache_t *cache, int64_t layers, const int32_t *page_table, int64_t max_pages,
+                              const int32_t *kv_lens, const int32_t *q_start, int64_t batch, const int32_t *path, int max_q,
+                              int32_t *new_lens, w4a16_stream_t stream);
+
+/*
  * w4a16_can_implement - host-only check of a layer configuration, mirroring
  * TritonW4A16LinearKernel.can_implement (PR #43731 report, key source snippets): returns W4A16_OK or
  * the rejection status, with the reason available from w4a16_last_error(). No device access.

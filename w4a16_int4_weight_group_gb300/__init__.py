@@ -482,5 +482,8 @@ __all__ = ["w4a16_pack", "w4a16_unpack", "w4a16_prepack", "w4a16_dequant", "w4a1
 from . import serving as _serving  # noqa: E402  (the serving operators build on the helpers above)
 from .serving import *  # noqa: E402,F401,F403
 
-SIGNATURES += _serving.SIGNATURES
-__all__ += _serving.__all__
+from . import step as _step  # noqa: E402
+from .step import *  # noqa: E402,F401,F403
+
+SIGNATURES += _serving.SIGNATURES + _step.SIGNATURES
+__all__ += _serving.__all__ + _step.__all__

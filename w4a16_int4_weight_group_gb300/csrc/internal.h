@@ -199,4 +199,74 @@ struct LogprobArgs {
 };
 cudaError_t launch_token_logprobs(const LogprobArgs &a, const DeviceInfo &dev);
 
+// ---------------------------------------------------------------------------------------------
+// Operators around a step of many users: low-rank adapters, verification of drafted tokens, pages of the cache
+// ---------------------------------------------------------------------------------------------
+struct LoraArgs {
+  const void *x, *a, *b, *base;
+  void *out;
+  const int32_t *ids;
+  const float *scales;  // or null
+  int64_t x_stride, base_stride, out_stride;
+  int64_t tokens, K, N;
+  int rank;
+  int64_t adapters;
+  int dtype;
+  void *workspace;
+  cudaStream_t stream;
+};
+cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev);
+// 0: none is needed
+size_t lora_workspace_bytes(int64_t tokens, int rank, int64_t adapters);
+int lora_most_adapters();
+
+struct VerifyArgs {
+  const void *logits;
+  int64_t row_stride, total, vocab;
+  int dtype;
+  const int64_t *tokens;
+  const int32_t *q_start;  // null: one token for each sequence
+  int64_t batch;
+  int max_q;
+  const uint64_t *tree_mask;  // null: chains
+  const float *uniforms, *noise;
+  int64_t noise_stride;
+  const float *draft;  // null: guesses
+  int64_t draft_stride;
+  const float *temperature;  // null: 1
+  int32_t *accepted, *path;
+  int64_t *out;
+  float *probs;
+  void *workspace;
+  cudaStream_t stream;
+};
+cudaError_t launch_verify(const VerifyArgs &a, const DeviceInfo &dev);
+size_t verify_workspace_bytes(int64_t total, int64_t vocab, int num_sms);
+
+struct PoolArgs {
+  int32_t *refs;
+  int64_t num_pages;
+  int page_size;
+  int64_t max_pages;
+};
+cudaError_t launch_kv_fork(const PoolArgs &a, const int32_t *table, const int32_t *lens, int64_t batch, const int32_t *parents, int64_t rows,
+                           int32_t *new_table, int32_t *new_lens, cudaStream_t stream);
+cudaError_t launch_kv_free(const PoolArgs &a, int32_t *table, const int32_t *lens, const int32_t *keep, int64_t batch, cudaStream_t stream);
+cudaError_t launch_kv_reserve(const PoolArgs &a, int32_t *table, const int32_t *lens, const int32_t *new_lens, int64_t batch, int32_t *held,
+                              int32_t *copies, cudaStream_t stream);
+int kv_reserve_most_sequences();
+cudaError_t launch_kv_copy(const w4a16_kv_cache_t &cache, int64_t layers, const int32_t *pairs, int64_t n, cudaStream_t stream);
+
+struct CompactArgs {
+  w4a16_kv_cache_t cache;
+  int64_t layers;
+  const int32_t *page_table;
+  int64_t max_pages;
+  const int32_t *kv_lens, *q_start, *path;
+  int64_t batch;
+  int max_q;
+  int32_t *new_lens;
+};
+cudaError_t launch_kv_compact(const CompactArgs &a, cudaStream_t stream);
+
 }  // namespace w4a16

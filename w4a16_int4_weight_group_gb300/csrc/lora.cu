@@ -1,0 +1,538 @@
+// Low-rank adapters of many requests beside a shared projection.
+//
+//     out_t = base_t + s_i (x_t A_i^T) B_i^T,   i = ids[t];  A_i [r, K], B_i [N, r]
+//
+// One kernel does both products; h = x A^T (r numbers a token) never leaves the SMs. A cluster of CTAs takes a tile of tokens
+// of one adapter. First product: the CTAs and their warps split K, so that A and x are read once a tile, each
+// straight from global memory into the fragments of mma.m16n8k16 (adapter rows on the M side, tokens on the N side). The order
+// of k within a sum is free, so a lane's 16 contiguous bytes of a row serve as its elements of two MMAs, for both operands
+// alike: no shared memory, no shuffles. The warps' partial sums are added in shared memory, the CTAs' through
+// distributed shared memory, in a fixed order. Second product: the CTAs and warps split N, tokens on the M side, h as
+// the A operand from shared memory; the columns of four n-tiles are dealt out so that a lane ends up with eight contiguous
+// columns of a token: 16-byte loads of base and stores of out.
+//
+// h is fp32 and goes into the second product as two numbers of the dtype, the upper part and the rest: 16 bits of it for
+// bfloat16, 22 below the token's largest for float16 (whose range its sums may leave: each token's h is scaled by a power
+// of two). The rounding of out is then the only one that shows.
+//
+// Tiles: tokens of the same adapter wherever they stand. Up to kFewTokens tokens every CTA ranks the tokens among
+// those of their adapter by itself (one launch); more are sorted by a kernel before this one (counting sort). The
+// composition of a tile does not change a token's result: the rows of an MMA do not mix and K is split in the same way.
+//
+// Bound by memory: base read and out written are most of the bytes for long prompts, A and B of every adapter for single
+// tokens.
+#include <algorithm>
+#include <atomic>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kFewTokens = 256;  // one thread for each
+constexpr int kSortThreads = 1024;
+constexpr int kMaxAdapters = 8191;  // counters of the sort in shared memory
+
+struct Tile {
+  int adapter, first, count;  // of the sorted tokens
+};
+
+struct Params {
+  const uint16_t *x, *a, *b, *base;
+  uint16_t *out;
+  const int32_t *ids;
+  const float *scales;
+  int64_t x_stride, base_stride, out_stride;
+  int64_t tokens, K, N;
+  int rank, adapters;
+  int csize;
+  bool copy;  // out is not base: tokens without an adapter are copied
+  int32_t *order;     // sorted tokens (null: few tokens, ranked here)
+  const Tile *tiles;
+  const int32_t *num_tiles;
+};
+
+__device__ __forceinline__ uint4 ld16(const uint16_t *p) { return *reinterpret_cast<const uint4 *>(p); }
+
+// upper and lower part of two numbers, as pairs of the dtype
+template <class DT>
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+  float ha, hb;
+  if constexpr (DT::kBF16) {  // truncated, so that a finite number's upper part is finite
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    hi = prmt(ua, ub, 0x7632);
+    ha = __uint_as_float(ua & 0xFFFF0000u), hb = __uint_as_float(ub & 0xFFFF0000u);
+    if (!(a == a)) hi |= 0x7FFFu;  // a NaN's payload may lie in the lost bits
+    if (!(b == b)) hi |= 0x7FFF0000u;
+  } else {
+    const __half2 h = __floats2half2_rn(a, b);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    ha = __low2float(h), hb = __high2float(h);
+  }
+  // an infinite or NaN number has no rest
+  const float ra = fabsf(a) < INFINITY ? a - ha : 0.f, rb = fabsf(b) < INFINITY ? b - hb : 0.f;
+  if constexpr (DT::kBF16) {
+    const __nv_bfloat162 l = __floats2bfloat162_rn(ra, rb);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+  } else {
+    const __half2 l = __floats2half2_rn(ra, rb);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+  }
+}
+
+template <int MR, int NT>
+struct Shape {
+  static constexpr int kRanks = 16 * MR, kTokens = 8 * NT;
+  static constexpr int kMT = (NT + 1) / 2;      // m-tiles of the second product
+  static constexpr int kChunks = (MR + 1) / 2;  // its k, in steps of 32
+  static constexpr int kHStride = kRanks + 4;
+  static constexpr int kPart = kWarps * MR * NT * 32 * 4;  // floats
+  static constexpr int kH = kMT * 16 * kHStride;
+  static constexpr int kFrag = kMT * kChunks * 2 * 2 * 32 * 4;  // words: [m-tile][chunk][step][hi, lo][lane][4]
+  static constexpr int kSmem = (kPart + kH + kFrag) * 4;
+};
+
+template <class DT, int MR, int NT, bool SORTED>
+__global__ void __launch_bounds__(kThreads, MR * NT <= 2 ? 3 : 2) lora_kernel(const Params p) {
+  using S = Shape<MR, NT>;
+  extern __shared__ __align__(16) float smem[];
+  float4 *part = reinterpret_cast<float4 *>(smem);  // [warp][MR][NT][lane]
+  float *h = smem + S::kPart;                       // [token][rank]
+  uint32_t *frag = reinterpret_cast<uint32_t *>(h + S::kH);
+  __shared__ int tok[S::kTokens];
+  __shared__ float back[S::kMT * 16];  // what a token's h was divided by (float16)
+  __shared__ int ids_s[SORTED ? 4 : kFewTokens];
+  __shared__ int leaders[SORTED ? 4 : kFewTokens];
+  __shared__ int warp_count[kWarps];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int csize = p.csize;
+  const int crank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  int my_id = -2, my_rank = 0, ntiles;
+  if constexpr (SORTED) {
+    ntiles = *p.num_tiles;
+  } else {
+    if (tid < p.tokens) {
+      my_id = p.ids[tid];
+      if (my_id < 0 || my_id >= p.adapters) my_id = -1;
+    }
+    ids_s[tid] = my_id;
+    __syncthreads();
+    const int4 *all = reinterpret_cast<const int4 *>(ids_s);
+    for (int j = 0; j * 4 < p.tokens; ++j) {
+      const int4 v = all[j];
+      my_rank += (v.x == my_id && j * 4 < tid) + (v.y == my_id && j * 4 + 1 < tid) + (v.z == my_id && j * 4 + 2 < tid) +
+                 (v.w == my_id && j * 4 + 3 < tid);
+    }
+    const bool lead = tid < p.tokens && my_rank % S::kTokens == 0 && (my_id >= 0 || p.copy);
+    const unsigned vote = __ballot_sync(0xFFFFFFFFu, lead);
+    if (lane == 0) warp_count[warp] = __popc(vote);
+    __syncthreads();
+    int at = __popc(vote & ((1u << lane) - 1));
+    ntiles = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w == warp) at += ntiles;
+      ntiles += warp_count[w];
+    }
+    if (lead) leaders[at] = tid;
+    __syncthreads();
+  }
+
+  for (int tile = cluster; tile < ntiles; tile += clusters) {
+    int adapter, count;
+    if constexpr (SORTED) {
+      const Tile d = p.tiles[tile];
+      adapter = d.adapter, count = d.count;
+      if (tid < count) tok[tid] = p.order[d.first + tid];
+    } else {
+      const int leader = leaders[tile];
+      adapter = ids_s[leader];
+      // (the leader's rank is counted by its own thread only)
+      const bool same = my_id == adapter && tid < p.tokens;
+      int lead_rank = 0;
+      for (int j = lane; j < leader; j += 32) lead_rank += ids_s[j] == adapter;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) lead_rank += __shfl_xor_sync(0xFFFFFFFFu, lead_rank, o);
+      const int at = my_rank - lead_rank;
+      const bool in = same && at >= 0 && at < S::kTokens;
+      if (in) tok[at] = tid;
+      count = __syncthreads_count(in);
+    }
+    __syncthreads();
+
+    // ---- first product: h^T = A x^T, K split over the cluster's warps
+    const uint16_t *ap = nullptr, *bp = nullptr;
+    if (adapter >= 0) {
+      ap = p.a + int64_t(adapter) * p.rank * p.K;
+      bp = p.b + int64_t(adapter) * p.N * p.rank;
+      float acc[MR][NT][4];
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
+      const uint16_t *xr[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) xr[n] = n * 8 + g < count ? p.x + tok[n * 8 + g] * p.x_stride : nullptr;
+      constexpr int U = MR * NT <= 8 ? 2 : 1;  // steps of 32 whose loads are in flight together
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      for (int64_t k0 = int64_t(crank * kWarps + warp) * (32 * U); k0 < p.K; k0 += int64_t(csize) * kWarps * (32 * U)) {
+        uint4 av[U][MR][2], xv[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t k = k0 + u * 32 + t * 8;
+          const bool in = k < p.K;
+#pragma unroll
+          for (int m = 0; m < MR; ++m)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int row = m * 16 + i * 8 + g;
+              av[u][m][i] = in && row < p.rank ? ld16(ap + row * p.K + k) : zero;
+            }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) xv[u][n] = in && xr[n] ? ld16(xr[n] + k) : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (NT > 1 && n * 8 >= count) break;
+#pragma unroll
+            for (int m = 0; m < MR; ++m) {
+              const uint4 v0 = av[u][m][0], v1 = av[u][m][1];
+              const uint32_t f0[4] = {v0.x, v1.x, v0.y, v1.y}, f1[4] = {v0.z, v1.z, v0.w, v1.w};
+              mma_16816<DT::kBF16>(acc[m][n], f0, xv[u][n].x, xv[u][n].y);
+              mma_16816<DT::kBF16>(acc[m][n], f1, xv[u][n].z, xv[u][n].w);
+            }
+          }
+      }
+#pragma unroll
+      for (int m = 0; m < MR; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          part[((warp * MR + m) * NT + n) * 32 + lane] = make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+    }
+    __syncthreads();
+    const float s = adapter >= 0 ? (p.scales ? p.scales[adapter] : 1.f) : 0.f;
+    if (adapter >= 0) {
+      // the warps' sums, then the CTAs', each in order
+      for (int e = tid; e < MR * NT * 32; e += kThreads) {
+        float4 v = part[e];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+          const float4 o = part[w * MR * NT * 32 + e];
+          v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        }
+        part[e] = v;
+      }
+      if (csize > 1) cluster_sync_all();
+      for (int e = tid; e < MR * NT * 32; e += kThreads) {
+        float4 v = part[e];
+        if (csize > 1) {
+          const uint32_t mine = smem_u32(&part[e]);
+          v = ld_dsmem_v4(map_to_rank(mine, 0));
+          for (int c = 1; c < csize; ++c) {
+            const float4 o = ld_dsmem_v4(map_to_rank(mine, c));
+            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+          }
+        }
+        const int l = e & 31, n = (e >> 5) % NT, m = (e >> 5) / NT;
+        float *at = h + (n * 8 + 2 * (l & 3)) * S::kHStride + m * 16 + (l >> 2);
+        at[0] = v.x * s, at[S::kHStride] = v.y * s, at[8] = v.z * s, at[S::kHStride + 8] = v.w * s;
+      }
+      __syncthreads();
+      if constexpr (!DT::kBF16) {  // power of two that brings a token's largest to [2^13, 2^14)
+        for (int i = warp; i < S::kTokens; i += kWarps) {
+          float top = 0.f;
+          for (int r = lane; r < S::kRanks; r += 32) top = fmaxf(top, fabsf(h[i * S::kHStride + r]));  // (a NaN does not count)
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+          const int e = static_cast<int>(__float_as_uint(top) >> 23);  // 0: zero or subnormal; 255: infinite
+          const int d = e == 0 || e == 255 ? 0 : max(-126, min(126, e - 127 - 13));
+          if (lane == 0) back[i] = __uint_as_float(static_cast<uint32_t>(127 + d) << 23);
+        }
+        __syncthreads();
+      }
+      for (int e = tid; e < S::kMT * S::kChunks * 32; e += kThreads) {
+        const int l = e & 31, c = (e >> 5) % S::kChunks, m = (e >> 5) / S::kChunks;
+        uint32_t hi[2][4], lo[2][4];  // [row g, g + 8][pair]
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = m * 16 + i * 8 + (l >> 2), r0 = c * 32 + (l & 3) * 8;
+          const bool in = row < S::kTokens;  // (one n-tile fills half an m-tile)
+          float f = 1.f;
+          if constexpr (!DT::kBF16) f = in ? 1.f / back[row] : 1.f;  // (exact: a power of two)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bool ok = in && r0 + 2 * j < S::kRanks;
+            const float v0 = ok ? h[row * S::kHStride + r0 + 2 * j] * f : 0.f, v1 = ok ? h[row * S::kHStride + r0 + 2 * j + 1] * f : 0.f;
+            split2<DT>(v0, v1, hi[i][j], lo[i][j]);
+          }
+        }
+        uint4 *at = reinterpret_cast<uint4 *>(frag) + ((m * S::kChunks + c) * 4) * 32 + l;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          at[(st * 2) * 32] = make_uint4(hi[0][2 * st], hi[1][2 * st], hi[0][2 * st + 1], hi[1][2 * st + 1]);
+          at[(st * 2 + 1) * 32] = make_uint4(lo[0][2 * st], lo[1][2 * st], lo[0][2 * st + 1], lo[1][2 * st + 1]);
+        }
+      }
+      __syncthreads();
+    }
+
+    // ---- second product: out = base + h B^T, N split over the cluster's warps in groups of 32 columns
+    for (int64_t n0 = int64_t(crank * kWarps + warp) * 32; n0 < p.N; n0 += int64_t(csize) * kWarps * 32) {
+      uint4 bv[4][S::kChunks];
+      if (adapter >= 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t col = n0 + (g >> 1) * 8 + 2 * j + (g & 1);
+#pragma unroll
+          for (int c = 0; c < S::kChunks; ++c) {
+            const int r0 = c * 32 + t * 8;
+            bv[j][c] = col < p.N && r0 < p.rank ? ld16(bp + col * p.rank + r0) : make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
+      const int64_t col = n0 + t * 8;
+#pragma unroll
+      for (int m = 0; m < S::kMT; ++m) {
+        if (m * 16 >= count) break;
+        const int i0 = m * 16 + g, i1 = i0 + 8;
+        const bool in0 = i0 < count && col < p.N, in1 = i1 < count && col < p.N;
+        uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0;
+        if (in0) o0 = ld16(p.base + tok[i0] * p.base_stride + col);
+        if (in1) o1 = ld16(p.base + tok[i1] * p.base_stride + col);
+        if (adapter >= 0) {
+          float acc[4][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+          for (int c = 0; c < S::kChunks; ++c)
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+              const uint4 *at = reinterpret_cast<const uint4 *>(frag) + ((m * S::kChunks + c) * 4 + st * 2) * 32 + lane;
+              const uint4 hi = at[0], lo = at[32];
+              const uint32_t fh[4] = {hi.x, hi.y, hi.z, hi.w}, fl[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t b0 = st ? bv[j][c].z : bv[j][c].x, b1 = st ? bv[j][c].w : bv[j][c].y;
+                mma_16816<DT::kBF16>(acc[j], fl, b0, b1);
+                mma_16816<DT::kBF16>(acc[j], fh, b0, b1);
+              }
+            }
+          float f0 = 1.f, f1 = 1.f;
+          if constexpr (!DT::kBF16) f0 = back[i0 < S::kTokens ? i0 : 0], f1 = back[i1 < S::kTokens ? i1 : 0];
+          auto add = [&](uint32_t &w, float a, float b, float f) {
+            typename DT::T lo16, hi16;
+            const float x = bits_to_float(static_cast<uint16_t>(w & 0xFFFF), DT::kBF16), y = bits_to_float(static_cast<uint16_t>(w >> 16), DT::kBF16);
+            lo16 = DT::from_float_rn(fmaf(a, f, x));
+            hi16 = DT::from_float_rn(fmaf(b, f, y));
+            w = static_cast<uint32_t>(*reinterpret_cast<uint16_t *>(&lo16)) | static_cast<uint32_t>(*reinterpret_cast<uint16_t *>(&hi16)) << 16;
+          };
+          add(o0.x, acc[0][0], acc[0][1], f0), add(o1.x, acc[0][2], acc[0][3], f1);
+          add(o0.y, acc[1][0], acc[1][1], f0), add(o1.y, acc[1][2], acc[1][3], f1);
+          add(o0.z, acc[2][0], acc[2][1], f0), add(o1.z, acc[2][2], acc[2][3], f1);
+          add(o0.w, acc[3][0], acc[3][1], f0), add(o1.w, acc[3][2], acc[3][3], f1);
+        }
+        if (in0) *reinterpret_cast<uint4 *>(p.out + tok[i0] * p.out_stride + col) = o0;
+        if (in1) *reinterpret_cast<uint4 *>(p.out + tok[i1] * p.out_stride + col) = o1;
+      }
+    }
+    // the cluster's partial sums have been read, and this CTA is done with its tile's tables
+    if (csize > 1) cluster_sync_all();
+    else __syncthreads();
+  }
+}
+
+// Counting sort of the tokens by adapter (those without one last), and the list of tiles. One CTA.
+__global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *ids, int tokens, int adapters, int tile_tokens, bool copy,
+                                                                 int32_t *order, Tile *tiles, int32_t *num_tiles) {
+  extern __shared__ int counts[];  // [adapters + 1], then the next place of each
+  __shared__ int sums[2][kSortThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_wait();  // the kernel before this one may still read the lists
+  griddep_launch_dependents();
+  for (int i = tid; i <= adapters; i += kSortThreads) counts[i] = 0;
+  __syncthreads();
+  auto key = [&](int i) {
+    const int id = ids[i];
+    return id < 0 || id >= adapters ? adapters : id;
+  };
+  // lanes with the same key add once
+  for (int i = tid; i - lane < tokens; i += kSortThreads) {
+    const int k = i < tokens ? key(i) : -1;
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, k);
+    if (k >= 0 && lane == __ffs(same) - 1) atomicAdd(&counts[k], __popc(same));
+  }
+  __syncthreads();
+  // places of each adapter's tokens and tiles: exclusive sums over the adapters, in chunks of one a thread
+  int tokens_before = 0, tiles_before = 0;
+  for (int k0 = 0; k0 <= adapters; k0 += kSortThreads) {
+    const int k = k0 + tid;
+    const int n = k <= adapters ? counts[k] : 0;
+    const int nt = k == adapters && !copy ? 0 : (n + tile_tokens - 1) / tile_tokens;
+    int a = n, b = nt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int ua = __shfl_up_sync(0xFFFFFFFFu, a, o), ub = __shfl_up_sync(0xFFFFFFFFu, b, o);
+      if (lane >= o) a += ua, b += ub;
+    }
+    if (lane == 31) sums[0][warp] = a, sums[1][warp] = b;
+    __syncthreads();
+    int ta = 0, tb = 0, wa = 0, wb = 0;
+    for (int w = 0; w < kSortThreads / 32; ++w) {
+      if (w == warp) wa = ta, wb = tb;
+      ta += sums[0][w], tb += sums[1][w];
+    }
+    const int first = tokens_before + wa + a - n;
+    int at = tiles_before + wb + b - nt;
+    if (k <= adapters) {
+      counts[k] = first;
+      for (int i = 0; i < nt; ++i)
+        tiles[at++] = Tile{k == adapters ? -1 : k, first + i * tile_tokens, min(tile_tokens, n - i * tile_tokens)};
+    }
+    tokens_before += ta, tiles_before += tb;
+    __syncthreads();
+  }
+  if (tid == 0) *num_tiles = tiles_before;
+  for (int i = tid; i - lane < tokens; i += kSortThreads) {
+    const int k = i < tokens ? key(i) : -1;
+    const unsigned same = __match_any_sync(0xFFFFFFFFu, k);
+    const int leader = __ffs(same) - 1;
+    int at = 0;
+    if (k >= 0 && lane == leader) at = atomicAdd(&counts[k], __popc(same));
+    at = __shfl_sync(0xFFFFFFFFu, at, leader);
+    if (k >= 0) order[at + __popc(same & ((1u << lane) - 1))] = i;
+  }
+}
+
+// Tokens of a tile: as many as the accumulators of the first product leave room for
+int tile_tokens(int rank, bool few) {
+  if (few) return 8;
+  return rank <= 32 ? 64 : rank <= 64 ? 32 : 16;
+}
+int64_t most_tiles(int64_t tokens, int rank, int64_t adapters) {
+  return tokens / tile_tokens(rank, false) + std::min<int64_t>(tokens, adapters + 1);
+}
+
+template <class DT, int MR, int NT, bool SORTED>
+cudaError_t go(Params p, int64_t tiles, int num_sms, cudaStream_t stream) {
+  using S = Shape<MR, NT>;
+  constexpr int kCtas = MR * NT <= 2 ? 3 : 2;  // on an SM
+  static std::atomic<bool> asked[64];  // dynamic shared memory past 48 KB is asked for once a device
+  auto kernel = lora_kernel<DT, MR, NT, SORTED>;
+  if (S::kSmem > 48 * 1024) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !asked[dev]) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) asked[dev] = true;
+    }
+  }
+  // CTAs of a tile: up to eight, while all tiles' CTAs are resident together
+  int c = 1;
+  while (c < 8 && tiles * c * 2 <= int64_t(kCtas) * num_sms) c *= 2;
+  p.csize = c;
+  const int64_t clusters = std::min<int64_t>(tiles, int64_t(kCtas) * num_sms / c);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * c), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (c > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(c);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+template <class DT>
+cudaError_t run(const Params &p, bool few, int64_t tiles, int num_sms, cudaStream_t stream) {
+  const int r = p.rank;
+  if (few) {
+    if (r <= 16) return go<DT, 1, 1, false>(p, tiles, num_sms, stream);
+    if (r <= 32) return go<DT, 2, 1, false>(p, tiles, num_sms, stream);
+    if (r <= 64) return go<DT, 4, 1, false>(p, tiles, num_sms, stream);
+    return go<DT, 8, 1, false>(p, tiles, num_sms, stream);
+  }
+  if (r <= 16) return go<DT, 1, 8, true>(p, tiles, num_sms, stream);
+  if (r <= 32) return go<DT, 2, 8, true>(p, tiles, num_sms, stream);
+  if (r <= 64) return go<DT, 4, 4, true>(p, tiles, num_sms, stream);
+  return go<DT, 8, 2, true>(p, tiles, num_sms, stream);
+}
+
+}  // namespace
+
+size_t lora_workspace_bytes(int64_t tokens, int rank, int64_t adapters) {
+  if (tokens <= kFewTokens) return 0;
+  return 4096 + 256 + static_cast<size_t>((tokens * 4 + 255) / 256 * 256) + static_cast<size_t>(most_tiles(tokens, rank, adapters)) * sizeof(Tile);
+}
+int lora_most_adapters() { return kMaxAdapters; }
+
+cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
+  Params p{};
+  p.x = static_cast<const uint16_t *>(a.x);
+  p.a = static_cast<const uint16_t *>(a.a);
+  p.b = static_cast<const uint16_t *>(a.b);
+  p.base = static_cast<const uint16_t *>(a.base);
+  p.out = static_cast<uint16_t *>(a.out);
+  p.ids = a.ids;
+  p.scales = a.scales;
+  p.x_stride = a.x_stride;
+  p.base_stride = a.base_stride;
+  p.out_stride = a.out_stride;
+  p.tokens = a.tokens;
+  p.K = a.K;
+  p.N = a.N;
+  p.rank = a.rank;
+  p.adapters = static_cast<int>(a.adapters);
+  p.copy = a.base != a.out;
+  const bool few = a.tokens <= kFewTokens;
+  int64_t tiles = a.tokens;
+  if (!few) {
+    // (past the first 4 KiB: the counters of other calls)
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace) + 4096;
+    int32_t *num = reinterpret_cast<int32_t *>(ws);
+    p.order = reinterpret_cast<int32_t *>(ws + 256);
+    Tile *list = reinterpret_cast<Tile *>(ws + 256 + (a.tokens * 4 + 255) / 256 * 256);
+    p.num_tiles = num;
+    p.tiles = list;
+    const int per = tile_tokens(a.rank, false);
+    tiles = (a.tokens + per - 1) / per;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, 1, 1);
+    cfg.blockDim = dim3(kSortThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.adapters + 1) * 4;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, lora_sort_kernel, a.ids, static_cast<int>(a.tokens), p.adapters, per, p.copy, p.order, list, num);
+    if (e != cudaSuccess) return e;
+    note_launch();
+  }
+  return a.dtype == W4A16_BF16 ? run<BF16>(p, few, tiles, dev.num_sms, a.stream) : run<F16>(p, few, tiles, dev.num_sms, a.stream);
+}
+
+}  // namespace w4a16

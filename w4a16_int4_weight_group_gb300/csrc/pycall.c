@@ -18,6 +18,9 @@
  *     w4a16_rope_t (positions, table, table_rows, rot_dim, interleaved; positions 0: no rope) and of
  *     w4a16_kv_cache_t (data, num_pages, kv_heads, head_dim, page_size, bits) in the place of the structures. The GIL is
  *     released around each: a launch waits while the stream's queue is full.
+ *
+ *   bind_step(lora, verify_drafts, kv_fork, kv_reserve, kv_free, kv_copy, kv_compact)   addresses of the seven
+ *   lora, verify_drafts, kv_fork, kv_reserve, kv_free, kv_copy, kv_compact -> status (int): the same way.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -220,6 +223,119 @@ static PyObject *token_logprobs(PyObject *self, PyObject *const *args, Py_ssize_
   return PyLong_FromLong(st);
 }
 
+static w4a16_status (*g_lora)(const void *, int64_t, const void *, const void *, const int32_t *, const float *, const void *, int64_t, void *,
+                              int64_t, int64_t, int64_t, int64_t, int, int64_t, w4a16_dtype, void *, size_t, w4a16_stream_t);
+static w4a16_status (*g_verify)(const void *, int64_t, int64_t, int64_t, w4a16_dtype, const int64_t *, const int32_t *, int64_t, int,
+                                const uint64_t *, const float *, const float *, int64_t, const float *, int64_t, const float *, int32_t *,
+                                int32_t *, int64_t *, float *, void *, size_t, w4a16_stream_t);
+static w4a16_status (*g_kv_fork)(int32_t *, int64_t, int, const int32_t *, int64_t, const int32_t *, int64_t, const int32_t *, int64_t, int32_t *,
+                                 int32_t *, w4a16_stream_t);
+static w4a16_status (*g_kv_reserve)(int32_t *, int64_t, int, int32_t *, int64_t, const int32_t *, const int32_t *, int64_t, int32_t *, int32_t *,
+                                    w4a16_stream_t);
+static w4a16_status (*g_kv_free)(int32_t *, int64_t, int, int32_t *, int64_t, const int32_t *, const int32_t *, int64_t, w4a16_stream_t);
+static w4a16_status (*g_kv_copy)(const w4a16_kv_cache_t *, int64_t, const int32_t *, int64_t, w4a16_stream_t);
+static w4a16_status (*g_kv_compact)(const w4a16_kv_cache_t *, int64_t, const int32_t *, int64_t, const int32_t *, const int32_t *, int64_t,
+                                    const int32_t *, int, int32_t *, w4a16_stream_t);
+
+static PyObject *bind_step(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  (void)self;
+  int64_t v[7];
+  if (take("bind_step", args, nargs, 7, -1, v, NULL)) return NULL;
+  for (int i = 0; i < 7; ++i)
+    if (!v[i]) {
+      PyErr_SetString(PyExc_ValueError, "bind_step: null function address");
+      return NULL;
+    }
+  *(void **)&g_lora = PTR(0);
+  *(void **)&g_verify = PTR(1);
+  *(void **)&g_kv_fork = PTR(2);
+  *(void **)&g_kv_reserve = PTR(3);
+  *(void **)&g_kv_free = PTR(4);
+  *(void **)&g_kv_copy = PTR(5);
+  *(void **)&g_kv_compact = PTR(6);
+  Py_RETURN_NONE;
+}
+static int step_unbound(const void *fn) {
+  if (fn == NULL) PyErr_SetString(PyExc_RuntimeError, "bind_step() was not called");
+  return fn == NULL;
+}
+
+/* the arguments of the C functions in their order, a cache as its six fields */
+static PyObject *lora(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  (void)self;
+  int64_t v[19];
+  if (step_unbound(*(void **)&g_lora) || take("lora", args, nargs, 19, -1, v, NULL)) return NULL;
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g_lora(PTR(0), v[1], PTR(2), PTR(3), PTR(4), PTR(5), PTR(6), v[7], PTR(8), v[9], v[10], v[11], v[12], I32(13), v[14], (w4a16_dtype)I32(15),
+              PTR(16), (size_t)v[17], PTR(18));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+static PyObject *verify_drafts(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  (void)self;
+  int64_t v[23];
+  if (step_unbound(*(void **)&g_verify) || take("verify_drafts", args, nargs, 23, -1, v, NULL)) return NULL;
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g_verify(PTR(0), v[1], v[2], v[3], (w4a16_dtype)I32(4), PTR(5), PTR(6), v[7], I32(8), PTR(9), PTR(10), PTR(11), v[12], PTR(13), v[14],
+                PTR(15), PTR(16), PTR(17), PTR(18), PTR(19), PTR(20), (size_t)v[21], PTR(22));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+static PyObject *kv_fork(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  (void)self;
+  int64_t v[12];
+  if (step_unbound(*(void **)&g_kv_fork) || take("kv_fork", args, nargs, 12, -1, v, NULL)) return NULL;
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g_kv_fork(PTR(0), v[1], I32(2), PTR(3), v[4], PTR(5), v[6], PTR(7), v[8], PTR(9), PTR(10), PTR(11));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+static PyObject *kv_reserve(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  (void)self;
+  int64_t v[11];
+  if (step_unbound(*(void **)&g_kv_reserve) || take("kv_reserve", args, nargs, 11, -1, v, NULL)) return NULL;
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g_kv_reserve(PTR(0), v[1], I32(2), PTR(3), v[4], PTR(5), PTR(6), v[7], PTR(8), PTR(9), PTR(10));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+static PyObject *kv_free(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  (void)self;
+  int64_t v[9];
+  if (step_unbound(*(void **)&g_kv_free) || take("kv_free", args, nargs, 9, -1, v, NULL)) return NULL;
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g_kv_free(PTR(0), v[1], I32(2), PTR(3), v[4], PTR(5), PTR(6), v[7], PTR(8));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+static PyObject *kv_copy(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  (void)self;
+  int64_t v[10];
+  if (step_unbound(*(void **)&g_kv_copy) || take("kv_copy", args, nargs, 10, -1, v, NULL)) return NULL;
+  const w4a16_kv_cache_t c = cache_at(v);
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g_kv_copy(&c, v[6], PTR(7), v[8], PTR(9));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+static PyObject *kv_compact(PyObject *self, PyObject *const *args, Py_ssize_t nargs) {
+  (void)self;
+  int64_t v[16];
+  if (step_unbound(*(void **)&g_kv_compact) || take("kv_compact", args, nargs, 16, -1, v, NULL)) return NULL;
+  const w4a16_kv_cache_t c = cache_at(v);
+  int st;
+  Py_BEGIN_ALLOW_THREADS
+  st = g_kv_compact(&c, v[6], PTR(7), v[8], PTR(9), PTR(10), v[11], PTR(12), I32(13), PTR(14), PTR(15));
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(st);
+}
+
 #define FAST(f) (PyCFunction)(void (*)(void))f, METH_FASTCALL
 static PyMethodDef kMethods[] = {
     {"bind", (PyCFunction)bind, METH_O, "bind(address of w4a16_layer_gemm)"},
@@ -233,6 +349,14 @@ static PyMethodDef kMethods[] = {
     {"kv_read", FAST(kv_read), "w4a16_kv_read, flat arguments -> status"},
     {"tree_attention", FAST(tree_attention), "w4a16_tree_attention_fill, flat arguments -> status"},
     {"token_logprobs", FAST(token_logprobs), "w4a16_token_logprobs, flat arguments -> status"},
+    {"bind_step", FAST(bind_step), "bind_step(lora, verify_drafts, kv_fork, kv_reserve, kv_free, kv_copy, kv_compact)"},
+    {"lora", FAST(lora), "w4a16_lora -> status"},
+    {"verify_drafts", FAST(verify_drafts), "w4a16_verify_drafts -> status"},
+    {"kv_fork", FAST(kv_fork), "w4a16_kv_fork -> status"},
+    {"kv_reserve", FAST(kv_reserve), "w4a16_kv_reserve -> status"},
+    {"kv_free", FAST(kv_free), "w4a16_kv_free -> status"},
+    {"kv_copy", FAST(kv_copy), "w4a16_kv_copy, flat arguments -> status"},
+    {"kv_compact", FAST(kv_compact), "w4a16_kv_compact, flat arguments -> status"},
     {NULL, NULL, 0, NULL},
 };
 

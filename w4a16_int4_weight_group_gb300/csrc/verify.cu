@@ -1,0 +1,524 @@
+// Which drafted tokens stand, and the token after them, from given random numbers.
+//
+//     p = softmax(logits row / T) of a node (T = 0: all on the largest logit, the lowest index of equal ones)
+//     chain with the drafter's q: token d stands if u q(d) < p(d); else the next token comes from max(p - q, 0)
+//     tree of guesses: a node's children in the order of their indices, Z = 1 - the p of those rejected so far;
+//       child d stands if u Z < p(d) (0 for a token that was rejected at this node before); the next
+//       token comes from p without the rejected ones
+//     a draw from weights r: the j with the largest r_j / e_j, e the given exponential numbers (the first to go off of
+//       exponential clocks of rates r); nothing left of r: from p
+//
+// Both give the target's own distribution. A draw by clocks compares single ratios, so that its result does not hang on
+// the last bits of a sum over the vocabulary, nor on the order in which that is added.
+//
+// Two kernels. The first reads every row once: running maximum and sum of exponentials, rows split over CTAs when
+// they are few. The second has a cluster for each sequence: a thread for each token finds its parent, gathers p(d) and q(d) and
+// looks for an earlier sibling of the same token; one thread walks down the tree (a single pass over the tokens, as a
+// parent comes before its children); then the cluster's CTAs take a part of the vocabulary each, of the last node's row
+// alone. Whether a token was rejected is only looked up for the ratios that exceed a thread's best so far.
+//
+// Bound by memory in the first kernel, by the latency of its chain of small steps in the second.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace w4a16 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStatCtas = 6;   // on an SM
+constexpr int kMaxQ = 64;
+constexpr int kMaxSplits = 32;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kFar = -1.0e4f;  // exp2(kFar) is zero; keeps infinities out of differences
+
+struct F32 {};
+template <class DT>
+struct Elem {
+  static constexpr int kBytes = 2, kVec = 8;
+  static __device__ __forceinline__ float at(const void *p, int64_t i) {
+    return bits_to_float(reinterpret_cast<const uint16_t *>(p)[i], DT::kBF16);
+  }
+  static __device__ __forceinline__ void values(const uint4 &v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT::kBF16) {
+        f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+        f[2 * i] = h.x, f[2 * i + 1] = h.y;
+      }
+    }
+  }
+};
+template <>
+struct Elem<F32> {
+  static constexpr int kBytes = 4, kVec = 4;
+  static __device__ __forceinline__ float at(const void *p, int64_t i) { return reinterpret_cast<const float *>(p)[i]; }
+  static __device__ __forceinline__ void values(const uint4 &v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  }
+};
+
+struct Params {
+  const uint8_t *logits;
+  int64_t row_stride, total, vocab;
+  const int64_t *tokens;
+  const int32_t *q_start;  // null: one token for each sequence
+  int64_t batch;
+  int max_q;
+  const uint64_t *tree_mask;
+  const float *uniforms, *noise, *draft, *temperature;
+  int64_t noise_stride, draft_stride;
+  int32_t *accepted, *path;
+  int64_t *out;
+  float *probs;
+  float2 *stats;  // [total][splits]: maximum, sum of exp((x - maximum) / T); T = 0: the index of the maximum in place of the sum
+  int splits;
+  int64_t share;  // elements of a split
+  int csize;
+  int64_t cshare;  // elements of a CTA of a sequence's cluster
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// log2(e) / T, kept so small that zero times it is zero (a tiny T is as good as none)
+__device__ __forceinline__ float unit_of(float temp) {
+  const float c = kLog2e / temp;
+  return c > 1e30f ? 1e30f : c;
+}
+// exp2((a - m) c) of a running maximum a that grows to m
+__device__ __forceinline__ float shrink(float a, float m, float c) {
+  return a == -INFINITY ? 0.f : exp2_approx(max_nan(a - m, kFar) * c);
+}
+__device__ __forceinline__ void join(float &m, float &s, float om, float os, float c) {
+  const float top = max_nan(m, om);
+  s = s * shrink(m, top, c) + os * shrink(om, top, c);
+  m = top;
+}
+// the larger value, the lower index of equal ones; a NaN stays
+__device__ __forceinline__ void join_index(float &m, int &i, float om, int oi) {
+  if (om > m || (om == m && oi < i) || !(om == om)) m = om, i = oi;
+}
+
+// A row as head (up to the first 16-byte boundary), whole vectors, tail
+template <class DT>
+struct Span {
+  const uint4 *vec;
+  int64_t lo;
+  int head, n_vec, tail;
+  __device__ __forceinline__ Span(const uint8_t *row, int64_t lo_, int64_t hi) : lo(lo_) {
+    using E = Elem<DT>;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + lo * E::kBytes);
+    head = static_cast<int>(min(int64_t((16 - (at & 15)) & 15) / E::kBytes, hi - lo));
+    n_vec = static_cast<int>((hi - lo - head) / E::kVec);
+    tail = static_cast<int>(hi - lo - head - int64_t(n_vec) * E::kVec);
+    vec = reinterpret_cast<const uint4 *>(row + (lo + head) * E::kBytes);
+  }
+  // index of the i-th element that is in no vector
+  __device__ __forceinline__ int64_t loose(int i) const {
+    return i < head ? lo + i : lo + head + int64_t(n_vec) * Elem<DT>::kVec + (i - head);
+  }
+};
+
+template <class DT>
+__global__ void __launch_bounds__(kThreads, kStatCtas) verify_stats_kernel(const Params p) {
+  using E = Elem<DT>;
+  constexpr int kVec = E::kVec, U = 4;
+  __shared__ float ms[kWarps], ss[kWarps];
+  __shared__ int is[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = blockIdx.x / p.splits;
+  const int split = static_cast<int>(blockIdx.x % p.splits);
+  griddep_wait();
+  griddep_launch_dependents();
+
+  float temp = 1.f;
+  if (p.temperature) {
+    int64_t seq = row;
+    if (p.q_start) {  // sequences that end at or before the row
+      seq = 0;
+      for (int64_t b0 = 0; b0 < p.batch; b0 += kThreads) seq += __syncthreads_count(b0 + tid < p.batch && p.q_start[b0 + tid + 1] <= row);
+    }
+    if (seq < p.batch) temp = p.temperature[seq];
+  }
+  const float c = temp == 0.f ? 0.f : unit_of(temp);
+  const uint8_t *x = p.logits + row * p.row_stride * E::kBytes;
+  const int64_t lo = min(p.share * split, p.vocab), hi = min(lo + p.share, p.vocab);
+  const Span<DT> span(x, lo, hi);
+  float m = -INFINITY, s = 0.f;
+  int first = 0x7FFFFFFF;
+  if (temp == 0.f) {
+    for (int j = tid; j < span.head + span.tail; j += kThreads) {
+      const int64_t i = span.loose(j);
+      join_index(m, first, E::at(x, i), static_cast<int>(i));
+    }
+    for (int j0 = 0; j0 < span.n_vec; j0 += kThreads * U) {
+      uint4 w[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * kThreads + tid;
+        if (j < span.n_vec) w[u] = __ldcs(span.vec + j);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * kThreads + tid;
+        if (j >= span.n_vec) break;
+        float f[kVec];
+        E::values(w[u], f);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) join_index(m, first, f[e], static_cast<int>(lo) + span.head + j * kVec + e);
+      }
+    }
+  } else {
+    if (tid < span.head + span.tail) {  // (fewer than two vectors)
+      m = E::at(x, span.loose(tid));
+      s = m == -INFINITY ? 0.f : m - m + 1.f;  // NaN for a NaN or an infinity
+    }
+    for (int j0 = 0; j0 < span.n_vec; j0 += kThreads * U) {
+      uint4 w[U];
+      bool in[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * kThreads + tid;
+        in[u] = j < span.n_vec;
+        if (in[u]) w[u] = __ldcs(span.vec + j);
+      }
+      float top = m;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (in[u]) {
+          float f[kVec];
+          E::values(w[u], f);
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) top = max_nan(top, f[e]);
+        }
+      s *= shrink(m, top, c);
+      m = top;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (in[u]) {
+          float f[kVec];
+          E::values(w[u], f);
+          float part = 0.f;
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) part += exp2_approx((m == -INFINITY ? f[e] : f[e] - m) * c);
+          s += part;
+        }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float om = __shfl_xor_sync(0xFFFFFFFFu, m, o);
+    if (temp == 0.f) {
+      const int oi = __shfl_xor_sync(0xFFFFFFFFu, first, o);
+      join_index(m, first, om, oi);
+    } else {
+      const float os = __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      join(m, s, om, os, c);
+    }
+  }
+  if (lane == 0) ms[warp] = m, ss[warp] = s, is[warp] = first;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kWarps; ++w) {
+      if (temp == 0.f) join_index(m, first, ms[w], is[w]);
+      else join(m, s, ms[w], ss[w], c);
+    }
+    p.stats[row * p.splits + split] = make_float2(m, temp == 0.f ? __int_as_float(first) : s);
+  }
+}
+
+// score and index as a number that grows with the score and falls with the index; 0: none
+__device__ __forceinline__ uint64_t key_of(float score, uint32_t i) {
+  return uint64_t(__float_as_uint(score) + 1u) << 32 | (0xFFFFFFFFu - i);
+}
+
+template <class DT>
+__global__ void __launch_bounds__(kThreads) verify_walk_kernel(const Params p) {
+  using E = Elem<DT>;
+  constexpr int kVec = E::kVec;
+  __shared__ float row_m[kMaxQ], row_s[kMaxQ];  // s: 1 / sum, or the index of the maximum
+  __shared__ float pd[kMaxQ], qd[kMaxQ], us[kMaxQ];
+  __shared__ int64_t tok[kMaxQ];
+  __shared__ int parent[kMaxQ];  // -1: a token that cannot stand
+  __shared__ bool again[kMaxQ];
+  __shared__ int chosen[kMaxQ];
+  __shared__ int64_t rejected[kMaxQ];
+  __shared__ int s_accepted, s_rejected;
+  __shared__ uint64_t warp_key[kWarps];
+  __shared__ uint64_t cta_key;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int csize = p.csize;
+  const int crank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t b = blockIdx.x / csize;
+  griddep_wait();
+  griddep_launch_dependents();
+  int64_t start = b, end = b + 1;
+  if (p.q_start) start = max(p.q_start[b], 0), end = min(int64_t(p.q_start[b + 1]), p.total);
+  const int n = static_cast<int>(min(int64_t(p.max_q), end - start));
+  if (n <= 0) {  // (the same for the whole cluster)
+    if (crank == 0) {
+      if (tid == 0) p.accepted[b] = 0;
+      for (int i = tid; i < p.max_q; i += kThreads) p.path[b * p.max_q + i] = -1, p.out[b * p.max_q + i] = -1, p.probs[b * p.max_q + i] = 0.f;
+    }
+    return;
+  }
+  const float temp = p.temperature ? p.temperature[b] : 1.f;
+  const bool greedy = temp == 0.f;
+  const float c = greedy ? 0.f : unit_of(temp);
+  // the rows' statistics, four threads a row
+  {
+    const int i = tid >> 2;
+    if (i < n) {
+      const float2 *st = p.stats + (start + i) * p.splits;
+      float m = -INFINITY, s = 0.f;
+      int at = 0x7FFFFFFF;
+      for (int k = tid & 3; k < p.splits; k += 4) {
+        const float2 o = st[k];
+        if (greedy) join_index(m, at, o.x, __float_as_int(o.y));
+        else join(m, s, o.x, o.y, c);
+      }
+      const unsigned quad = 0xFu << (lane & 28);
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        const float om = __shfl_xor_sync(quad, m, o);
+        if (greedy) {
+          const int oi = __shfl_xor_sync(quad, at, o);
+          join_index(m, at, om, oi);
+        } else {
+          const float os = __shfl_xor_sync(quad, s, o);
+          join(m, s, om, os, c);
+        }
+      }
+      if ((tid & 3) == 0) {
+        // a row without probabilities (NaN, +infinity, nothing finite): NaN, and every comparison with it fails
+        const bool ok = fabsf(m) < INFINITY && (greedy || s < INFINITY);
+        row_m[i] = ok ? m : __int_as_float(0x7FFFFFFF);
+        row_s[i] = greedy ? __int_as_float(at) : 1.f / s;
+      }
+    }
+    if (tid < n) {
+      tok[tid] = p.tokens[start + tid];
+      us[tid] = p.uniforms[start + tid];
+    }
+  }
+  __syncthreads();
+  // the target's probability of a token under a node's row
+  auto prob = [&](int node, int64_t token) {
+    const float m = row_m[node];
+    if (!(m == m)) return m;
+    if (greedy) return token == __float_as_int(row_s[node]) ? 1.f : 0.f;
+    return exp2f((E::at(p.logits + (start + node) * p.row_stride * E::kBytes, token) - m) * c) * row_s[node];
+  };
+  if (tid < n) {
+    const uint64_t word = p.tree_mask ? p.tree_mask[start + tid] : ~0ull;
+    const uint64_t below = word & ((1ull << tid) - 1);
+    const int up = below == 0 || tok[tid] < 0 || tok[tid] >= p.vocab ? -1 : 63 - __clzll(static_cast<long long>(below));
+    parent[tid] = up;
+    if (up >= 0) {
+      pd[tid] = prob(up, tok[tid]);
+      qd[tid] = p.draft ? p.draft[(start + up) * p.draft_stride + tok[tid]] : 0.f;
+    }
+  }
+  __syncthreads();
+  if (tid < n) {
+    bool dup = false;
+    if (p.tree_mask)
+      for (int j = 1; j < tid; ++j) dup |= parent[j] == parent[tid] && tok[j] == tok[tid];
+    again[tid] = dup;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int node = 0, k = 0, nr = 0;
+    float left = 1.f;
+    chosen[0] = 0;
+    for (int i = 1; i < n; ++i) {
+      if (parent[i] != node) continue;
+      const float pi = again[i] ? 0.f : pd[i];
+      if (p.draft ? us[i] * qd[i] < pi : us[i] * left < pi) {
+        node = i, left = 1.f, nr = 0;
+        chosen[++k] = i;
+      } else {
+        left -= pi;
+        rejected[nr++] = tok[i];
+      }
+    }
+    s_accepted = k, s_rejected = nr;
+  }
+  __syncthreads();
+  const int k = s_accepted, last = chosen[k];
+  int nr = s_rejected;
+  const float m = row_m[last];
+  const bool valid = m == m;
+  uint64_t best = 0;
+  if (valid && greedy) {
+    best = key_of(1.f, static_cast<uint32_t>(__float_as_int(row_s[last])));
+  } else if (valid) {
+    const uint8_t *x = p.logits + (start + last) * p.row_stride * E::kBytes;
+    const float *e = p.noise + b * p.noise_stride;
+    const float *q = p.draft && nr ? p.draft + (start + last) * p.draft_stride : nullptr;
+    const float inv = row_s[last];
+    if (q) nr = 0;
+    const int64_t lo = min(p.cshare * crank, p.vocab), hi = min(lo + p.cshare, p.vocab);
+    const Span<DT> span(x, lo, hi);
+    while (true) {
+      float top = -1.f;
+      uint32_t top_i = 0;
+      auto take = [&](float xv, float ev, float qv, uint32_t i) {
+        const float r = fmaxf(exp2_approx((xv - m) * c) * inv - qv, 0.f);
+        const float score = __fdividef(r, ev);
+        if (r > 0.f && score > top) {
+          bool gone = false;
+          for (int j = 0; j < nr; ++j) gone |= rejected[j] == i;
+          if (!gone) top = score, top_i = i;
+        }
+      };
+      // ascending indices within a thread, so that the first of equal ratios stays
+      if (tid < span.head) {
+        const int64_t i = lo + tid;
+        take(E::at(x, i), e[i], q ? q[i] : 0.f, static_cast<uint32_t>(i));
+      }
+      for (int j = tid; j < span.n_vec; j += kThreads) {
+        float f[kVec], ev[kVec], qv[kVec];
+        const uint4 w = span.vec[j];
+        const int64_t i = lo + span.head + int64_t(j) * kVec;
+#pragma unroll
+        for (int a = 0; a < kVec; ++a) ev[a] = __ldcs(e + i + a), qv[a] = q ? __ldcs(q + i + a) : 0.f;
+        E::values(w, f);
+#pragma unroll
+        for (int a = 0; a < kVec; ++a) take(f[a], ev[a], qv[a], static_cast<uint32_t>(i) + a);
+      }
+      if (tid < span.tail) {
+        const int64_t i = span.loose(span.head + tid);
+        take(E::at(x, i), e[i], q ? q[i] : 0.f, static_cast<uint32_t>(i));
+      }
+      best = top >= 0.f ? key_of(top, top_i) : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+      if (lane == 0) warp_key[warp] = best;
+      __syncthreads();
+      best = warp_key[0];
+      for (int w = 1; w < kWarps; ++w) best = max(best, warp_key[w]);
+      if (csize > 1) {
+        if (tid == 0) cta_key = best;
+        cluster_sync_all();
+        for (int r = 0; r < csize; ++r) {
+          uint64_t o;
+          asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(o) : "r"(map_to_rank(smem_u32(&cta_key), r)));
+          best = max(best, o);
+        }
+        cluster_sync_all();  // read by all, before it is written again or its CTA leaves
+      } else {
+        __syncthreads();
+      }
+      if (best != 0 || (!q && nr == 0)) break;
+      q = nullptr, nr = 0;  // nothing is left: from p itself
+    }
+  }
+  if (crank != 0) return;
+  if (tid < p.max_q) {
+    const int64_t at = b * p.max_q + tid;
+    int64_t token = -1;
+    float pr = 0.f;
+    if (tid < k) {
+      token = tok[chosen[tid + 1]];
+      pr = pd[chosen[tid + 1]];
+    } else if (tid == k) {
+      token = best ? static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(best)) : -1;
+      pr = token >= 0 ? prob(last, token) : __int_as_float(0x7FFFFFFF);
+    }
+    p.path[at] = tid <= k ? chosen[tid] : -1;
+    p.out[at] = token;
+    p.probs[at] = pr;
+  }
+  if (tid == 0) p.accepted[b] = k;
+}
+
+// CTAs of a row: while all are resident at once and each keeps 4096 elements
+int splits_of(int64_t total, int64_t vocab, int num_sms) {
+  int s = 1;
+  while (s < kMaxSplits && total * s * 2 <= int64_t(kStatCtas) * num_sms && vocab / (s * 2) >= 4096) s *= 2;
+  return s;
+}
+
+template <class DT>
+cudaError_t go(const Params &p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.total * p.splits), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (p.total > 0) {
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_stats_kernel<DT>, p);
+    if (e != cudaSuccess) return e;
+    note_launch();
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(p.batch * p.csize), 1, 1);
+  if (p.csize > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.csize);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_walk_kernel<DT>, p);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+}  // namespace
+
+size_t verify_workspace_bytes(int64_t total, int64_t vocab, int num_sms) {
+  return 4096 + static_cast<size_t>(total) * splits_of(total, vocab, num_sms) * sizeof(float2);
+}
+
+cudaError_t launch_verify(const VerifyArgs &a, const DeviceInfo &dev) {
+  Params p{};
+  p.logits = static_cast<const uint8_t *>(a.logits);
+  p.row_stride = a.row_stride;
+  p.total = a.total;
+  p.vocab = a.vocab;
+  p.tokens = a.tokens;
+  p.q_start = a.q_start;
+  p.batch = a.batch;
+  p.max_q = a.max_q;
+  p.tree_mask = a.tree_mask;
+  p.uniforms = a.uniforms;
+  p.noise = a.noise;
+  p.noise_stride = a.noise_stride;
+  p.draft = a.draft;
+  p.draft_stride = a.draft_stride;
+  p.temperature = a.temperature;
+  p.accepted = a.accepted;
+  p.path = a.path;
+  p.out = a.out;
+  p.probs = a.probs;
+  p.stats = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.workspace) + 4096);  // (past the counters of other calls)
+  p.splits = splits_of(a.total, a.vocab, dev.num_sms);
+  p.share = ((a.vocab + p.splits - 1) / p.splits + 63) / 64 * 64;
+  int c = 1;
+  while (c < 8 && a.vocab / (c * 2) >= 2048) c *= 2;
+  p.csize = c;
+  p.cshare = ((a.vocab + c - 1) / c + 63) / 64 * 64;
+  if (a.dtype == W4A16_F32) return go<F32>(p, a.stream);
+  return a.dtype == W4A16_BF16 ? go<BF16>(p, a.stream) : go<F16>(p, a.stream);
+}
+
+}  // namespace w4a16

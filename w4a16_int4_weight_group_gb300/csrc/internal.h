@@ -217,7 +217,7 @@ struct LoraArgs {
 };
 cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev);
 // 0: none is needed
-size_t lora_workspace_bytes(int64_t tokens, int rank, int64_t adapters);
+size_t lora_workspace_bytes(int64_t tokens, int64_t adapters);
 int lora_most_adapters();
 
 struct VerifyArgs {

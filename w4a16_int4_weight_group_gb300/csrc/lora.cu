@@ -55,8 +55,6 @@ struct Params {
   const int32_t *num_tiles;
 };
 
-__device__ __forceinline__ uint4 ld16(const uint16_t *p) { return *reinterpret_cast<const uint4 *>(p); }
-
 // upper and lower part of two numbers, as pairs of the dtype
 template <class DT>
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
@@ -83,25 +81,50 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
   }
 }
 
-template <int MR, int NT>
+// a pair of the dtype plus two sums (times a power of two), each rounded once
+template <class DT>
+__device__ __forceinline__ void add2(uint32_t &w, float a, float b, float f) {
+  if constexpr (DT::kBF16) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(__uint_as_float(w << 16) + a, __uint_as_float(w & 0xFFFF0000u) + b);
+    w = *reinterpret_cast<const uint32_t *>(&r);
+  } else {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    const __half2 r = __floats2half2_rn(fmaf(a, f, x.x), fmaf(b, f, x.y));
+    w = *reinterpret_cast<const uint32_t *>(&r);
+  }
+}
+
+// MR, NT: m-tiles (adapter rows) and n-tiles (tokens) of a warp's first product; RS: parts of the rank, each with its warps
+template <int MR_, int NT_, int RS_, int STAGES, int CTAS>
 struct Shape {
-  static constexpr int kRanks = 16 * MR, kTokens = 8 * NT;
-  static constexpr int kMT = (NT + 1) / 2;      // m-tiles of the second product
-  static constexpr int kChunks = (MR + 1) / 2;  // its k, in steps of 32
+  static constexpr int MR = MR_, NT = NT_, RS = RS_, kCtas = CTAS;
+  static constexpr int kRanks = 16 * MR * RS, kTokens = 8 * NT;
+  static constexpr int kSlices = kWarps / RS;       // parts of K in a CTA
+  static constexpr int kMT = (NT + 1) / 2;          // m-tiles of the second product
+  static constexpr int kHalves = NT == 1 ? 1 : 2;   // (one n-tile fills half an m-tile)
+  static constexpr int kChunks = (MR * RS + 1) / 2; // its k, in steps of 32
   static constexpr int kHStride = kRanks + 4;
-  static constexpr int kPart = kWarps * MR * NT * 32 * 4;  // floats
-  static constexpr int kH = kMT * 16 * kHStride;
-  static constexpr int kFrag = kMT * kChunks * 2 * 2 * 32 * 4;  // words: [m-tile][chunk][step][hi, lo][lane][4]
-  static constexpr int kSmem = (kPart + kH + kFrag) * 4;
+  // 16-byte slots of a thread in a stage of each product's ring
+  static constexpr int kSlots1 = 2 * MR + NT, kSlots2 = kMT * kHalves + 4 * kChunks;
+  static constexpr int kSlots = STAGES * (kSlots1 > kSlots2 ? kSlots1 : kSlots2);
+  static constexpr int kStages1 = kSlots / kSlots1, kStages2 = kSlots / kSlots2;
+  static constexpr int kRing = kSlots * kThreads * 16;  // bytes
+  static constexpr int kSums = MR * RS * NT * 32;       // float4 of a K slice's sums
+  static constexpr int kH = kMT * 16 * kHStride;        // floats
+  static_assert(kSlices * kSums * 16 + kH * 4 <= kRing, "the partial sums and h lie in the ring");
+  static_assert(kStages1 >= 2 && kStages2 >= 2, "one stage is in flight while another is used");
+  static constexpr int kFrag = kMT * kChunks * 2 * 2 * 32 * 16;  // bytes: [m-tile][chunk][step][upper, lower][lane]
+  static constexpr int kSmem = kRing + kFrag;
 };
 
-template <class DT, int MR, int NT, bool SORTED>
-__global__ void __launch_bounds__(kThreads, MR * NT <= 2 ? 3 : 2) lora_kernel(const Params p) {
-  using S = Shape<MR, NT>;
-  extern __shared__ __align__(16) float smem[];
-  float4 *part = reinterpret_cast<float4 *>(smem);  // [warp][MR][NT][lane]
-  float *h = smem + S::kPart;                       // [token][rank]
-  uint32_t *frag = reinterpret_cast<uint32_t *>(h + S::kH);
+template <class DT, class S, bool SORTED>
+__global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p) {
+  constexpr int MR = S::MR, NT = S::NT;
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint4 *ring = reinterpret_cast<uint4 *>(smem) + threadIdx.x;           // this thread's slots, kThreads apart
+  float4 *part = reinterpret_cast<float4 *>(smem);                       // [slice][m-tile][n-tile][lane], in the ring's place
+  float *h = reinterpret_cast<float *>(part + S::kSlices * S::kSums);    // [token][rank], behind it
+  uint4 *frag = reinterpret_cast<uint4 *>(smem + S::kRing);
   __shared__ int tok[S::kTokens];
   __shared__ float back[S::kMT * 16];  // what a token's h was divided by (float16)
   __shared__ int ids_s[SORTED ? 4 : kFewTokens];
@@ -110,6 +133,7 @@ __global__ void __launch_bounds__(kThreads, MR * NT <= 2 ? 3 : 2) lora_kernel(co
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
+  const int slice = warp / S::RS, ranks = warp % S::RS;  // part of K, part of the rank
   const int csize = p.csize;
   const int crank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
@@ -178,62 +202,81 @@ __global__ void __launch_bounds__(kThreads, MR * NT <= 2 ? 3 : 2) lora_kernel(co
       for (int m = 0; m < MR; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-      const uint16_t *xr[NT];
+      // rows in units of 16 bytes; a token past the tile's last is the last one again, a row past the adapter's rank
+      // its last row: neither is used
+      uint32_t xr[NT], ar[MR][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) xr[n] = n * 8 + g < count ? p.x + tok[n * 8 + g] * p.x_stride : nullptr;
-      constexpr int U = MR * NT <= 8 ? 2 : 1;  // steps of 32 whose loads are in flight together
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      for (int64_t k0 = int64_t(crank * kWarps + warp) * (32 * U); k0 < p.K; k0 += int64_t(csize) * kWarps * (32 * U)) {
-        uint4 av[U][MR][2], xv[U][NT];
+      for (int n = 0; n < NT; ++n) xr[n] = static_cast<uint32_t>(tok[min(n * 8 + g, count - 1)] * p.x_stride >> 3);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t k = k0 + u * 32 + t * 8;
-          const bool in = k < p.K;
+      for (int m = 0; m < MR; ++m)
 #pragma unroll
-          for (int m = 0; m < MR; ++m)
+        for (int i = 0; i < 2; ++i) ar[m][i] = static_cast<uint32_t>(min((ranks * MR + m) * 16 + i * 8 + g, p.rank - 1)) * static_cast<uint32_t>(p.K >> 3);
+      const uint4 *x16 = reinterpret_cast<const uint4 *>(p.x), *a16 = reinterpret_cast<const uint4 *>(ap);
+      const uint32_t units = static_cast<uint32_t>(p.K >> 3);  // of 8 elements
+      const uint32_t u0 = (crank * S::kSlices + slice) * 4, step = csize * S::kSlices * 4;
+      const int steps = u0 < units ? static_cast<int>((units - u0 + step - 1) / step) : 0;
+      // loads of step i, into this thread's own slots: no barrier between them and their use
+      auto fetch = [&](int i) {
+        const uint32_t k = u0 + i * step + t;
+        const bool in = k < units;
+        const uint32_t kk = in ? k : 0;
+        const uint32_t at = smem_u32(ring + (i % S::kStages1) * S::kSlots1 * kThreads);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int row = m * 16 + i * 8 + g;
-              av[u][m][i] = in && row < p.rank ? ld16(ap + row * p.K + k) : zero;
-            }
+        for (int n = 0; n < NT; ++n)
+          if (NT == 1 || n * 8 < count) cp_async_16(at + n * (kThreads * 16), x16 + (xr[n] + kk), in);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) xv[u][n] = in && xr[n] ? ld16(xr[n] + k) : zero;
-        }
+        for (int m = 0; m < MR; ++m)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+          for (int i2 = 0; i2 < 2; ++i2) cp_async_16(at + (NT + m * 2 + i2) * (kThreads * 16), a16 + (ar[m][i2] + kk), in);
+      };
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (NT > 1 && n * 8 >= count) break;
-#pragma unroll
-            for (int m = 0; m < MR; ++m) {
-              const uint4 v0 = av[u][m][0], v1 = av[u][m][1];
-              const uint32_t f0[4] = {v0.x, v1.x, v0.y, v1.y}, f1[4] = {v0.z, v1.z, v0.w, v1.w};
-              mma_16816<DT::kBF16>(acc[m][n], f0, xv[u][n].x, xv[u][n].y);
-              mma_16816<DT::kBF16>(acc[m][n], f1, xv[u][n].z, xv[u][n].w);
-            }
-          }
+      for (int i = 0; i < S::kStages1 - 1; ++i) {
+        if (i < steps) fetch(i);
+        cp_async_commit();
       }
+      for (int i = 0; i < steps; ++i) {
+        cp_async_wait<S::kStages1 - 2>();
+        const uint4 *at = ring + (i % S::kStages1) * S::kSlots1 * kThreads;
+        uint4 av[MR][2];
+#pragma unroll
+        for (int m = 0; m < MR; ++m) av[m][0] = at[(NT + m * 2) * kThreads], av[m][1] = at[(NT + m * 2 + 1) * kThreads];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (NT > 1 && n * 8 >= count) break;
+          const uint4 xv = at[n * kThreads];
+#pragma unroll
+          for (int m = 0; m < MR; ++m) {
+            const uint4 v0 = av[m][0], v1 = av[m][1];
+            const uint32_t f0[4] = {v0.x, v1.x, v0.y, v1.y}, f1[4] = {v0.z, v1.z, v0.w, v1.w};
+            mma_16816<DT::kBF16>(acc[m][n], f0, xv.x, xv.y);
+            mma_16816<DT::kBF16>(acc[m][n], f1, xv.z, xv.w);
+          }
+        }
+        if (i + S::kStages1 - 1 < steps) fetch(i + S::kStages1 - 1);
+        cp_async_commit();
+      }
+      __syncthreads();  // the ring is not read any more (every load of it was waited for)
 #pragma unroll
       for (int m = 0; m < MR; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          part[((warp * MR + m) * NT + n) * 32 + lane] = make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
+          part[slice * S::kSums + ((ranks * MR + m) * NT + n) * 32 + lane] = make_float4(acc[m][n][0], acc[m][n][1], acc[m][n][2], acc[m][n][3]);
     }
     __syncthreads();
     const float s = adapter >= 0 ? (p.scales ? p.scales[adapter] : 1.f) : 0.f;
     if (adapter >= 0) {
-      // the warps' sums, then the CTAs', each in order
-      for (int e = tid; e < MR * NT * 32; e += kThreads) {
+      // the slices' sums, then the CTAs', each in order
+      for (int e = tid; e < S::kSums; e += kThreads) {
         float4 v = part[e];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-          const float4 o = part[w * MR * NT * 32 + e];
+        for (int w = 1; w < S::kSlices; ++w) {
+          const float4 o = part[w * S::kSums + e];
           v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
         }
         part[e] = v;
       }
       if (csize > 1) cluster_sync_all();
-      for (int e = tid; e < MR * NT * 32; e += kThreads) {
+      for (int e = tid; e < S::kSums; e += kThreads) {
         float4 v = part[e];
         if (csize > 1) {
           const uint32_t mine = smem_u32(&part[e]);
@@ -251,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, MR * NT <= 2 ? 3 : 2) lora_kernel(co
       if constexpr (!DT::kBF16) {  // power of two that brings a token's largest to [2^13, 2^14)
         for (int i = warp; i < S::kTokens; i += kWarps) {
           float top = 0.f;
-          for (int r = lane; r < S::kRanks; r += 32) top = fmaxf(top, fabsf(h[i * S::kHStride + r]));  // (a NaN does not count)
+          for (int r = lane; r < p.rank; r += 32) top = fmaxf(top, fabsf(h[i * S::kHStride + r]));  // (a NaN does not count)
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
           const int e = static_cast<int>(__float_as_uint(top) >> 23);  // 0: zero or subnormal; 255: infinite
@@ -271,44 +314,73 @@ __global__ void __launch_bounds__(kThreads, MR * NT <= 2 ? 3 : 2) lora_kernel(co
           if constexpr (!DT::kBF16) f = in ? 1.f / back[row] : 1.f;  // (exact: a power of two)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const bool ok = in && r0 + 2 * j < S::kRanks;
+            const bool ok = in && r0 + 2 * j < p.rank;  // (rank is even)
             const float v0 = ok ? h[row * S::kHStride + r0 + 2 * j] * f : 0.f, v1 = ok ? h[row * S::kHStride + r0 + 2 * j + 1] * f : 0.f;
             split2<DT>(v0, v1, hi[i][j], lo[i][j]);
           }
         }
-        uint4 *at = reinterpret_cast<uint4 *>(frag) + ((m * S::kChunks + c) * 4) * 32 + l;
+        uint4 *at = frag + ((m * S::kChunks + c) * 4) * 32 + l;
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
           at[(st * 2) * 32] = make_uint4(hi[0][2 * st], hi[1][2 * st], hi[0][2 * st + 1], hi[1][2 * st + 1]);
           at[(st * 2 + 1) * 32] = make_uint4(lo[0][2 * st], lo[1][2 * st], lo[0][2 * st + 1], lo[1][2 * st + 1]);
         }
       }
-      __syncthreads();
+      // the ring takes the second product's loads: the partial sums in its place were read by the whole cluster
+      if (csize > 1) cluster_sync_all();
+      else __syncthreads();
     }
 
     // ---- second product: out = base + h B^T, N split over the cluster's warps in groups of 32 columns
-    for (int64_t n0 = int64_t(crank * kWarps + warp) * 32; n0 < p.N; n0 += int64_t(csize) * kWarps * 32) {
-      uint4 bv[4][S::kChunks];
-      if (adapter >= 0) {
+    const uint32_t n_units = static_cast<uint32_t>(p.N >> 3), r_units = p.rank >> 3;
+    const uint4 *b16 = reinterpret_cast<const uint4 *>(bp), *base16 = reinterpret_cast<const uint4 *>(p.base);
+    uint4 *out16 = reinterpret_cast<uint4 *>(p.out);
+    const uint32_t c0 = (crank * kWarps + warp) * 4, cstep = csize * kWarps * 4;  // in units of 8 columns
+    const int groups = c0 < n_units ? static_cast<int>((n_units - c0 + cstep - 1) / cstep) : 0;
+    auto fetch = [&](int i) {
+      const uint32_t n0 = c0 + i * cstep, col = n0 + t;
+      const uint32_t at = smem_u32(ring + (i % S::kStages2) * S::kSlots2 * kThreads);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t col = n0 + (g >> 1) * 8 + 2 * j + (g & 1);
+      for (int m = 0; m < S::kMT; ++m)
+#pragma unroll
+        for (int i2 = 0; i2 < S::kHalves; ++i2) {
+          const int row = m * 16 + i2 * 8 + g;
+          if (col < n_units && row < count)
+            cp_async_16(at + (m * S::kHalves + i2) * (kThreads * 16), base16 + ((tok[row] * p.base_stride >> 3) + col), true);
+        }
+      if (adapter >= 0) {
+        const bool has = n0 + (g >> 1) < n_units;
+        const uint32_t brow = has ? n0 * 8 + (g >> 1) * 8 + (g & 1) : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int c = 0; c < S::kChunks; ++c) {
-            const int r0 = c * 32 + t * 8;
-            bv[j][c] = col < p.N && r0 < p.rank ? ld16(bp + col * p.rank + r0) : make_uint4(0, 0, 0, 0);
+            const bool in = has && c * 4 + t < r_units;
+            cp_async_16(at + (S::kMT * S::kHalves + j * S::kChunks + c) * (kThreads * 16),
+                        b16 + (in ? uint64_t(brow + 2 * j) * r_units + c * 4 + t : 0), in);
           }
-        }
       }
-      const int64_t col = n0 + t * 8;
+    };
+#pragma unroll
+    for (int i = 0; i < S::kStages2 - 1; ++i) {
+      if (i < groups) fetch(i);
+      cp_async_commit();
+    }
+    for (int i = 0; i < groups; ++i) {
+      cp_async_wait<S::kStages2 - 2>();
+      const uint32_t col = c0 + i * cstep + t;
+      const bool in = col < n_units;
+      const uint4 *at = ring + (i % S::kStages2) * S::kSlots2 * kThreads;
+      uint4 bv[4][S::kChunks];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int c = 0; c < S::kChunks; ++c) bv[j][c] = at[(S::kMT * S::kHalves + j * S::kChunks + c) * kThreads];
 #pragma unroll
       for (int m = 0; m < S::kMT; ++m) {
         if (m * 16 >= count) break;
         const int i0 = m * 16 + g, i1 = i0 + 8;
-        const bool in0 = i0 < count && col < p.N, in1 = i1 < count && col < p.N;
-        uint4 o0 = make_uint4(0, 0, 0, 0), o1 = o0;
-        if (in0) o0 = ld16(p.base + tok[i0] * p.base_stride + col);
-        if (in1) o1 = ld16(p.base + tok[i1] * p.base_stride + col);
+        uint4 o0 = at[m * S::kHalves * kThreads], o1 = at[(m * S::kHalves + S::kHalves - 1) * kThreads];
         if (adapter >= 0) {
           float acc[4][4];
 #pragma unroll
@@ -317,8 +389,8 @@ __global__ void __launch_bounds__(kThreads, MR * NT <= 2 ? 3 : 2) lora_kernel(co
           for (int c = 0; c < S::kChunks; ++c)
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
-              const uint4 *at = reinterpret_cast<const uint4 *>(frag) + ((m * S::kChunks + c) * 4 + st * 2) * 32 + lane;
-              const uint4 hi = at[0], lo = at[32];
+              const uint4 *f = frag + ((m * S::kChunks + c) * 4 + st * 2) * 32 + lane;
+              const uint4 hi = f[0], lo = f[32];
               const uint32_t fh[4] = {hi.x, hi.y, hi.z, hi.w}, fl[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
@@ -329,25 +401,18 @@ __global__ void __launch_bounds__(kThreads, MR * NT <= 2 ? 3 : 2) lora_kernel(co
             }
           float f0 = 1.f, f1 = 1.f;
           if constexpr (!DT::kBF16) f0 = back[i0 < S::kTokens ? i0 : 0], f1 = back[i1 < S::kTokens ? i1 : 0];
-          auto add = [&](uint32_t &w, float a, float b, float f) {
-            typename DT::T lo16, hi16;
-            const float x = bits_to_float(static_cast<uint16_t>(w & 0xFFFF), DT::kBF16), y = bits_to_float(static_cast<uint16_t>(w >> 16), DT::kBF16);
-            lo16 = DT::from_float_rn(fmaf(a, f, x));
-            hi16 = DT::from_float_rn(fmaf(b, f, y));
-            w = static_cast<uint32_t>(*reinterpret_cast<uint16_t *>(&lo16)) | static_cast<uint32_t>(*reinterpret_cast<uint16_t *>(&hi16)) << 16;
-          };
-          add(o0.x, acc[0][0], acc[0][1], f0), add(o1.x, acc[0][2], acc[0][3], f1);
-          add(o0.y, acc[1][0], acc[1][1], f0), add(o1.y, acc[1][2], acc[1][3], f1);
-          add(o0.z, acc[2][0], acc[2][1], f0), add(o1.z, acc[2][2], acc[2][3], f1);
-          add(o0.w, acc[3][0], acc[3][1], f0), add(o1.w, acc[3][2], acc[3][3], f1);
+          add2<DT>(o0.x, acc[0][0], acc[0][1], f0), add2<DT>(o1.x, acc[0][2], acc[0][3], f1);
+          add2<DT>(o0.y, acc[1][0], acc[1][1], f0), add2<DT>(o1.y, acc[1][2], acc[1][3], f1);
+          add2<DT>(o0.z, acc[2][0], acc[2][1], f0), add2<DT>(o1.z, acc[2][2], acc[2][3], f1);
+          add2<DT>(o0.w, acc[3][0], acc[3][1], f0), add2<DT>(o1.w, acc[3][2], acc[3][3], f1);
         }
-        if (in0) *reinterpret_cast<uint4 *>(p.out + tok[i0] * p.out_stride + col) = o0;
-        if (in1) *reinterpret_cast<uint4 *>(p.out + tok[i1] * p.out_stride + col) = o1;
+        if (in && i0 < count) __stcs(out16 + (tok[i0] * p.out_stride >> 3) + col, o0);
+        if (S::kHalves == 2 && in && i1 < count) __stcs(out16 + (tok[i1] * p.out_stride >> 3) + col, o1);
       }
+      if (i + S::kStages2 - 1 < groups) fetch(i + S::kStages2 - 1);
+      cp_async_commit();
     }
-    // the cluster's partial sums have been read, and this CTA is done with its tile's tables
-    if (csize > 1) cluster_sync_all();
-    else __syncthreads();
+    __syncthreads();  // done with the tile's tables and the ring
   }
 }
 
@@ -365,11 +430,17 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *
     const int id = ids[i];
     return id < 0 || id >= adapters ? adapters : id;
   };
-  // lanes with the same key add once
-  for (int i = tid; i - lane < tokens; i += kSortThreads) {
-    const int k = i < tokens ? key(i) : -1;
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, k);
-    if (k >= 0 && lane == __ffs(same) - 1) atomicAdd(&counts[k], __popc(same));
+  // lanes with the same key add once; the loads of eight steps are in flight together
+  constexpr int kBatch = 8;
+  for (int i0 = tid; i0 - lane < tokens; i0 += kSortThreads * kBatch) {
+    int k[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) k[j] = i0 + j * kSortThreads < tokens ? key(i0 + j * kSortThreads) : -1;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, k[j]);
+      if (k[j] >= 0 && lane == __ffs(same) - 1) atomicAdd(&counts[k[j]], __popc(same));
+    }
   }
   __syncthreads();
   // places of each adapter's tokens and tiles: exclusive sums over the adapters, in chunks of one a thread
@@ -402,32 +473,35 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *
     __syncthreads();
   }
   if (tid == 0) *num_tiles = tiles_before;
-  for (int i = tid; i - lane < tokens; i += kSortThreads) {
-    const int k = i < tokens ? key(i) : -1;
-    const unsigned same = __match_any_sync(0xFFFFFFFFu, k);
-    const int leader = __ffs(same) - 1;
-    int at = 0;
-    if (k >= 0 && lane == leader) at = atomicAdd(&counts[k], __popc(same));
-    at = __shfl_sync(0xFFFFFFFFu, at, leader);
-    if (k >= 0) order[at + __popc(same & ((1u << lane) - 1))] = i;
+  for (int i0 = tid; i0 - lane < tokens; i0 += kSortThreads * kBatch) {
+    int k[kBatch], at[kBatch];
+    unsigned same[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) k[j] = i0 + j * kSortThreads < tokens ? key(i0 + j * kSortThreads) : -1;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      same[j] = __match_any_sync(0xFFFFFFFFu, k[j]);
+      at[j] = 0;
+      if (k[j] >= 0 && lane == __ffs(same[j]) - 1) at[j] = atomicAdd(&counts[k[j]], __popc(same[j]));
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int first = __shfl_sync(0xFFFFFFFFu, at[j], __ffs(same[j]) - 1);
+      if (k[j] >= 0) order[first + __popc(same[j] & ((1u << lane) - 1))] = i0 + j * kSortThreads;
+    }
   }
 }
 
-// Tokens of a tile: as many as the accumulators of the first product leave room for
-int tile_tokens(int rank, bool few) {
-  if (few) return 8;
-  return rank <= 32 ? 64 : rank <= 64 ? 32 : 16;
-}
-int64_t most_tiles(int64_t tokens, int rank, int64_t adapters) {
-  return tokens / tile_tokens(rank, false) + std::min<int64_t>(tokens, adapters + 1);
+constexpr int kSortedTile = 64;  // tokens
+int64_t most_tiles(int64_t tokens, int64_t adapters) {
+  return tokens / kSortedTile + std::min<int64_t>(tokens, adapters + 1);
 }
 
-template <class DT, int MR, int NT, bool SORTED>
-cudaError_t go(Params p, int64_t tiles, int num_sms, cudaStream_t stream) {
-  using S = Shape<MR, NT>;
-  constexpr int kCtas = MR * NT <= 2 ? 3 : 2;  // on an SM
+template <class DT, class S, bool SORTED>
+cudaError_t go(Params p, int64_t tiles, int64_t most, int num_sms, cudaStream_t stream) {
+  constexpr int kCtas = S::kCtas;  // on an SM
   static std::atomic<bool> asked[64];  // dynamic shared memory past 48 KB is asked for once a device
-  auto kernel = lora_kernel<DT, MR, NT, SORTED>;
+  auto kernel = lora_kernel<DT, S, SORTED>;
   if (S::kSmem > 48 * 1024) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -442,7 +516,7 @@ cudaError_t go(Params p, int64_t tiles, int num_sms, cudaStream_t stream) {
   int c = 1;
   while (c < 8 && tiles * c * 2 <= int64_t(kCtas) * num_sms) c *= 2;
   p.csize = c;
-  const int64_t clusters = std::min<int64_t>(tiles, int64_t(kCtas) * num_sms / c);
+  const int64_t clusters = std::min<int64_t>(most, int64_t(kCtas) * num_sms / c);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * c), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -466,25 +540,25 @@ cudaError_t go(Params p, int64_t tiles, int num_sms, cudaStream_t stream) {
 }
 
 template <class DT>
-cudaError_t run(const Params &p, bool few, int64_t tiles, int num_sms, cudaStream_t stream) {
+cudaError_t run(const Params &p, bool few, int64_t tiles, int64_t most, int num_sms, cudaStream_t stream) {
   const int r = p.rank;
   if (few) {
-    if (r <= 16) return go<DT, 1, 1, false>(p, tiles, num_sms, stream);
-    if (r <= 32) return go<DT, 2, 1, false>(p, tiles, num_sms, stream);
-    if (r <= 64) return go<DT, 4, 1, false>(p, tiles, num_sms, stream);
-    return go<DT, 8, 1, false>(p, tiles, num_sms, stream);
+    if (r <= 16) return go<DT, Shape<1, 1, 1, 3, 3>, false>(p, tiles, most, num_sms, stream);
+    if (r <= 32) return go<DT, Shape<2, 1, 1, 3, 3>, false>(p, tiles, most, num_sms, stream);
+    if (r <= 64) return go<DT, Shape<4, 1, 1, 3, 2>, false>(p, tiles, most, num_sms, stream);
+    return go<DT, Shape<4, 1, 2, 2, 1>, false>(p, tiles, most, num_sms, stream);
   }
-  if (r <= 16) return go<DT, 1, 8, true>(p, tiles, num_sms, stream);
-  if (r <= 32) return go<DT, 2, 8, true>(p, tiles, num_sms, stream);
-  if (r <= 64) return go<DT, 4, 4, true>(p, tiles, num_sms, stream);
-  return go<DT, 8, 2, true>(p, tiles, num_sms, stream);
+  if (r <= 16) return go<DT, Shape<1, 8, 1, 2, 2>, true>(p, tiles, most, num_sms, stream);
+  if (r <= 32) return go<DT, Shape<2, 8, 1, 2, 2>, true>(p, tiles, most, num_sms, stream);
+  if (r <= 64) return go<DT, Shape<4, 8, 1, 3, 1>, true>(p, tiles, most, num_sms, stream);
+  return go<DT, Shape<4, 8, 2, 2, 1>, true>(p, tiles, most, num_sms, stream);
 }
 
 }  // namespace
 
-size_t lora_workspace_bytes(int64_t tokens, int rank, int64_t adapters) {
+size_t lora_workspace_bytes(int64_t tokens, int64_t adapters) {
   if (tokens <= kFewTokens) return 0;
-  return 4096 + 256 + static_cast<size_t>((tokens * 4 + 255) / 256 * 256) + static_cast<size_t>(most_tiles(tokens, rank, adapters)) * sizeof(Tile);
+  return 4096 + 256 + static_cast<size_t>((tokens * 4 + 255) / 256 * 256) + static_cast<size_t>(most_tiles(tokens, adapters)) * sizeof(Tile);
 }
 int lora_most_adapters() { return kMaxAdapters; }
 
@@ -507,7 +581,7 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
   p.adapters = static_cast<int>(a.adapters);
   p.copy = a.base != a.out;
   const bool few = a.tokens <= kFewTokens;
-  int64_t tiles = a.tokens;
+  int64_t tiles = a.tokens, most = a.tokens;  // as far as can be told here, and at most
   if (!few) {
     // (past the first 4 KiB: the counters of other calls)
     uint8_t *ws = static_cast<uint8_t *>(a.workspace) + 4096;
@@ -516,8 +590,9 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
     Tile *list = reinterpret_cast<Tile *>(ws + 256 + (a.tokens * 4 + 255) / 256 * 256);
     p.num_tiles = num;
     p.tiles = list;
-    const int per = tile_tokens(a.rank, false);
-    tiles = (a.tokens + per - 1) / per;
+    const int per = kSortedTile;
+    tiles = (a.tokens + per - 1) / per + std::min<int64_t>(a.adapters, a.tokens / 2) / 2;
+    most = most_tiles(a.tokens, a.adapters);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
@@ -532,7 +607,7 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
     if (e != cudaSuccess) return e;
     note_launch();
   }
-  return a.dtype == W4A16_BF16 ? run<BF16>(p, few, tiles, dev.num_sms, a.stream) : run<F16>(p, few, tiles, dev.num_sms, a.stream);
+  return a.dtype == W4A16_BF16 ? run<BF16>(p, few, tiles, most, dev.num_sms, a.stream) : run<F16>(p, few, tiles, most, dev.num_sms, a.stream);
 }
 
 }  // namespace w4a16

@@ -17,8 +17,8 @@ Range rows_range(const void *p, int64_t rows, int64_t stride, int64_t cols, int 
 // A matrix of 16-bit elements that the kernels read in vectors: contiguous rows that share no elements
 w4a16_status check_rows(const void *p, int64_t rows, int64_t stride, int64_t cols, const char *name) {
   if (!p) return fail(W4A16_ERR_INVALID_ARG, "%s must not be NULL", name);
-  if (rows > 1 && (stride < cols || stride >= (int64_t(1) << 31)))
-    return fail(W4A16_ERR_INVALID_ARG, "%s: a row stride of %lld does not hold rows of %lld elements (or is 2^31 and more)", name,
+  if (rows > 1 && (stride < cols || stride >= (int64_t(1) << 35) / rows))
+    return fail(W4A16_ERR_INVALID_ARG, "%s: a row stride of %lld does not hold rows of %lld elements, or all rows span 2^35 elements and more", name,
                 (long long)stride, (long long)cols);
   if (!aligned(p, 16) || (rows > 1 && stride % 8 != 0))
     return fail(W4A16_ERR_MISALIGNED, "%s must be 16-byte aligned, its row stride a multiple of 8 elements", name);
@@ -77,7 +77,7 @@ extern "C" {
 
 size_t w4a16_lora_workspace_size(int64_t tokens, int rank, int64_t adapters) {
   if (tokens < 0 || tokens >= kMaxTokens || rank < 1 || rank > kMaxRank || adapters < 1 || adapters > lora_most_adapters()) return 0;
-  return lora_workspace_bytes(tokens, rank, adapters);
+  return lora_workspace_bytes(tokens, adapters);
 }
 
 w4a16_status w4a16_lora(const void *x, int64_t x_stride, const void *a, const void *b, const int32_t *ids, const float *scales, const void *base,
@@ -101,7 +101,7 @@ w4a16_status w4a16_lora(const void *x, int64_t x_stride, const void *a, const vo
   if (!a || !b || !ids) return fail(W4A16_ERR_INVALID_ARG, "a, b and ids must not be NULL");
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(ids, 4) || !aligned(scales, 4))
     return fail(W4A16_ERR_MISALIGNED, "a and b must be 16-byte, ids and scales 4-byte aligned");
-  const size_t need = lora_workspace_bytes(tokens, rank, adapters);
+  const size_t need = lora_workspace_bytes(tokens, adapters);
   if (need && (!workspace || workspace_bytes < need))
     return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : size_t(0), need);
   if (workspace && !aligned(workspace, 256)) return fail(W4A16_ERR_MISALIGNED, "workspace must be 256-byte aligned");

@@ -267,6 +267,6 @@ struct CompactArgs {
   int max_q;
   int32_t *new_lens;
 };
-cudaError_t launch_kv_compact(const CompactArgs &a, cudaStream_t stream);
+cudaError_t launch_kv_compact(const CompactArgs &a, int num_sms, cudaStream_t stream);
 
 }  // namespace w4a16

@@ -33,6 +33,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kFewTokens = 256;  // one thread for each
+constexpr int kFewTile = 8;      // tokens of a tile then
 constexpr int kSortThreads = 1024;
 constexpr int kMaxAdapters = 8191;  // counters of the sort in shared memory
 
@@ -581,7 +582,8 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
   p.adapters = static_cast<int>(a.adapters);
   p.copy = a.base != a.out;
   const bool few = a.tokens <= kFewTokens;
-  int64_t tiles = a.tokens, most = a.tokens;  // as far as can be told here, and at most
+  // tiles, as far as can be told here, and at most
+  int64_t tiles = std::min<int64_t>(a.tokens, a.tokens / kFewTile + a.adapters), most = a.tokens;
   if (!few) {
     // (past the first 4 KiB: the counters of other calls)
     uint8_t *ws = static_cast<uint8_t *>(a.workspace) + 4096;

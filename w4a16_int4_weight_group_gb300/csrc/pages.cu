@@ -18,7 +18,7 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kMaxQ = 64;
+constexpr int kMaxQ = 64;  // drafted tokens of a sequence
 constexpr int kMaxSequences = 4096;  // of one reserve: their tables are in shared memory
 constexpr int kReserveThreads = 1024;
 constexpr int kCopyThreads = 256;
@@ -217,13 +217,13 @@ struct CompactParams {
   const int32_t *table, *lens, *q_start, *path;
   int max_q;
   int32_t *new_lens;
+  int layers, each;  // each: layers of a CTA
 };
 constexpr int kCompactThreads = 128;
-constexpr int kMaxCode = 256;
+constexpr int kCompactSmem = 34 * 1024;  // 64 tokens of 512 + 8 bytes: one layer always fits
 
 __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactParams p) {
-  __shared__ __align__(16) uint8_t codes[kMaxQ * 2 * kMaxCode];
-  __shared__ uint32_t params[kMaxQ][2];
+  extern __shared__ __align__(16) uint8_t rows[];  // codes [layer][token][2 code_bytes], then parameters [layer][token][2]
   __shared__ int64_t src[kMaxQ], dst[kMaxQ];  // tiles' first bytes, within a layer
   __shared__ int src_row[kMaxQ], dst_row[kMaxQ];
   __shared__ int moved, kept;
@@ -263,30 +263,31 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactP
     }
   }
   __syncthreads();
-  uint8_t *layer = p.cache + blockIdx.z * p.layer_bytes;
   const int units = 2 * p.code_bytes / 16, half = p.code_bytes / 16;
-  const int m = moved;
-  for (int e = tid; e < m * units; e += kCompactThreads) {
-    const int i = e / units, u = e % units, kind = u >= half;
-    reinterpret_cast<uint4 *>(codes)[e] =
-        *reinterpret_cast<const uint4 *>(layer + src[i] + kind * 16 * p.code_bytes + src_row[i] * p.code_bytes + (u - kind * half) * 16);
-  }
-  for (int e = tid; e < m * 2; e += kCompactThreads)
-    params[e >> 1][e & 1] = *reinterpret_cast<const uint32_t *>(layer + src[e >> 1] + 32 * p.code_bytes + (e & 1) * 64 + src_row[e >> 1] * 4);
+  const int m = moved, first = blockIdx.z * p.each, layers = min(p.each, p.layers - first);
+  uint8_t *cache = p.cache + first * p.layer_bytes;
+  uint4 *codes = reinterpret_cast<uint4 *>(rows);
+  uint32_t *params = reinterpret_cast<uint32_t *>(rows + p.each * p.max_q * 2 * p.code_bytes);
+  auto code_at = [&](int e, const int64_t *tile, const int *row) {  // of vector e: layer, token, unit
+    const int u = e % units, i = e / units % m, kind = u >= half;
+    return reinterpret_cast<uint4 *>(cache + e / units / m * p.layer_bytes + tile[i] + (kind * 16 + row[i]) * p.code_bytes + (u - kind * half) * 16);
+  };
+  auto param_at = [&](int e, const int64_t *tile, const int *row) {
+    const int i = e / 2 % m;
+    return reinterpret_cast<uint32_t *>(cache + e / 2 / m * p.layer_bytes + tile[i] + 32 * p.code_bytes + (e & 1) * 64 + row[i] * 4);
+  };
+  for (int e = tid; e < layers * m * units; e += kCompactThreads) codes[e] = *code_at(e, src, src_row);
+  for (int e = tid; e < layers * m * 2; e += kCompactThreads) params[e] = *param_at(e, src, src_row);
   __syncthreads();
-  for (int e = tid; e < m * units; e += kCompactThreads) {
-    const int i = e / units, u = e % units, kind = u >= half;
-    *reinterpret_cast<uint4 *>(layer + dst[i] + kind * 16 * p.code_bytes + dst_row[i] * p.code_bytes + (u - kind * half) * 16) =
-        reinterpret_cast<const uint4 *>(codes)[e];
-  }
-  for (int e = tid; e < m * 2; e += kCompactThreads)
-    *reinterpret_cast<uint32_t *>(layer + dst[e >> 1] + 32 * p.code_bytes + (e & 1) * 64 + dst_row[e >> 1] * 4) = params[e >> 1][e & 1];
+  for (int e = tid; e < layers * m * units; e += kCompactThreads) *code_at(e, dst, dst_row) = codes[e];
+  for (int e = tid; e < layers * m * 2; e += kCompactThreads) *param_at(e, dst, dst_row) = params[e];
   if (blockIdx.x == 0 && blockIdx.z == 0 && tid == 0) p.new_lens[b] = static_cast<int32_t>(max(place0 + min(count, n), int64_t(0)));
 }
 
 template <class... P, class... A>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.stream = stream;
@@ -308,14 +309,14 @@ int kv_reserve_most_sequences() { return kMaxSequences; }
 
 cudaError_t launch_kv_fork(const PoolArgs &a, const int32_t *table, const int32_t *lens, int64_t batch, const int32_t *parents, int64_t rows,
                            int32_t *new_table, int32_t *new_lens, cudaStream_t stream) {
-  return launch(fork_kernel, dim3(static_cast<unsigned>(rows)), 256, stream, pool_of(a), table, lens, batch, parents, new_table, new_lens);
+  return launch(fork_kernel, dim3(static_cast<unsigned>(rows)), 256, 0, stream, pool_of(a), table, lens, batch, parents, new_table, new_lens);
 }
 cudaError_t launch_kv_free(const PoolArgs &a, int32_t *table, const int32_t *lens, const int32_t *keep, int64_t batch, cudaStream_t stream) {
-  return launch(free_kernel, dim3(static_cast<unsigned>(batch)), 256, stream, pool_of(a), table, lens, keep);
+  return launch(free_kernel, dim3(static_cast<unsigned>(batch)), 256, 0, stream, pool_of(a), table, lens, keep);
 }
 cudaError_t launch_kv_reserve(const PoolArgs &a, int32_t *table, const int32_t *lens, const int32_t *new_lens, int64_t batch, int32_t *held,
                               int32_t *copies, cudaStream_t stream) {
-  return launch(reserve_kernel, dim3(1), kReserveThreads, stream, pool_of(a), table, lens, new_lens, static_cast<int>(batch), held,
+  return launch(reserve_kernel, dim3(1), kReserveThreads, 0, stream, pool_of(a), table, lens, new_lens, static_cast<int>(batch), held,
                 reinterpret_cast<int2 *>(copies));
 }
 cudaError_t launch_kv_copy(const w4a16_kv_cache_t &c, int64_t layers, const int32_t *pairs, int64_t n, cudaStream_t stream) {
@@ -324,13 +325,13 @@ cudaError_t launch_kv_copy(const w4a16_kv_cache_t &c, int64_t layers, const int3
   for (int64_t done = 0; done < n; done += 65535) {
     const int64_t m = std::min<int64_t>(n - done, 65535);
     const cudaError_t e = launch(copy_kernel, dim3(static_cast<unsigned>(parts), static_cast<unsigned>(m), static_cast<unsigned>(layers)),
-                                 kCopyThreads, stream, static_cast<uint8_t *>(c.data), c.num_pages * page_bytes, page_bytes,
+                                 kCopyThreads, 0, stream, static_cast<uint8_t *>(c.data), c.num_pages * page_bytes, page_bytes,
                                  static_cast<int>(c.num_pages), reinterpret_cast<const int2 *>(pairs) + done);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
-cudaError_t launch_kv_compact(const CompactArgs &a, cudaStream_t stream) {
+cudaError_t launch_kv_compact(const CompactArgs &a, int num_sms, cudaStream_t stream) {
   const w4a16_kv_cache_t &c = a.cache;
   CompactParams p{};
   p.cache = static_cast<uint8_t *>(c.data);
@@ -346,10 +347,19 @@ cudaError_t launch_kv_compact(const CompactArgs &a, cudaStream_t stream) {
   p.path = a.path;
   p.max_q = a.max_q;
   p.new_lens = a.new_lens;
+  // Several layers a CTA, which share the look-up of the places and have their loads in flight together, while the rows fit and
+  // the CTAs fill the device (eight of 128 threads on an SM)
+  const int row_bytes = 2 * p.code_bytes + 8;
+  const int64_t ctas = a.batch * c.kv_heads;
+  p.layers = static_cast<int>(a.layers);
+  p.each = 1;
+  while (p.each < p.layers && p.each * 2 * a.max_q * row_bytes <= kCompactSmem && ctas * (p.layers / (p.each * 2)) >= 8 * num_sms) p.each *= 2;
+  const size_t smem = static_cast<size_t>(p.each) * a.max_q * row_bytes;
+  const unsigned parts = static_cast<unsigned>((p.layers + p.each - 1) / p.each);
   for (int64_t done = 0; done < a.batch; done += 65535) {
     const int64_t m = std::min<int64_t>(a.batch - done, 65535);
-    const cudaError_t e = launch(compact_kernel, dim3(static_cast<unsigned>(c.kv_heads), static_cast<unsigned>(m), static_cast<unsigned>(a.layers)),
-                                 kCompactThreads, stream, p);
+    const cudaError_t e = launch(compact_kernel, dim3(static_cast<unsigned>(c.kv_heads), static_cast<unsigned>(m), parts),
+                                 kCompactThreads, smem, stream, p);
     if (e != cudaSuccess) return e;
     p.table += m * a.max_pages;
     p.lens += m;

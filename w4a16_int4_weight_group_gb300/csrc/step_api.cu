@@ -263,8 +263,11 @@ w4a16_status w4a16_kv_compact(const w4a16_kv_cache_t *cache, int64_t layers, con
                       range(path, batch * max_q * 4)};
   const Range written[] = {layers_range(*cache, layers), range(new_lens, batch * 4)};
   if (conflict(written, in)) return fail(W4A16_ERR_INVALID_ARG, "the cache or new_lens overlaps an input, or each other");
-  const cudaError_t e = launch_kv_compact(CompactArgs{*cache, layers, page_table, max_pages, kv_lens, q_start, path, batch, max_q, new_lens},
-                                          as_stream(stream));
+  DeviceInfo dev;
+  cudaError_t e = current_device_info(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "device query");
+  e = launch_kv_compact(CompactArgs{*cache, layers, page_table, max_pages, kv_lens, q_start, path, batch, max_q, new_lens}, dev.num_sms,
+                        as_stream(stream));
   if (e != cudaSuccess) return cuda_fail(e, "w4a16_kv_compact launch");
   return ok();
 }

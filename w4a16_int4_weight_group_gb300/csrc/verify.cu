@@ -12,10 +12,9 @@
 // the last bits of a sum over the vocabulary, nor on the order in which that is added.
 //
 // Two kernels. The first reads every row once: running maximum and sum of exponentials, rows split over CTAs when
-// they are few. The second has a cluster for each sequence: a thread for each token finds its parent, gathers p(d) and q(d) and
-// looks for an earlier sibling of the same token; one thread walks down the tree (a single pass over the tokens, as a
-// parent comes before its children); then the cluster's CTAs take a part of the vocabulary each, of the last node's row
-// alone. Whether a token was rejected is only looked up for the ratios that exceed a thread's best so far.
+// they are few. The second has a cluster for each sequence: a thread for each token finds its parent and gathers p(d) and q(d); four
+// threads for each token look at its siblings, so that every node knows the child that would stand there; the walk down the tree only
+// follows these. Then the cluster's CTAs take a part of the vocabulary each, of the last node's row alone. Whether a token was rejected is only looked up for the ratios that exceed a thread's best so far.
 //
 // Bound by memory in the first kernel, by the latency of its chain of small steps in the second.
 #include <algorithm>
@@ -28,16 +27,67 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStatCtas = 6;   // on an SM
+constexpr int kStatCtas = 4;   // on an SM
 constexpr int kMaxQ = 64;
 constexpr int kMaxSplits = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFar = -1.0e4f;  // exp2(kFar) is zero; keeps infinities out of differences
 
+// Two fp32 numbers in one 64-bit register pair
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 struct F32 {};
 template <class DT>
 struct Elem {
   static constexpr int kBytes = 2, kVec = 8;
+  static constexpr uint32_t kNone = DT::kBF16 ? 0xFF80FF80u : 0xFC00FC00u;  // -infinity
+  // the largest of a word's (largest's) elements, element by element; NaN if one is NaN
+  static __device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if constexpr (DT::kBF16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ uint64_t two(uint32_t w) {
+    if constexpr (DT::kBF16) {
+      return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+      return pair(f.x, f.y);
+    }
+  }
+  static __device__ __forceinline__ uint64_t two(const uint4 &v, int i) { return two(i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w); }
+  template <int N>
+  static __device__ __forceinline__ float top_of(const uint4 (&w)[N]) {
+    uint32_t t = kNone;
+#pragma unroll
+    for (int i = 0; i < N; ++i) t = max_words(t, max_words(max_words(w[i].x, w[i].y), max_words(w[i].z, w[i].w)));
+    float a, b;
+    unpair(two(t), a, b);
+    return max_nan(a, b);
+  }
   static __device__ __forceinline__ float at(const void *p, int64_t i) {
     return bits_to_float(reinterpret_cast<const uint16_t *>(p)[i], DT::kBF16);
   }
@@ -57,6 +107,19 @@ struct Elem {
 template <>
 struct Elem<F32> {
   static constexpr int kBytes = 4, kVec = 4;
+  static constexpr uint32_t kNone = 0xFF800000u;
+  static __device__ __forceinline__ uint64_t two(const uint4 &v, int i) {
+    return i == 0 ? pair(__uint_as_float(v.x), __uint_as_float(v.y)) : pair(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  template <int N>
+  static __device__ __forceinline__ float top_of(const uint4 (&w)[N]) {
+    float t = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      t = max_nan(max_nan(t, max_nan(__uint_as_float(w[i].x), __uint_as_float(w[i].y))),
+                  max_nan(__uint_as_float(w[i].z), __uint_as_float(w[i].w)));
+    return t;
+  }
   static __device__ __forceinline__ float at(const void *p, int64_t i) { return reinterpret_cast<const float *>(p)[i]; }
   static __device__ __forceinline__ void values(const uint4 &v, float (&f)[4]) {
     f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
@@ -83,11 +146,6 @@ struct Params {
   int64_t cshare;  // elements of a CTA of a sequence's cluster
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -186,37 +244,41 @@ __global__ void __launch_bounds__(kThreads, kStatCtas) verify_stats_kernel(const
       m = E::at(x, span.loose(tid));
       s = m == -INFINITY ? 0.f : m - m + 1.f;  // NaN for a NaN or an infinity
     }
-    for (int j0 = 0; j0 < span.n_vec; j0 += kThreads * U) {
-      uint4 w[U];
-      bool in[U];
+    uint4 w[U], ahead[U];
+    auto fetch = [&](uint4 (&v)[U], int j0) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int j = j0 + u * kThreads + tid;
-        in[u] = j < span.n_vec;
-        if (in[u]) w[u] = __ldcs(span.vec + j);
+        v[u] = make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+        if (j < span.n_vec) v[u] = __ldcs(span.vec + j);
       }
-      float top = m;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (in[u]) {
-          float f[kVec];
-          E::values(w[u], f);
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) top = max_nan(top, f[e]);
-        }
-      s *= shrink(m, top, c);
+    };
+    uint64_t s2 = 0;  // the sums of the even and the odd elements
+    const uint64_t unit = pair(c, c);
+    if (span.n_vec > 0) fetch(w, 0);
+    for (int j0 = 0; j0 < span.n_vec; j0 += kThreads * U) {
+      if (j0 + kThreads * U < span.n_vec) fetch(ahead, j0 + kThreads * U);  // in flight while this step is computed
+      const float top = max_nan(m, E::top_of(w));
+      const float f = shrink(m, top, c);
+      s2 = mul2(s2, pair(f, f));
+      s *= f;
       m = top;
+      const float minus = m == -INFINITY ? 0.f : -m;
+      const uint64_t shift = pair(minus, minus);
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (in[u]) {
-          float f[kVec];
-          E::values(w[u], f);
-          float part = 0.f;
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) part += exp2_approx((m == -INFINITY ? f[e] : f[e] - m) * c);
-          s += part;
+        for (int e = 0; e < kVec / 2; ++e) {
+          float x0, x1;
+          unpair(mul2(add2(E::two(w[u], e), shift), unit), x0, x1);
+          s2 = add2(s2, pair(exp2_approx(x0), exp2_approx(x1)));
         }
+#pragma unroll
+      for (int u = 0; u < U; ++u) w[u] = ahead[u];
     }
+    float se, so;
+    unpair(s2, se, so);
+    s += se + so;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -246,14 +308,15 @@ __device__ __forceinline__ uint64_t key_of(float score, uint32_t i) {
 }
 
 template <class DT>
-__global__ void __launch_bounds__(kThreads) verify_walk_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 4) verify_walk_kernel(const Params p) {
   using E = Elem<DT>;
-  constexpr int kVec = E::kVec;
   __shared__ float row_m[kMaxQ], row_s[kMaxQ];  // s: 1 / sum, or the index of the maximum
   __shared__ float pd[kMaxQ], qd[kMaxQ], us[kMaxQ];
   __shared__ int64_t tok[kMaxQ];
   __shared__ int parent[kMaxQ];  // -1: a token that cannot stand
-  __shared__ bool again[kMaxQ];
+  __shared__ float weight[kMaxQ];  // p(d), 0 for a token that an earlier sibling has
+  __shared__ bool passed[kMaxQ];
+  __shared__ int next[kMaxQ];      // the child that stands, -1: none
   __shared__ int chosen[kMaxQ];
   __shared__ int64_t rejected[kMaxQ];
   __shared__ int s_accepted, s_rejected;
@@ -279,6 +342,9 @@ __global__ void __launch_bounds__(kThreads) verify_walk_kernel(const Params p) {
   const float temp = p.temperature ? p.temperature[b] : 1.f;
   const bool greedy = temp == 0.f;
   const float c = greedy ? 0.f : unit_of(temp);
+  const int64_t my_token = tid < n ? p.tokens[start + tid] : 0;
+  const float my_uniform = tid < n ? p.uniforms[start + tid] : 0.f;
+  const uint64_t my_word = tid < n && p.tree_mask ? p.tree_mask[start + tid] : ~0ull;
   // the rows' statistics, four threads a row
   {
     const int i = tid >> 2;
@@ -291,15 +357,15 @@ __global__ void __launch_bounds__(kThreads) verify_walk_kernel(const Params p) {
         if (greedy) join_index(m, at, o.x, __float_as_int(o.y));
         else join(m, s, o.x, o.y, c);
       }
-      const unsigned quad = 0xFu << (lane & 28);
+      const unsigned four = 0xFu << (lane & 28);
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
-        const float om = __shfl_xor_sync(quad, m, o);
+        const float om = __shfl_xor_sync(four, m, o);
         if (greedy) {
-          const int oi = __shfl_xor_sync(quad, at, o);
+          const int oi = __shfl_xor_sync(four, at, o);
           join_index(m, at, om, oi);
         } else {
-          const float os = __shfl_xor_sync(quad, s, o);
+          const float os = __shfl_xor_sync(four, s, o);
           join(m, s, om, os, c);
         }
       }
@@ -311,8 +377,8 @@ __global__ void __launch_bounds__(kThreads) verify_walk_kernel(const Params p) {
       }
     }
     if (tid < n) {
-      tok[tid] = p.tokens[start + tid];
-      us[tid] = p.uniforms[start + tid];
+      tok[tid] = my_token;
+      us[tid] = my_uniform;
     }
   }
   __syncthreads();
@@ -324,39 +390,65 @@ __global__ void __launch_bounds__(kThreads) verify_walk_kernel(const Params p) {
     return exp2f((E::at(p.logits + (start + node) * p.row_stride * E::kBytes, token) - m) * c) * row_s[node];
   };
   if (tid < n) {
-    const uint64_t word = p.tree_mask ? p.tree_mask[start + tid] : ~0ull;
-    const uint64_t below = word & ((1ull << tid) - 1);
-    const int up = below == 0 || tok[tid] < 0 || tok[tid] >= p.vocab ? -1 : 63 - __clzll(static_cast<long long>(below));
+    const uint64_t below = my_word & ((1ull << tid) - 1);
+    const int up = below == 0 || my_token < 0 || my_token >= p.vocab ? -1 : 63 - __clzll(static_cast<long long>(below));
     parent[tid] = up;
     if (up >= 0) {
-      pd[tid] = prob(up, tok[tid]);
-      qd[tid] = p.draft ? p.draft[(start + up) * p.draft_stride + tok[tid]] : 0.f;
+      qd[tid] = p.draft ? p.draft[(start + up) * p.draft_stride + my_token] : 0.f;
+      pd[tid] = prob(up, my_token);
     }
   }
   __syncthreads();
-  if (tid < n) {
+  // four threads for each token look at its siblings
+  const int own = tid >> 2, part = tid & 3;
+  const unsigned quad = 0xFu << (lane & 28);
+  if (own < n) {
     bool dup = false;
     if (p.tree_mask)
-      for (int j = 1; j < tid; ++j) dup |= parent[j] == parent[tid] && tok[j] == tok[tid];
-    again[tid] = dup;
+      for (int j = 1 + part; j < own; j += 4) dup |= parent[j] == parent[own] && tok[j] == tok[own];
+    dup = __any_sync(quad, dup);
+    if (part == 0) {
+      weight[own] = dup || parent[own] < 0 ? 0.f : pd[own];
+      next[own] = -1;
+    }
   }
   __syncthreads();
-  if (tid == 0) {
-    int node = 0, k = 0, nr = 0;
-    float left = 1.f;
-    chosen[0] = 0;
-    for (int i = 1; i < n; ++i) {
-      if (parent[i] != node) continue;
-      const float pi = again[i] ? 0.f : pd[i];
-      if (p.draft ? us[i] * qd[i] < pi : us[i] * left < pi) {
-        node = i, left = 1.f, nr = 0;
-        chosen[++k] = i;
-      } else {
-        left -= pi;
-        rejected[nr++] = tok[i];
-      }
+  if (own < n) {
+    float gone = 0.f;
+    if (!p.draft && p.tree_mask)
+      for (int j = 1 + part; j < own; j += 4)
+        if (parent[j] == parent[own]) gone += weight[j];
+    gone += __shfl_xor_sync(quad, gone, 1);
+    gone += __shfl_xor_sync(quad, gone, 2);
+    if (part == 0) passed[own] = parent[own] >= 0 && (p.draft ? us[own] * qd[own] < weight[own] : us[own] * (1.f - gone) < weight[own]);
+  }
+  __syncthreads();
+  if (own < n) {
+    bool before = false;  // an earlier sibling stands
+    if (p.tree_mask)
+      for (int j = 1 + part; j < own; j += 4) before |= passed[j] && parent[j] == parent[own];
+    before = __any_sync(quad, before);
+    if (part == 0 && own > 0 && passed[own] && !before) next[parent[own]] = own;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int node = 0, k = 0;
+    while (true) {  // (a child's index is larger than its parent's)
+      if (lane == 0) chosen[k] = node;
+      const int to = next[node];
+      if (to < 0) break;
+      node = to, ++k;
     }
-    s_accepted = k, s_rejected = nr;
+    // its children, none of which stands
+    int nr = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      const bool kid = i > 0 && i < n && parent[i] == node;
+      const unsigned vote = __ballot_sync(0xFFFFFFFFu, kid);
+      if (kid) rejected[nr + __popc(vote & ((1u << lane) - 1))] = tok[i];
+      nr += __popc(vote);
+    }
+    if (lane == 0) s_accepted = k, s_rejected = nr;
   }
   __syncthreads();
   const int k = s_accepted, last = chosen[k];
@@ -373,37 +465,33 @@ __global__ void __launch_bounds__(kThreads) verify_walk_kernel(const Params p) {
     const float inv = row_s[last];
     if (q) nr = 0;
     const int64_t lo = min(p.cshare * crank, p.vocab), hi = min(lo + p.cshare, p.vocab);
-    const Span<DT> span(x, lo, hi);
     while (true) {
       float top = -1.f;
       uint32_t top_i = 0;
-      auto take = [&](float xv, float ev, float qv, uint32_t i) {
-        const float r = fmaxf(exp2_approx((xv - m) * c) * inv - qv, 0.f);
-        const float score = __fdividef(r, ev);
-        if (r > 0.f && score > top) {
-          bool gone = false;
-          for (int j = 0; j < nr; ++j) gone |= rejected[j] == i;
-          if (!gone) top = score, top_i = i;
+      // neighbouring elements in neighbouring threads: the three rows start at different offsets from 16 bytes
+      constexpr int U = 8;
+      for (int64_t i0 = lo + tid; i0 < hi; i0 += kThreads * U) {
+        float xv[U], ev[U], qv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int64_t i = i0 + u * kThreads;
+          const bool in = i < hi;
+          xv[u] = in ? E::at(x, i) : -INFINITY;
+          ev[u] = in ? __ldcs(e + i) : 1.f;
+          qv[u] = in && q ? __ldcs(q + i) : 0.f;
         }
-      };
-      // ascending indices within a thread, so that the first of equal ratios stays
-      if (tid < span.head) {
-        const int64_t i = lo + tid;
-        take(E::at(x, i), e[i], q ? q[i] : 0.f, static_cast<uint32_t>(i));
-      }
-      for (int j = tid; j < span.n_vec; j += kThreads) {
-        float f[kVec], ev[kVec], qv[kVec];
-        const uint4 w = span.vec[j];
-        const int64_t i = lo + span.head + int64_t(j) * kVec;
 #pragma unroll
-        for (int a = 0; a < kVec; ++a) ev[a] = __ldcs(e + i + a), qv[a] = q ? __ldcs(q + i + a) : 0.f;
-        E::values(w, f);
-#pragma unroll
-        for (int a = 0; a < kVec; ++a) take(f[a], ev[a], qv[a], static_cast<uint32_t>(i) + a);
-      }
-      if (tid < span.tail) {
-        const int64_t i = span.loose(span.head + tid);
-        take(E::at(x, i), e[i], q ? q[i] : 0.f, static_cast<uint32_t>(i));
+        for (int u = 0; u < U; ++u) {
+          const float r = fmaxf(exp2_approx((xv[u] - m) * c) * inv - qv[u], 0.f);
+          const float score = __fdividef(r, ev[u]);
+          // (ascending indices within a thread, so that the first of equal ratios stays)
+          if (r > 0.f && score > top) {
+            const uint32_t i = static_cast<uint32_t>(i0) + u * kThreads;
+            bool gone = false;
+            for (int j = 0; j < nr; ++j) gone |= rejected[j] == i;
+            if (!gone) top = score, top_i = i;
+          }
+        }
       }
       best = top >= 0.f ? key_of(top, top_i) : 0;
 #pragma unroll

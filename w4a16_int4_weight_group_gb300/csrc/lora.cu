@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *
     const int id = ids[i];
     return id < 0 || id >= adapters ? adapters : id;
   };
-  // lanes with the same key add once; the loads of eight steps are in flight together
+  // (the loads of eight steps are in flight together)
   constexpr int kBatch = 8;
   for (int i0 = tid; i0 - lane < tokens; i0 += kSortThreads * kBatch) {
     int k[kBatch];
@@ -439,8 +439,9 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *
     for (int j = 0; j < kBatch; ++j) k[j] = i0 + j * kSortThreads < tokens ? key(i0 + j * kSortThreads) : -1;
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, k[j]);
-      if (k[j] >= 0 && lane == __ffs(same) - 1) atomicAdd(&counts[k[j]], __popc(same));
+      // a run of one request's tokens fills most warps; else each lane adds for itself
+      const bool one = __all_sync(0xFFFFFFFFu, k[j] == __shfl_sync(0xFFFFFFFFu, k[j], 0));
+      if (k[j] >= 0 && (!one || lane == 0)) atomicAdd(&counts[k[j]], one ? 32 : 1);
     }
   }
   __syncthreads();
@@ -476,20 +477,18 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *
   if (tid == 0) *num_tiles = tiles_before;
   for (int i0 = tid; i0 - lane < tokens; i0 += kSortThreads * kBatch) {
     int k[kBatch], at[kBatch];
-    unsigned same[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) k[j] = i0 + j * kSortThreads < tokens ? key(i0 + j * kSortThreads) : -1;
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      same[j] = __match_any_sync(0xFFFFFFFFu, k[j]);
+      const bool one = __all_sync(0xFFFFFFFFu, k[j] == __shfl_sync(0xFFFFFFFFu, k[j], 0));
       at[j] = 0;
-      if (k[j] >= 0 && lane == __ffs(same[j]) - 1) at[j] = atomicAdd(&counts[k[j]], __popc(same[j]));
+      if (k[j] >= 0 && (!one || lane == 0)) at[j] = atomicAdd(&counts[k[j]], one ? 32 : 1);
+      if (one) at[j] = __shfl_sync(0xFFFFFFFFu, at[j], 0) + lane;
     }
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int first = __shfl_sync(0xFFFFFFFFu, at[j], __ffs(same[j]) - 1);
-      if (k[j] >= 0) order[first + __popc(same[j] & ((1u << lane) - 1))] = i0 + j * kSortThreads;
-    }
+    for (int j = 0; j < kBatch; ++j)
+      if (k[j] >= 0) order[at[j]] = i0 + j * kSortThreads;
   }
 }
 

@@ -14,10 +14,12 @@
 // Two kernels. The first reads every row once: running maximum and sum of exponentials, rows split over CTAs when
 // they are few. The second has a cluster for each sequence: a thread for each token finds its parent and gathers p(d) and q(d); four
 // threads for each token look at its siblings, so that every node knows the child that would stand there; the walk down the tree only
-// follows these. Then the cluster's CTAs take a part of the vocabulary each, of the last node's row alone. Whether a token was rejected is only looked up for the ratios that exceed a thread's best so far.
+// follows these. Then the cluster's CTAs take a part of the vocabulary each, of the last node's row alone. A token's ratio costs an exponential and a division;
+// whether it was rejected is only looked up by the few threads that meet a rejected one.
 //
 // Bound by memory in the first kernel, by the latency of its chain of small steps in the second.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -91,18 +93,6 @@ struct Elem {
   static __device__ __forceinline__ float at(const void *p, int64_t i) {
     return bits_to_float(reinterpret_cast<const uint16_t *>(p)[i], DT::kBF16);
   }
-  static __device__ __forceinline__ void values(const uint4 &v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (DT::kBF16) {
-        f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      } else {
-        const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        f[2 * i] = h.x, f[2 * i + 1] = h.y;
-      }
-    }
-  }
 };
 template <>
 struct Elem<F32> {
@@ -121,9 +111,6 @@ struct Elem<F32> {
     return t;
   }
   static __device__ __forceinline__ float at(const void *p, int64_t i) { return reinterpret_cast<const float *>(p)[i]; }
-  static __device__ __forceinline__ void values(const uint4 &v, float (&f)[4]) {
-    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y), f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
-  }
 };
 
 struct Params {
@@ -195,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, kStatCtas) verify_stats_kernel(const
   using E = Elem<DT>;
   constexpr int kVec = E::kVec, U = 4;
   __shared__ float ms[kWarps], ss[kWarps];
-  __shared__ int is[kWarps];
+  __shared__ int is[1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row = blockIdx.x / p.splits;
   const int split = static_cast<int>(blockIdx.x % p.splits);
@@ -217,45 +204,59 @@ __global__ void __launch_bounds__(kThreads, kStatCtas) verify_stats_kernel(const
   const Span<DT> span(x, lo, hi);
   float m = -INFINITY, s = 0.f;
   int first = 0x7FFFFFFF;
+  uint4 w[U], ahead[U];
+  auto fetch = [&](uint4 (&v)[U], int j0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * kThreads + tid;
+      v[u] = make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
+      if (j < span.n_vec) v[u] = __ldg(span.vec + j);
+    }
+  };
+  if (span.n_vec > 0) fetch(w, 0);
+  float loose = -INFINITY;  // an element that is in no vector (there are fewer than two vectors of them)
+  if (tid < span.head + span.tail) loose = E::at(x, span.loose(tid));
   if (temp == 0.f) {
-    for (int j = tid; j < span.head + span.tail; j += kThreads) {
-      const int64_t i = span.loose(j);
-      join_index(m, first, E::at(x, i), static_cast<int>(i));
-    }
+    int where = 0;  // the first step of this thread's largest element; its index is looked up at the end
     for (int j0 = 0; j0 < span.n_vec; j0 += kThreads * U) {
-      uint4 w[U];
+      if (j0 + kThreads * U < span.n_vec) fetch(ahead, j0 + kThreads * U);
+      const float top = E::top_of(w);
+      if (!(top <= m)) m = max_nan(m, top), where = j0;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * kThreads + tid;
-        if (j < span.n_vec) w[u] = __ldcs(span.vec + j);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * kThreads + tid;
-        if (j >= span.n_vec) break;
-        float f[kVec];
-        E::values(w[u], f);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) join_index(m, first, f[e], static_cast<int>(lo) + span.head + j * kVec + e);
-      }
+      for (int u = 0; u < U; ++u) w[u] = ahead[u];
     }
-  } else {
-    if (tid < span.head + span.tail) {  // (fewer than two vectors)
-      m = E::at(x, span.loose(tid));
-      s = m == -INFINITY ? 0.f : m - m + 1.f;  // NaN for a NaN or an infinity
-    }
-    uint4 w[U], ahead[U];
-    auto fetch = [&](uint4 (&v)[U], int j0) {
+    float all = max_nan(m, loose);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * kThreads + tid;
-        v[u] = make_uint4(E::kNone, E::kNone, E::kNone, E::kNone);
-        if (j < span.n_vec) v[u] = __ldcs(span.vec + j);
-      }
-    };
+    for (int o = 16; o > 0; o >>= 1) all = max_nan(all, __shfl_xor_sync(0xFFFFFFFFu, all, o));
+    if (lane == 0) ms[warp] = all;
+    if (tid == 0) is[0] = 0x7FFFFFFF;
+    __syncthreads();
+    all = ms[0];
+    for (int i = 1; i < kWarps; ++i) all = max_nan(all, ms[i]);
+    if (loose == all && tid < span.head + span.tail) first = static_cast<int>(span.loose(tid));
+    if (m == all && span.n_vec > 0) {
+      fetch(w, where);
+#pragma unroll
+      for (int u = U - 1; u >= 0; --u)
+#pragma unroll
+        for (int e = kVec / 2 - 1; e >= 0; --e) {
+          float x0, x1;
+          unpair(E::two(w[u], e), x0, x1);
+          const int i = static_cast<int>(lo) + span.head + (where + u * kThreads + tid) * kVec + 2 * e;
+          if (x1 == all && i + 1 < hi) first = min(first, i + 1);
+          if (x0 == all && i < hi) first = min(first, i);
+        }
+    }
+    if (first != 0x7FFFFFFF) atomicMin(&is[0], first);
+    __syncthreads();
+    if (tid == 0) p.stats[row * p.splits + split] = make_float2(all, __int_as_float(is[0]));
+    return;
+  }
+  m = loose;
+  if (m > -INFINITY || !(m == m)) s = m - m + 1.f;  // NaN for a NaN or an infinity
+  {
     uint64_t s2 = 0;  // the sums of the even and the odd elements
     const uint64_t unit = pair(c, c);
-    if (span.n_vec > 0) fetch(w, 0);
     for (int j0 = 0; j0 < span.n_vec; j0 += kThreads * U) {
       if (j0 + kThreads * U < span.n_vec) fetch(ahead, j0 + kThreads * U);  // in flight while this step is computed
       const float top = max_nan(m, E::top_of(w));
@@ -282,23 +283,14 @@ __global__ void __launch_bounds__(kThreads, kStatCtas) verify_stats_kernel(const
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const float om = __shfl_xor_sync(0xFFFFFFFFu, m, o);
-    if (temp == 0.f) {
-      const int oi = __shfl_xor_sync(0xFFFFFFFFu, first, o);
-      join_index(m, first, om, oi);
-    } else {
-      const float os = __shfl_xor_sync(0xFFFFFFFFu, s, o);
-      join(m, s, om, os, c);
-    }
+    const float om = __shfl_xor_sync(0xFFFFFFFFu, m, o), os = __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    join(m, s, om, os, c);
   }
-  if (lane == 0) ms[warp] = m, ss[warp] = s, is[warp] = first;
+  if (lane == 0) ms[warp] = m, ss[warp] = s;
   __syncthreads();
   if (tid == 0) {
-    for (int w = 1; w < kWarps; ++w) {
-      if (temp == 0.f) join_index(m, first, ms[w], is[w]);
-      else join(m, s, ms[w], ss[w], c);
-    }
-    p.stats[row * p.splits + split] = make_float2(m, temp == 0.f ? __int_as_float(first) : s);
+    for (int i = 1; i < kWarps; ++i) join(m, s, ms[i], ss[i], c);
+    p.stats[row * p.splits + split] = make_float2(m, s);
   }
 }
 
@@ -327,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_walk_kernel(const Params p
   const int csize = p.csize;
   const int crank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int64_t b = blockIdx.x / csize;
+  const int64_t lo = min(p.cshare * crank, p.vocab), hi = min(lo + p.cshare, p.vocab);
   griddep_wait();
   griddep_launch_dependents();
   int64_t start = b, end = b + 1;
@@ -464,35 +457,48 @@ __global__ void __launch_bounds__(kThreads, 4) verify_walk_kernel(const Params p
     const float *q = p.draft && nr ? p.draft + (start + last) * p.draft_stride : nullptr;
     const float inv = row_s[last];
     if (q) nr = 0;
-    const int64_t lo = min(p.cshare * crank, p.vocab), hi = min(lo + p.cshare, p.vocab);
+    // The threads that come across a rejected token (few of them, and only these look a ratio's token up)
+    bool meets = false;
+    if (nr) {
+      for (int j = 0; j < nr; ++j) {
+        const int64_t d = rejected[j];
+        meets |= d >= lo && d < hi && static_cast<int>((d - lo) % kThreads) == tid;
+      }
+    }
     while (true) {
       float top = -1.f;
       uint32_t top_i = 0;
       // neighbouring elements in neighbouring threads: the three rows start at different offsets from 16 bytes
       constexpr int U = 8;
-      for (int64_t i0 = lo + tid; i0 < hi; i0 += kThreads * U) {
-        float xv[U], ev[U], qv[U];
+      auto pass = [&](auto with_q) {
+        for (int64_t i0 = lo + tid; i0 < hi; i0 += kThreads * U) {
+          float xv[U], ev[U], qv[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t i = i0 + u * kThreads;
-          const bool in = i < hi;
-          xv[u] = in ? E::at(x, i) : -INFINITY;
-          ev[u] = in ? __ldcs(e + i) : 1.f;
-          qv[u] = in && q ? __ldcs(q + i) : 0.f;
-        }
+          for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + u * kThreads;
+            const bool in = i < hi;
+            xv[u] = in ? E::at(x, i) : -INFINITY;
+            ev[u] = in ? __ldcs(e + i) : 1.f;
+            if constexpr (decltype(with_q)::value) qv[u] = in ? __ldcs(q + i) : 0.f;
+            else qv[u] = 0.f;
+          }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float r = fmaxf(exp2_approx((xv[u] - m) * c) * inv - qv[u], 0.f);
-          const float score = __fdividef(r, ev[u]);
-          // (ascending indices within a thread, so that the first of equal ratios stays)
-          if (r > 0.f && score > top) {
-            const uint32_t i = static_cast<uint32_t>(i0) + u * kThreads;
-            bool gone = false;
-            for (int j = 0; j < nr; ++j) gone |= rejected[j] == i;
-            if (!gone) top = score, top_i = i;
+          for (int u = 0; u < U; ++u) {
+            const float r = fmaxf(exp2_approx((xv[u] - m) * c) * inv - qv[u], 0.f);
+            const float score = __fdividef(r, ev[u]);
+            // (ascending indices within a thread, so that the first of equal ratios stays)
+            if (r > 0.f && score > top) {
+              const uint32_t i = static_cast<uint32_t>(i0) + u * kThreads;
+              bool gone = false;
+              if (meets)
+                for (int j = 0; j < nr; ++j) gone |= rejected[j] == i;
+              if (!gone) top = score, top_i = i;
+            }
           }
         }
-      }
+      };
+      if (q) pass(std::true_type{});
+      else pass(std::false_type{});
       best = top >= 0.f ? key_of(top, top_i) : 0;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));

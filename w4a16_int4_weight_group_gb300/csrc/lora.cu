@@ -459,11 +459,16 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *
     }
     if (lane == 31) sums[0][warp] = a, sums[1][warp] = b;
     __syncthreads();
-    int ta = 0, tb = 0, wa = 0, wb = 0;
-    for (int w = 0; w < kSortThreads / 32; ++w) {
-      if (w == warp) wa = ta, wb = tb;
-      ta += sums[0][w], tb += sums[1][w];
+    static_assert(kSortThreads == 1024, "a lane for each warp's sums");
+    const int sa = sums[0][lane], sb = sums[1][lane];
+    int ta = sa, tb = sb;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int ua = __shfl_up_sync(0xFFFFFFFFu, ta, o), ub = __shfl_up_sync(0xFFFFFFFFu, tb, o);
+      if (lane >= o) ta += ua, tb += ub;
     }
+    const int wa = __shfl_sync(0xFFFFFFFFu, ta - sa, warp), wb = __shfl_sync(0xFFFFFFFFu, tb - sb, warp);
+    ta = __shfl_sync(0xFFFFFFFFu, ta, 31), tb = __shfl_sync(0xFFFFFFFFu, tb, 31);
     const int first = tokens_before + wa + a - n;
     int at = tiles_before + wb + b - nt;
     if (k <= adapters) {
@@ -492,9 +497,12 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *
   }
 }
 
-constexpr int kSortedTile = 64;  // tokens
+// Tokens of a sorted tile: 32 while there are few of them (two CTAs on an SM at every rank, and clusters of eight: 520 tokens
+// 2560 -> 3840 of rank 64 TIME32 against TIME64 with 64), else 64 (A and B are read half as often)
+constexpr int64_t kMidTokens = 2048;
+int sorted_tile(int64_t tokens) { return tokens <= kMidTokens ? 32 : 64; }
 int64_t most_tiles(int64_t tokens, int64_t adapters) {
-  return tokens / kSortedTile + std::min<int64_t>(tokens, adapters + 1);
+  return tokens / sorted_tile(tokens) + std::min<int64_t>(tokens, adapters + 1);
 }
 
 template <class DT, class S, bool SORTED>
@@ -548,6 +556,12 @@ cudaError_t run(const Params &p, bool few, int64_t tiles, int64_t most, int num_
     if (r <= 64) return go<DT, Shape<4, 1, 1, 3, 2>, false>(p, tiles, most, num_sms, stream);
     return go<DT, Shape<4, 1, 2, 2, 1>, false>(p, tiles, most, num_sms, stream);
   }
+  if (p.tokens <= kMidTokens) {
+    if (r <= 16) return go<DT, Shape<1, 4, 1, 3, 2>, true>(p, tiles, most, num_sms, stream);
+    if (r <= 32) return go<DT, Shape<2, 4, 1, 3, 2>, true>(p, tiles, most, num_sms, stream);
+    if (r <= 64) return go<DT, Shape<4, 4, 1, 2, 2>, true>(p, tiles, most, num_sms, stream);
+    return go<DT, Shape<4, 4, 2, 2, 1>, true>(p, tiles, most, num_sms, stream);
+  }
   if (r <= 16) return go<DT, Shape<1, 8, 1, 2, 2>, true>(p, tiles, most, num_sms, stream);
   if (r <= 32) return go<DT, Shape<2, 8, 1, 2, 2>, true>(p, tiles, most, num_sms, stream);
   if (r <= 64) return go<DT, Shape<4, 8, 1, 3, 1>, true>(p, tiles, most, num_sms, stream);
@@ -591,7 +605,7 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
     Tile *list = reinterpret_cast<Tile *>(ws + 256 + (a.tokens * 4 + 255) / 256 * 256);
     p.num_tiles = num;
     p.tiles = list;
-    const int per = kSortedTile;
+    const int per = sorted_tile(a.tokens);
     tiles = (a.tokens + per - 1) / per + std::min<int64_t>(a.adapters, a.tokens / 2) / 2;
     most = most_tiles(a.tokens, a.adapters);
     cudaLaunchConfig_t cfg = {};

@@ -242,7 +242,10 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
         cp_async_commit();
       }
       for (int i = 0; i < steps; ++i) {
-        cp_async_wait<S::kStages1 - 2>();
+        // (into the slots that the step before this one has read)
+        if (i + S::kStages1 - 1 < steps) fetch(i + S::kStages1 - 1);
+        cp_async_commit();
+        cp_async_wait<S::kStages1 - 1>();
         const uint4 *at = ring + (i % S::kStages1) * S::kSlots1 * kThreads;
         uint4 av[MR][2];
 #pragma unroll
@@ -259,8 +262,6 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
             mma_16816<DT::kBF16>(acc[m][n], f1, xv.z, xv.w);
           }
         }
-        if (i + S::kStages1 - 1 < steps) fetch(i + S::kStages1 - 1);
-        cp_async_commit();
       }
       __syncthreads();  // the ring is not read any more (every load of it was waited for)
 #pragma unroll
@@ -389,7 +390,9 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
       cp_async_commit();
     }
     for (int i = 0; i < groups; ++i) {
-      cp_async_wait<S::kStages2 - 2>();
+      if (i + S::kStages2 - 1 < groups) fetch(i + S::kStages2 - 1);
+      cp_async_commit();
+      cp_async_wait<S::kStages2 - 1>();
       const uint32_t col = c0 + i * cstep + t;
       const bool in = col < n_units;
       const uint4 *at = ring + (i % S::kStages2) * S::kSlots2 * kThreads;
@@ -431,8 +434,6 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
         if (in && i0 < count) __stcs(out16 + (tok[i0] * p.out_stride >> 3) + col, o0);
         if (S::kHalves == 2 && in && i1 < count) __stcs(out16 + (tok[i1] * p.out_stride >> 3) + col, o1);
       }
-      if (i + S::kStages2 - 1 < groups) fetch(i + S::kStages2 - 1);
-      cp_async_commit();
     }
     __syncthreads();  // done with the tile's tables and the ring
   }

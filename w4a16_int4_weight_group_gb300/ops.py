@@ -14,7 +14,9 @@ the real runtime shape. Here the tile, split-K and cluster choice already live i
 
 The serving operators (``rope``, ``kv_write``, ``kv_write_q``, ``kv_read``, ``tree_attention``, ``tree_attention_lse``,
 ``token_logprobs``) are opaque calls in the same way: each forwards to the binding's function of that name, its fake
-implementation states the outputs' metadata, and the two writes say that they change the cache.
+implementation states the outputs' metadata, and the two writes say that they change the cache. So are those around a step of many
+users: ``lora``, ``verify_drafts``, ``kv_fork``, ``kv_reserve``, ``kv_free``, ``kv_copy`` and ``kv_compact``, which say which of the reference counts,
+the page table and the cache they change.
 
 Import this module to register the ops.
 """
@@ -25,6 +27,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import serving as _serving
+from . import step as _step
 from . import w4a16_gemm as _w4a16_gemm
 
 
@@ -131,3 +134,89 @@ def _token_logprobs_fake(logits, tokens=None, top_k=0):
     rows = logits.size(0)
     f = lambda *shape: logits.new_empty(shape, dtype=torch.float32)
     return f(*(tokens.shape if tokens is not None else (rows, 0))), f(rows), logits.new_empty((rows, top_k), dtype=torch.int64), f(rows, top_k)
+
+
+@torch.library.custom_op("w4a16::lora", mutates_args=())
+def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor, base: torch.Tensor,
+         scales: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """base plus the low-rank product of each token's adapter, in a new tensor."""
+    return _step.w4a16_lora(x, a, b, ids, base, scales)
+
+
+@lora.register_fake
+def _lora_fake(x, a, b, ids, base, scales=None):
+    return base.new_empty(base.shape)
+
+
+@torch.library.custom_op("w4a16::verify_drafts", mutates_args=())
+def verify_drafts(logits: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Tensor, noise: torch.Tensor, max_q: int,
+                  q_start: Optional[torch.Tensor] = None, tree_mask: Optional[torch.Tensor] = None,
+                  draft_probs: Optional[torch.Tensor] = None,
+                  temperature: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(accepted, path, out_tokens, out_probs) of each sequence's drafted tokens."""
+    return _step.w4a16_verify_drafts(logits, tokens, uniforms, noise, q_start, tree_mask, draft_probs, temperature, max_q)
+
+
+@verify_drafts.register_fake
+def _verify_drafts_fake(logits, tokens, uniforms, noise, max_q, q_start=None, tree_mask=None, draft_probs=None, temperature=None):
+    B = noise.size(0)
+    return (noise.new_empty((B,), dtype=torch.int32), noise.new_empty((B, max_q), dtype=torch.int32),
+            noise.new_empty((B, max_q), dtype=torch.int64), noise.new_empty((B, max_q)))
+
+
+@torch.library.custom_op("w4a16::kv_fork", mutates_args=("refs",))
+def kv_fork(refs: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, parents: torch.Tensor,
+            page_size: int) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(new_table, new_lens) of sequences that share their parents' pages."""
+    return _step.w4a16_kv_fork(refs, page_table, kv_lens, parents, page_size)
+
+
+@kv_fork.register_fake
+def _kv_fork_fake(refs, page_table, kv_lens, parents, page_size):
+    return refs.new_empty((parents.size(0), page_table.size(1))), refs.new_empty((parents.size(0),))
+
+
+@torch.library.custom_op("w4a16::kv_reserve", mutates_args=("refs", "page_table"))
+def kv_reserve(refs: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, new_lens: torch.Tensor,
+               page_size: int) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(held, copies): pages for the tokens up to new_lens."""
+    return _step.w4a16_kv_reserve(refs, page_table, kv_lens, new_lens, page_size)
+
+
+@kv_reserve.register_fake
+def _kv_reserve_fake(refs, page_table, kv_lens, new_lens, page_size):
+    return refs.new_empty((page_table.size(0),)), refs.new_empty((page_table.size(0), 2))
+
+
+@torch.library.custom_op("w4a16::kv_free", mutates_args=("refs", "page_table"))
+def kv_free(refs: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, page_size: int, keep: Optional[torch.Tensor] = None) -> None:
+    """Gives back the pages of the tokens from keep on."""
+    _step.w4a16_kv_free(refs, page_table, kv_lens, page_size, keep)
+
+
+@kv_free.register_fake
+def _kv_free_fake(refs, page_table, kv_lens, page_size, keep=None):
+    return None
+
+
+@torch.library.custom_op("w4a16::kv_copy", mutates_args=("cache",))
+def kv_copy(cache: torch.Tensor, copies: torch.Tensor) -> None:
+    """Copies whole pages of the cache."""
+    _step.w4a16_kv_copy(cache, copies)
+
+
+@kv_copy.register_fake
+def _kv_copy_fake(cache, copies):
+    return None
+
+
+@torch.library.custom_op("w4a16::kv_compact", mutates_args=("cache",))
+def kv_compact(cache: torch.Tensor, head_dim: int, page_table: torch.Tensor, kv_lens: torch.Tensor, path: torch.Tensor,
+               q_start: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Moves the accepted tokens of each tree together; the new lengths."""
+    return _step.w4a16_kv_compact(cache, head_dim, page_table, kv_lens, path, q_start)
+
+
+@kv_compact.register_fake
+def _kv_compact_fake(cache, head_dim, page_table, kv_lens, path, q_start=None):
+    return kv_lens.new_empty(kv_lens.shape)

@@ -51,12 +51,14 @@ def test_lora_refusals(w):
     refused(w, call(out=0x5000000 + 64), 1, "overlaps base")
     refused(w, call(out=0x5000000, os=40), 1, "overlaps base")
     refused(w, call(out=0x1000000 + 32), 1, "overlaps an input")
-    refused(w, call(T=300), 1, "workspace of 0 bytes")
-    need = w.w4a16_lora_workspace_size(300, 16, 4)
-    assert need > 4096 + 300 * 4 and w.w4a16_lora_workspace_size(256, 16, 4) == 0 and w.w4a16_lora_workspace_size(300, 16, 9000) == 0
-    refused(w, call(T=300, ws=0x7000000, wb=need - 1), 1, "needed")
-    refused(w, call(T=300, ws=0x7000080, wb=need), 3, "256-byte")
-    refused(w, call(T=300, ws=0x5000000, wb=need), 1, "overlaps")
+    refused(w, call(T=1025), 1, "workspace of 0 bytes")
+    refused(w, call(T=257, L=513), 1, "workspace of 0 bytes")
+    need = w.w4a16_lora_workspace_size(1100, 16, 4)
+    assert need > 4096 + 1100 * 4 and w.w4a16_lora_workspace_size(1100, 16, 9000) == 0
+    assert [w.w4a16_lora_workspace_size(T, 16, L) for T, L in ((256, 8191), (1024, 512))] == [0, 0]
+    refused(w, call(T=1100, ws=0x7000000, wb=need - 1), 1, "needed")
+    refused(w, call(T=1100, ws=0x7000080, wb=need), 3, "256-byte")
+    refused(w, call(T=1100, ws=0x5000000, wb=need), 1, "overlaps")
     # strides of a single row do not count (the NULL ids are what is refused)
     refused(w, call(T=1, xs=3, bs=-1, os=0, ids=None), 1, "must not be NULL")
     assert w.w4a16_debug_launch_count() == before

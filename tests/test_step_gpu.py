@@ -53,7 +53,9 @@ def cuda(c):
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("T,K,N,r,n", [(1, 2112, 1152, 8, 4), (1, 8, 8, 8, 1), (7, 200, 40, 24, 3), (9, 520, 264, 16, 1), (33, 1000, 136, 32, 5),
                                        (48, 640, 1160, 64, 48), (64, 264, 72, 128, 7), (256, 72, 96, 48, 2), (257, 136, 104, 16, 3),
-                                       (300, 264, 200, 8, 300), (333, 520, 328, 40, 2), (400, 200, 264, 72, 9), (600, 328, 136, 128, 4), (1000, 64, 32, 32, 1)])
+                                       (300, 264, 200, 8, 300), (333, 520, 328, 40, 2), (400, 200, 264, 72, 9), (600, 328, 136, 128, 4), (1000, 64, 32, 32, 1),
+                                       (1024, 72, 40, 8, 512), (270, 72, 40, 24, 513), (1025, 136, 72, 32, 4), (2049, 64, 40, 16, 30), (2100, 72, 96, 64, 2),
+                                       (2500, 64, 72, 128, 3)])
 def test_lora(w, T, K, N, r, n, dtype):
     c = make_lora(T, K, N, r, n, dtype, seed=T + r)
     d = cuda(c)
@@ -66,7 +68,7 @@ def test_lora(w, T, K, N, r, n, dtype):
     assert same is d["base"] and torch.equal(same, out)
 
 
-@pytest.mark.parametrize("T", [20, 500])
+@pytest.mark.parametrize("T", [20, 500, 1300])
 def test_lora_strided_rows_and_no_scales(w, T):
     c = make_lora(T, 264, 136, 16, 3, "bf16", seed=1)
     c["scales"] = None
@@ -82,10 +84,10 @@ def test_lora_strided_rows_and_no_scales(w, T):
     assert (qkv[:, :160] == 7.0).all() and (qkv[:, 296:] == 7.0).all()
 
 
-@pytest.mark.parametrize("T", [30, 700])
+@pytest.mark.parametrize("T", [30, 700, 1500])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_lora_of_a_token_does_not_depend_on_its_neighbours(w, T, dtype):
-    """The same token, alone in its adapter and among others, on both ways of finding tiles: the same bits."""
+    """The same token, among others in another order, on all ways of finding tiles: the same bits."""
     c = make_lora(T, 520, 264, 32, 4, dtype, seed=3, ids=[i % 4 for i in range(T)])
     d = cuda(c)
     first = w.w4a16_lora(**d)

@@ -78,7 +78,7 @@ def test_sampled_answers_differ_and_give_their_pages_back(w, example):
 
 
 def cases():
-    lora = [cuda(make_lora(T, 520, 264, 16, 5, "bf16", seed=T)) for T in (6, 700)]
+    lora = [cuda(make_lora(T, 520, 264, 16, 5, "bf16", seed=T)) for T in (6, 1500, 700)]
     verify = [cuda(make_verify([4, 9, 2], 3001, "bf16", True, False, seed=4, temps=[1.0, 0.0, 0.8])),
               cuda(make_verify([5, 1, 3], 40001, "f16", False, True, seed=5))]
     refs, table = make_pool(1, 3, 6, 16, 40, [40, 16, 90])
@@ -126,7 +126,7 @@ def test_everything_captured_without_a_warm_up_and_replayed(w):
     assert all(torch.equal(x, y) for x, y in zip(got, want))
     assert torch.equal(refs, refs2) and torch.equal(cache, cache2) and not torch.equal(refs, first)
     # other inputs in the same places
-    other = make_lora(700, 520, 264, 16, 5, "bf16", seed=77)
+    other = make_lora(1500, 520, 264, 16, 5, "bf16", seed=77)
     for name in ("x", "a", "b", "ids", "base", "scales"):
         lora[1][name].copy_(other[name])
     v = make_verify([4, 9, 2], 3001, "bf16", True, False, seed=41, temps=[0.6, 1.0, 0.0])
@@ -135,14 +135,14 @@ def test_everything_captured_without_a_warm_up_and_replayed(w):
     g.replay()
     torch.cuda.synchronize()
     check_lora(w, other, "bf16", got[1])
-    check_verify(w, v, got[2:6])
+    check_verify(w, v, got[3:7])
 
 
 def test_two_streams_at_once_and_between_attention_calls(w):
     """The stream's buffer serves the layer, the attention, the adapters and the verification in turn."""
     a, _ = make_attention(w, 128, 4, "bf16", 64, 2, 4, [3000], [5], tree=True, seed=6)
     a = {k: (x.cuda() if isinstance(x, torch.Tensor) else x) for k, x in a.items()}
-    c = [make_lora(900, 264, 520, 32, 7, "f16", seed=s) for s in (1, 2)]
+    c = [make_lora(1200, 264, 520, 32, 7, "f16", seed=s) for s in (1, 2)]
     v = [make_verify([8, 5], 20003, "f16", False, True, seed=s) for s in (3, 5)]
     dc, dv = [cuda(x) for x in c], [cuda(x) for x in v]
     want = w.w4a16_tree_attention(**a)
@@ -163,8 +163,8 @@ def test_two_streams_at_once_and_between_attention_calls(w):
 
 
 def test_a_workspace_of_the_callers_own(w):
-    c = cuda(make_lora(600, 264, 136, 16, 30, "bf16", seed=9))
-    need = w.w4a16_lora_workspace_size(600, 16, 30)
+    c = cuda(make_lora(1100, 264, 136, 16, 30, "bf16", seed=9))
+    need = w.w4a16_lora_workspace_size(1100, 16, 30)
     ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
     assert torch.equal(w.w4a16_lora(**c, workspace=ws), w.w4a16_lora(**c))
     assert (ws[:4096] == 255).all()

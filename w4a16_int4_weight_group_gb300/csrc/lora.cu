@@ -16,8 +16,8 @@
 // of two). The rounding of out is then the only one that shows.
 //
 // Tiles: tokens of the same adapter wherever they stand. Up to kFewTokens tokens every CTA ranks the tokens among
-// those of their adapter by itself (one launch); more are sorted by a kernel before this one (counting sort). The
-// composition of a tile does not change a token's result: the rows of an MMA do not mix and K is split in the same way.
+// those of their adapter by itself, up to kCountTokens it counts them by adapter in shared memory (one launch); more are sorted by a
+// kernel before this one (counting sort). The composition of a tile does not change a token's result: the rows of an MMA do not mix and K is split in the same way.
 //
 // Bound by memory: base read and out written are most of the bytes for long prompts, A and B of every adapter for single
 // tokens.
@@ -35,6 +35,8 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
 constexpr int kFewTokens = 256;  // one thread for each
 constexpr int kFewTile = 8;      // tokens of a tile then
+// Up to this many tokens of this many adapters a CTA counts the tokens of each adapter in shared memory
+constexpr int kCountTokens = 1024, kCountAdapters = 512;
 constexpr int kSortThreads = 1024;
 constexpr int kMaxAdapters = 8191;  // counters of the sort in shared memory
 
@@ -124,7 +126,14 @@ __device__ __forceinline__ void st_dsmem_f32(uint32_t cluster_addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 
-template <class DT, class S, bool SORTED>
+// How a CTA comes to its tiles
+enum Tiling {
+  kRanked,   // few tokens: each compared with those before it
+  kCounted,  // more: counted by adapter in shared memory
+  kListed    // sorted by a kernel before this one
+};
+
+template <class DT, class S, int TILING>
 __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p) {
   constexpr int MR = S::MR, NT = S::NT;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -134,8 +143,9 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
   uint4 *frag = reinterpret_cast<uint4 *>(smem + S::kRing);
   __shared__ int tok[S::kTokens];
   __shared__ float back[S::kMT * 16];  // what a token's h was divided by (float16)
-  __shared__ int ids_s[SORTED ? 4 : kFewTokens];
-  __shared__ int leaders[SORTED ? 4 : kFewTokens];
+  constexpr int kIds = TILING == kRanked ? kFewTokens : TILING == kCounted ? kCountTokens : 4;
+  __shared__ __align__(16) int ids_s[kIds];  // counted: adapter << 16 | the token's rank in it
+  __shared__ uint16_t leaders[TILING == kCounted ? kCountTokens / S::kTokens + kCountAdapters + 1 : kIds];  // counted: adapter << 5 | its tile
   __shared__ int warp_count[kWarps];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -148,8 +158,71 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
   griddep_launch_dependents();
 
   int my_id = -2, my_rank = 0, ntiles;
-  if constexpr (SORTED) {
+  if constexpr (TILING == kListed) {
     ntiles = *p.num_tiles;
+  } else if constexpr (TILING == kCounted) {
+    static_assert(kCountTokens / S::kTokens <= 32 && kCountAdapters < 2048, "a tile in 16 bits");
+    static_assert(((kWarps + 1) * (kCountAdapters + 1)) * 4 <= S::kRing, "the counters lie in the ring");
+    constexpr int kEach = kCountTokens / kThreads;
+    int *counts = reinterpret_cast<int *>(smem);  // [warp][adapter], tokens without one last; then the sums
+    const int na = p.adapters + 1, tokens = static_cast<int>(p.tokens);
+    // each warp has consecutive tokens, so that ranks follow the tokens' order whatever the timing
+    const int per = (tokens + kThreads - 1) / kThreads * 32;
+    int *mine = counts + warp * na;
+    int id[kEach], rank[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int i = warp * per + j * 32 + lane;
+      id[j] = -1;
+      if (j * 32 < per && i < tokens) {
+        id[j] = p.ids[i];
+        if (id[j] < 0 || id[j] >= p.adapters) id[j] = p.adapters;
+      }
+    }
+    for (int i = tid; i < kWarps * na; i += kThreads) counts[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, id[j]);
+      const int before = id[j] >= 0 ? mine[id[j]] : 0;
+      __syncwarp();
+      rank[j] = before + __popc(same & ((1u << lane) - 1));
+      if (id[j] >= 0 && lane == __ffs(same) - 1) mine[id[j]] = before + __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    for (int a = tid; a < na; a += kThreads) {
+      int sum = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const int v = counts[w * na + a];
+        counts[w * na + a] = sum;
+        sum += v;
+      }
+      counts[kWarps * na + a] = sum;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (id[j] >= 0) ids_s[warp * per + j * 32 + lane] = id[j] << 16 | (mine[id[j]] + rank[j]);
+    if (warp == 0) {
+      int listed = 0;
+      for (int a0 = 0; a0 < na; a0 += 32) {
+        const int a = a0 + lane;
+        const int n = a < na && (a < p.adapters || p.copy) ? (counts[kWarps * na + a] + S::kTokens - 1) / S::kTokens : 0;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+          if (lane >= o) sum += u;
+        }
+        for (int i = 0; i < n; ++i) leaders[listed + sum - n + i] = static_cast<uint16_t>(a << 5 | i);
+        listed += __shfl_sync(0xFFFFFFFFu, sum, 31);
+      }
+      if (lane == 0) warp_count[0] = listed;
+    }
+    __syncthreads();
+    ntiles = warp_count[0];
   } else {
     if (tid < p.tokens) {
       my_id = p.ids[tid];
@@ -173,16 +246,26 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
       if (w == warp) at += ntiles;
       ntiles += warp_count[w];
     }
-    if (lead) leaders[at] = tid;
+    if (lead) leaders[at] = static_cast<uint16_t>(tid);
     __syncthreads();
   }
 
   for (int tile = cluster; tile < ntiles; tile += clusters) {
     int adapter, count;
-    if constexpr (SORTED) {
+    if constexpr (TILING == kListed) {
       const Tile d = p.tiles[tile];
       adapter = d.adapter, count = d.count;
       if (tid < count) tok[tid] = p.order[d.first + tid];
+    } else if constexpr (TILING == kCounted) {
+      const int d = leaders[tile], a = d >> 5, first = (d & 31) * S::kTokens;
+      adapter = a == p.adapters ? -1 : a;
+      count = 0;
+      for (int i0 = 0; i0 < p.tokens; i0 += kThreads) {
+        const int i = i0 + tid, v = i < p.tokens ? ids_s[i] : -1, at = (v & 0xFFFF) - first;
+        const bool in = v >= 0 && (v >> 16) == a && at >= 0 && at < S::kTokens;
+        if (in) tok[at] = i;
+        count += __syncthreads_count(in);
+      }
     } else {
       const int leader = leaders[tile];
       adapter = ids_s[leader];
@@ -316,14 +399,15 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
         __syncthreads();
       }
       if constexpr (!DT::kBF16) {  // power of two that brings a token's largest to [2^13, 2^14)
-        for (int i = warp; i < S::kTokens; i += kWarps) {
+        for (int i = tid >> 3; i < S::kTokens; i += kThreads / 8) {  // eight threads a token
           float top = 0.f;
-          for (int r = lane; r < p.rank; r += 32) top = fmaxf(top, fabsf(h[i * S::kHStride + r]));  // (a NaN does not count)
+          for (int r = tid & 7; r < p.rank; r += 8) top = fmaxf(top, fabsf(h[i * S::kHStride + r]));  // (a NaN does not count)
+          const unsigned eight = 0xFFu << (lane & 24);
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+          for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(eight, top, o));
           const int e = static_cast<int>(__float_as_uint(top) >> 23);  // 0: zero or subnormal; 255: infinite
           const int d = e == 0 || e == 255 ? 0 : max(-126, min(126, e - 127 - 13));
-          if (lane == 0) back[i] = __uint_as_float(static_cast<uint32_t>(127 + d) << 23);
+          if ((tid & 7) == 0) back[i] = __uint_as_float(static_cast<uint32_t>(127 + d) << 23);
         }
         __syncthreads();
       }
@@ -527,11 +611,11 @@ int64_t most_tiles(int64_t tokens, int64_t adapters) {
   return tokens / sorted_tile(tokens) + std::min<int64_t>(tokens, adapters + 1);
 }
 
-template <class DT, class S, bool SORTED>
+template <class DT, class S, int TILING>
 cudaError_t go(Params p, int64_t tiles, int64_t most, int num_sms, cudaStream_t stream) {
   constexpr int kCtas = S::kCtas;  // on an SM
   static std::atomic<bool> asked[64];  // dynamic shared memory past 48 KB is asked for once a device
-  auto kernel = lora_kernel<DT, S, SORTED>;
+  auto kernel = lora_kernel<DT, S, TILING>;
   if (S::kSmem > 48 * 1024) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -573,27 +657,36 @@ template <class DT>
 cudaError_t run(const Params &p, bool few, int64_t tiles, int64_t most, int num_sms, cudaStream_t stream) {
   const int r = p.rank;
   if (few) {
-    if (r <= 16) return go<DT, Shape<1, 1, 1, 3, 3>, false>(p, tiles, most, num_sms, stream);
-    if (r <= 32) return go<DT, Shape<2, 1, 1, 3, 3>, false>(p, tiles, most, num_sms, stream);
-    if (r <= 64) return go<DT, Shape<4, 1, 1, 3, 2>, false>(p, tiles, most, num_sms, stream);
-    return go<DT, Shape<4, 1, 2, 2, 1>, false>(p, tiles, most, num_sms, stream);
+    if (r <= 16) return go<DT, Shape<1, 1, 1, 3, 3>, kRanked>(p, tiles, most, num_sms, stream);
+    if (r <= 32) return go<DT, Shape<2, 1, 1, 3, 3>, kRanked>(p, tiles, most, num_sms, stream);
+    if (r <= 64) return go<DT, Shape<4, 1, 1, 3, 2>, kRanked>(p, tiles, most, num_sms, stream);
+    return go<DT, Shape<4, 1, 2, 2, 1>, kRanked>(p, tiles, most, num_sms, stream);
+  }
+  if (!p.tiles) {
+    if (r <= 16) return go<DT, Shape<1, 4, 1, 3, 2>, kCounted>(p, tiles, most, num_sms, stream);
+    if (r <= 32) return go<DT, Shape<2, 4, 1, 3, 2>, kCounted>(p, tiles, most, num_sms, stream);
+    if (r <= 64) return go<DT, Shape<4, 4, 1, 2, 2>, kCounted>(p, tiles, most, num_sms, stream);
+    return go<DT, Shape<4, 4, 2, 2, 1>, kCounted>(p, tiles, most, num_sms, stream);
   }
   if (p.tokens <= kMidTokens) {
-    if (r <= 16) return go<DT, Shape<1, 4, 1, 3, 2>, true>(p, tiles, most, num_sms, stream);
-    if (r <= 32) return go<DT, Shape<2, 4, 1, 3, 2>, true>(p, tiles, most, num_sms, stream);
-    if (r <= 64) return go<DT, Shape<4, 4, 1, 2, 2>, true>(p, tiles, most, num_sms, stream);
-    return go<DT, Shape<4, 4, 2, 2, 1>, true>(p, tiles, most, num_sms, stream);
+    if (r <= 16) return go<DT, Shape<1, 4, 1, 3, 2>, kListed>(p, tiles, most, num_sms, stream);
+    if (r <= 32) return go<DT, Shape<2, 4, 1, 3, 2>, kListed>(p, tiles, most, num_sms, stream);
+    if (r <= 64) return go<DT, Shape<4, 4, 1, 2, 2>, kListed>(p, tiles, most, num_sms, stream);
+    return go<DT, Shape<4, 4, 2, 2, 1>, kListed>(p, tiles, most, num_sms, stream);
   }
-  if (r <= 16) return go<DT, Shape<1, 8, 1, 2, 2>, true>(p, tiles, most, num_sms, stream);
-  if (r <= 32) return go<DT, Shape<2, 8, 1, 2, 2>, true>(p, tiles, most, num_sms, stream);
-  if (r <= 64) return go<DT, Shape<4, 8, 1, 3, 1>, true>(p, tiles, most, num_sms, stream);
-  return go<DT, Shape<4, 8, 2, 2, 1>, true>(p, tiles, most, num_sms, stream);
+  if (r <= 16) return go<DT, Shape<1, 8, 1, 2, 2>, kListed>(p, tiles, most, num_sms, stream);
+  if (r <= 32) return go<DT, Shape<2, 8, 1, 2, 2>, kListed>(p, tiles, most, num_sms, stream);
+  if (r <= 64) return go<DT, Shape<4, 8, 1, 3, 1>, kListed>(p, tiles, most, num_sms, stream);
+  return go<DT, Shape<4, 8, 2, 2, 1>, kListed>(p, tiles, most, num_sms, stream);
 }
 
 }  // namespace
 
+// Whether the CTAs find their tiles by themselves
+static bool alone(int64_t tokens, int64_t adapters) { return tokens <= kFewTokens || (tokens <= kCountTokens && adapters <= kCountAdapters); }
+
 size_t lora_workspace_bytes(int64_t tokens, int64_t adapters) {
-  if (tokens <= kFewTokens) return 0;
+  if (alone(tokens, adapters)) return 0;
   return 4096 + 256 + static_cast<size_t>((tokens * 4 + 255) / 256 * 256) + static_cast<size_t>(most_tiles(tokens, adapters)) * sizeof(Tile);
 }
 int lora_most_adapters() { return kMaxAdapters; }
@@ -620,6 +713,10 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
   // tiles, as far as can be told here, and at most
   int64_t tiles = std::min<int64_t>(a.tokens, a.tokens / kFewTile + a.adapters), most = a.tokens;
   if (!few) {
+    tiles = (a.tokens + sorted_tile(a.tokens) - 1) / sorted_tile(a.tokens) + std::min<int64_t>(a.adapters, a.tokens / 2) / 2;
+    most = most_tiles(a.tokens, a.adapters);
+  }
+  if (!alone(a.tokens, a.adapters)) {
     // (past the first 4 KiB: the counters of other calls)
     uint8_t *ws = static_cast<uint8_t *>(a.workspace) + 4096;
     int32_t *num = reinterpret_cast<int32_t *>(ws);
@@ -628,8 +725,6 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
     p.num_tiles = num;
     p.tiles = list;
     const int per = sorted_tile(a.tokens);
-    tiles = (a.tokens + per - 1) / per + std::min<int64_t>(a.adapters, a.tokens / 2) / 2;
-    most = most_tiles(a.tokens, a.adapters);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);

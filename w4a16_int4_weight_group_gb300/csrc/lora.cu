@@ -374,15 +374,13 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
         for (int i = tid; i < S::kSums; i += kThreads) {
           const int e = crank * share + i / csize, to = i % csize;
           const uint32_t mine = smem_u32(&part[e]);
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int c0 = 0; c0 < csize; c0 += 4) {  // four loads in flight together
-            float4 o[4];
+          float4 o[kMaxCluster];  // all loads in flight together
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = ld_dsmem_v4(map_to_rank(mine, min(c0 + c, csize - 1)));
+          for (int c = 0; c < kMaxCluster; ++c) o[c] = ld_dsmem_v4(map_to_rank(mine, min(c, csize - 1)));
+          float4 v = o[0];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (c0 + c < csize) v.x += o[c].x, v.y += o[c].y, v.z += o[c].z, v.w += o[c].w;
-          }
+          for (int c = 1; c < kMaxCluster; ++c)
+            if (c < csize) v.x += o[c].x, v.y += o[c].y, v.z += o[c].z, v.w += o[c].w;
           const int l = e & 31, n = (e >> 5) % NT, m = (e >> 5) / NT;
           const uint32_t at = map_to_rank(smem_u32(h + (n * 8 + 2 * (l & 3)) * S::kHStride + m * 16 + (l >> 2)), to);
           st_dsmem_f32(at, v.x * s), st_dsmem_f32(at + S::kHStride * 4, v.y * s);

@@ -610,72 +610,77 @@ int64_t most_tiles(int64_t tokens, int64_t adapters) {
 }
 
 template <class DT, class S, int TILING>
-cudaError_t go(Params p, int64_t tiles, int64_t most, int num_sms, cudaStream_t stream) {
-  constexpr int kCtas = S::kCtas;  // on an SM
-  static std::atomic<bool> asked[64];  // dynamic shared memory past 48 KB is asked for once a device
+cudaError_t go(Params p, int64_t tiles, int64_t most, const DeviceInfo &dev, cudaStream_t stream) {
+  constexpr int kDevices = 64;
   auto kernel = lora_kernel<DT, S, TILING>;
-  if (S::kSmem > 48 * 1024) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 64 || !asked[dev]) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-      if (e != cudaSuccess) return e;
-      if (dev < 64) asked[dev] = true;
-    }
-  }
-  // CTAs of a tile: up to eight, while all tiles' CTAs are resident together
-  int c = 1;
-  while (c < kMaxCluster && tiles * c * 2 <= int64_t(kCtas) * num_sms) c *= 2;
-  p.csize = c;
-  const int64_t clusters = std::min<int64_t>(most, int64_t(kCtas) * num_sms / c);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * c), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (c > 1) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(c);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
+  // Clusters of 1, 2, 4 and 8 CTAs that are resident at once (asked for once a device, with the shared memory past 48 KB): fewer
+  // than the SMs' CTAs divided by the size, since a cluster stays within a group of SMs (36 of eight at two CTAs on each of 152 SMs)
+  static std::atomic<int> resident[kDevices][4];
+  int room[4];
+  const bool kept = dev.device < kDevices;
+  for (int i = 0; i < 4; ++i) room[i] = kept ? resident[dev.device][i].load(std::memory_order_acquire) : 0;
+  if (room[0] == 0) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    for (int i = 3; i >= 0 && e == cudaSuccess; --i) {  // (the first entry, which says that all are there, last)
+      attr[0].val.clusterDim.x = 1u << i;
+      cfg.gridDim = dim3(8, 1, 1);
+      cfg.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&room[i], kernel, &cfg);
+      if (e == cudaSuccess && room[i] < 1) e = cudaErrorInvalidConfiguration;
+      if (e == cudaSuccess && kept) resident[dev.device][i].store(room[i], std::memory_order_release);
+    }
+    if (e != cudaSuccess) return e;
   }
+  // CTAs of a tile: up to eight, while all tiles are resident together
+  int c = 0;
+  while (c < 3 && tiles <= room[c + 1]) ++c;
+  p.csize = 1 << c;
+  attr[0].val.clusterDim.x = 1u << c;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(most, room[c]) << c), 1, 1);
+  if (c > 0) cfg.numAttrs = 2;
+  else cfg.attrs = attr + 1, cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e == cudaSuccess) note_launch();
   return e;
 }
 
 template <class DT>
-cudaError_t run(const Params &p, bool few, int64_t tiles, int64_t most, int num_sms, cudaStream_t stream) {
+cudaError_t run(const Params &p, bool few, int64_t tiles, int64_t most, const DeviceInfo &dev, cudaStream_t stream) {
   const int r = p.rank;
   if (few) {
-    if (r <= 16) return go<DT, Shape<1, 1, 1, 3, 3>, kRanked>(p, tiles, most, num_sms, stream);
-    if (r <= 32) return go<DT, Shape<2, 1, 1, 3, 3>, kRanked>(p, tiles, most, num_sms, stream);
-    if (r <= 64) return go<DT, Shape<4, 1, 1, 3, 2>, kRanked>(p, tiles, most, num_sms, stream);
-    return go<DT, Shape<4, 1, 2, 2, 1>, kRanked>(p, tiles, most, num_sms, stream);
+    if (r <= 16) return go<DT, Shape<1, 1, 1, 3, 3>, kRanked>(p, tiles, most, dev, stream);
+    if (r <= 32) return go<DT, Shape<2, 1, 1, 3, 3>, kRanked>(p, tiles, most, dev, stream);
+    if (r <= 64) return go<DT, Shape<4, 1, 1, 3, 2>, kRanked>(p, tiles, most, dev, stream);
+    return go<DT, Shape<4, 1, 2, 2, 1>, kRanked>(p, tiles, most, dev, stream);
   }
   if (!p.tiles) {
-    if (r <= 16) return go<DT, Shape<1, 4, 1, 3, 2>, kCounted>(p, tiles, most, num_sms, stream);
-    if (r <= 32) return go<DT, Shape<2, 4, 1, 3, 2>, kCounted>(p, tiles, most, num_sms, stream);
-    if (r <= 64) return go<DT, Shape<4, 4, 1, 2, 2>, kCounted>(p, tiles, most, num_sms, stream);
-    return go<DT, Shape<4, 4, 2, 2, 1>, kCounted>(p, tiles, most, num_sms, stream);
+    if (r <= 16) return go<DT, Shape<1, 4, 1, 3, 2>, kCounted>(p, tiles, most, dev, stream);
+    if (r <= 32) return go<DT, Shape<2, 4, 1, 3, 2>, kCounted>(p, tiles, most, dev, stream);
+    if (r <= 64) return go<DT, Shape<4, 4, 1, 2, 2>, kCounted>(p, tiles, most, dev, stream);
+    return go<DT, Shape<4, 4, 2, 2, 1>, kCounted>(p, tiles, most, dev, stream);
   }
   if (p.tokens <= kMidTokens) {
-    if (r <= 16) return go<DT, Shape<1, 4, 1, 3, 2>, kListed>(p, tiles, most, num_sms, stream);
-    if (r <= 32) return go<DT, Shape<2, 4, 1, 3, 2>, kListed>(p, tiles, most, num_sms, stream);
-    if (r <= 64) return go<DT, Shape<4, 4, 1, 2, 2>, kListed>(p, tiles, most, num_sms, stream);
-    return go<DT, Shape<4, 4, 2, 2, 1>, kListed>(p, tiles, most, num_sms, stream);
+    if (r <= 16) return go<DT, Shape<1, 4, 1, 3, 2>, kListed>(p, tiles, most, dev, stream);
+    if (r <= 32) return go<DT, Shape<2, 4, 1, 3, 2>, kListed>(p, tiles, most, dev, stream);
+    if (r <= 64) return go<DT, Shape<4, 4, 1, 2, 2>, kListed>(p, tiles, most, dev, stream);
+    return go<DT, Shape<4, 4, 2, 2, 1>, kListed>(p, tiles, most, dev, stream);
   }
-  if (r <= 16) return go<DT, Shape<1, 8, 1, 2, 2>, kListed>(p, tiles, most, num_sms, stream);
-  if (r <= 32) return go<DT, Shape<2, 8, 1, 2, 2>, kListed>(p, tiles, most, num_sms, stream);
-  if (r <= 64) return go<DT, Shape<4, 8, 1, 3, 1>, kListed>(p, tiles, most, num_sms, stream);
-  return go<DT, Shape<4, 8, 2, 2, 1>, kListed>(p, tiles, most, num_sms, stream);
+  if (r <= 16) return go<DT, Shape<1, 8, 1, 2, 2>, kListed>(p, tiles, most, dev, stream);
+  if (r <= 32) return go<DT, Shape<2, 8, 1, 2, 2>, kListed>(p, tiles, most, dev, stream);
+  if (r <= 64) return go<DT, Shape<4, 8, 1, 3, 1>, kListed>(p, tiles, most, dev, stream);
+  return go<DT, Shape<4, 8, 2, 2, 1>, kListed>(p, tiles, most, dev, stream);
 }
 
 }  // namespace
@@ -737,7 +742,7 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
     if (e != cudaSuccess) return e;
     note_launch();
   }
-  return a.dtype == W4A16_BF16 ? run<BF16>(p, few, tiles, most, dev.num_sms, a.stream) : run<F16>(p, few, tiles, most, dev.num_sms, a.stream);
+  return a.dtype == W4A16_BF16 ? run<BF16>(p, few, tiles, most, dev, a.stream) : run<F16>(p, few, tiles, most, dev, a.stream);
 }
 
 }  // namespace w4a16

@@ -202,3 +202,51 @@ def test_a_compiled_step_keeps_one_graph(w, backend):
     want = fn(*args, r1, table, c1)
     got = torch.compile(fn, backend=backend, fullgraph=True)(*args, r2, table, c2)
     assert all(torch.equal(x, y) for x, y in zip(got, want)) and torch.equal(r1, r2) and torch.equal(c1, c2)
+
+
+def test_ordinary_calls_and_the_bindings_own_agree(w, monkeypatch):
+    """The module of ordinary calls makes the same calls as the binding, and leaves it those that it has something to say about."""
+    from w4a16_int4_weight_group_gb300 import step
+    if not step._bind_fast():
+        pytest.skip("the module of ordinary calls was not built")
+    made = []
+
+    class Count:
+        def __getattr__(self, name):
+            def call(*a):
+                out = getattr(fast, name)(*a)
+                made.append((name, out is not None))
+                return out
+            return call
+
+    fast = step._fast
+    lora, verify, refs, table, cache = cases()
+    r1, c1, r2, c2 = refs.clone(), cache.clone(), refs.clone(), cache.clone()
+    monkeypatch.setattr(step, "_fast", Count())
+    got = everything(w, lora, verify, r1, table, c1)
+    # 1500 tokens need a workspace, which is the binding's
+    assert made == [("lora", True), ("lora", False), ("lora", True), ("verify_drafts", True), ("verify_drafts", True), ("kv_fork", True),
+                    ("kv_reserve", True), ("kv_copy", True), ("kv_compact", True), ("kv_free", True)]
+    monkeypatch.setattr(step, "_fast", False)
+    want = everything(w, lora, verify, r2, table, c2)
+    assert all(torch.equal(x, y) and x.dtype == y.dtype and x.stride() == y.stride() for x, y in zip(got, want))
+    assert torch.equal(r1, r2) and torch.equal(c1, c2)
+    monkeypatch.setattr(step, "_fast", fast)
+    c = lora[0]
+    before = w.w4a16_debug_launch_count()
+    for kw, error in ((dict(ids=c["ids"].long()), ValueError), (dict(x=c["x"].t().contiguous().t()), ValueError), (dict(a=c["a"][:, :4].contiguous()), ValueError),
+                      (dict(out=c["base"][:2]), ValueError), (dict(out=c["x"][:, :264]), w.W4A16Error), (dict(scales=c["scales"].double()), ValueError),
+                      (dict(base=c["base"].cpu()), ValueError), (dict(x=c["x"].float()), w.W4A16Error)):
+        with pytest.raises(error):
+            w.w4a16_lora(**{**c, **kw})
+    v = verify[0]
+    for kw, error in ((dict(max_q=65), w.W4A16Error), (dict(max_q=2 ** 40), w.W4A16Error), (dict(tokens=v["tokens"].int()), ValueError),
+                      (dict(draft_probs=torch.zeros_like(v["logits"], dtype=torch.float32)), w.W4A16Error), (dict(noise=v["noise"][:2]), ValueError)):
+        with pytest.raises(error):
+            w.w4a16_verify_drafts(**{**v, **kw})
+    for fn, args in ((w.w4a16_kv_fork, (refs, table, table[:, 0].contiguous(), table[0], 0)), (w.w4a16_kv_reserve, (refs, table, refs[:3], refs[:3], 2 ** 33)),
+                     (w.w4a16_kv_free, (refs, table.t(), refs[:6], 16)), (w.w4a16_kv_copy, (cache, table[:, :3])),
+                     (w.w4a16_kv_compact, (cache, 256, table, refs[:3], table))):
+        with pytest.raises((ValueError, w.W4A16Error)):
+            fn(*args)
+    assert w.w4a16_debug_launch_count() == before

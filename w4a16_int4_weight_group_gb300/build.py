@@ -28,6 +28,10 @@ SOURCES = ["api.cu", "pack.cu", "gemm_generic.cu", "gemm_decode.cu", "gemm_prefi
 # cannot be built, e.g. without the Python headers)
 PYCALL_SRC = os.path.join(CSRC, "pycall.c")
 PYCALL_PATH = os.path.join(HERE, "_w4a16_call" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+# The ordinary calls of the operators around a step of many users on tensors, against torch's own headers (optional: without it the
+# binding reads the tensors from Python)
+FAST_SRC = os.path.join(CSRC, "fastcall.cpp")
+FAST_PATH = os.path.join(HERE, "_w4a16_fast" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
                      "-I", INCLUDE, "-Xptxas", "-warn-spills"]
@@ -74,10 +78,39 @@ def build_pycall(force: bool = False) -> bool:
     return True
 
 
+def build_fast(force: bool = False) -> bool:
+    """Compile the module of ordinary calls beside the library; False when it cannot be built."""
+    header = os.path.join(INCLUDE, "w4a16.h")
+    if not force and os.path.exists(FAST_PATH) and os.path.getmtime(FAST_PATH) >= max(os.path.getmtime(FAST_SRC), os.path.getmtime(header)):
+        return True
+    inc = sysconfig.get_paths().get("include")
+    cxx = shutil.which(os.environ.get("CXX", "c++")) or shutil.which("g++")
+    try:
+        import torch
+        top = os.path.dirname(torch.__file__)
+        cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    except (ImportError, RuntimeError):
+        return False
+    if not cxx or not inc or not os.path.exists(os.path.join(inc, "Python.h")) or not os.path.isdir(os.path.join(top, "include")):
+        return False
+    tmp = FAST_PATH + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", inc, "-I", INCLUDE,
+           "-isystem", os.path.join(top, "include"), "-isystem", os.path.join(top, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
+           FAST_SRC, "-o", tmp, "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        if os.environ.get("W4A16_BUILD_VERBOSE"):
+            print(r.stderr, file=sys.stderr)
+        return False
+    os.replace(tmp, FAST_PATH)
+    return True
+
+
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
     """Compile and link libw4a16.so (sm_103a) and the marshalling module. Returns the library path."""
     build_pycall(force)
     if not force and up_to_date():
+        build_fast(force)
         return LIB_PATH
     nvcc = _nvcc()
     os.makedirs(OBJ_DIR, exist_ok=True)
@@ -93,8 +126,10 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
         return obj
 
     jobs = jobs or min(len(SOURCES), os.cpu_count() or 4)
-    with ThreadPoolExecutor(max_workers=jobs) as ex:
+    with ThreadPoolExecutor(max_workers=jobs + 1) as ex:
+        fast = ex.submit(build_fast, force)
         objs = list(ex.map(compile_one, SOURCES))
+        fast.result()
     tmp = LIB_PATH + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs, "-lrt", "-ldl", "-lpthread"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -61,6 +61,24 @@ def _bind():
     return _calls
 
 
+_fast = None  # the module of ordinary calls (see csrc/fastcall.cpp), False when it was not built
+
+
+def _bind_fast():
+    """The calls that check ordinary tensors and make them in one step of C++. Each returns None where there is something to say or
+    to provide; the functions below then go their own way."""
+    global _fast
+    L = lib()
+    try:
+        from . import _w4a16_fast as m
+        m.bind(*(ctypes.cast(getattr(L, "w4a16_" + n), _vp).value
+                 for n in ("lora", "verify_drafts", "kv_fork", "kv_reserve", "kv_free", "kv_copy", "kv_compact", "lora_workspace_size")))
+        _fast = m
+    except ImportError:
+        _fast = False
+    return _fast
+
+
 class _Ctypes:
     """The flat calls of the marshalling module through ctypes."""
 
@@ -127,6 +145,12 @@ def w4a16_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Ten
     keeps one for each stream, and one for each capture by torch.cuda.graph. Calls of up to 256 tokens need none, nor those of up to 1024 tokens
     and 512 adapters.
     """
+    if workspace is None:
+        fast = _bind_fast() if _fast is None else _fast
+        if fast:
+            y = fast.lora(x, a, b, ids, base, scales, out)
+            if y is not None:
+                return y
     sx, sa, sb = x.shape, a.shape, b.shape
     if len(sx) != 2 or len(sa) != 3 or len(sb) != 3:
         raise ValueError("x must be [tokens, k], a [adapters, rank, k] and b [adapters, n, rank]")
@@ -206,21 +230,8 @@ def w4a16_verify_drafts(logits: torch.Tensor, tokens: torch.Tensor, uniforms: to
     code = 2 if dtype is torch.float32 else _code(dtype)
     total, V = s
     B = sn[0]
-    la = _rows(logits, "logits", dtype, s, dev)
-    na = _rows(noise, "noise", torch.float32, (B, V), dev)
-    tp = _index(tokens, "tokens", torch.int64, (total,), dev)
-    up = _index(uniforms, "uniforms", torch.float32, (total,), dev)
-    qp = 0 if q_start is None else _index(q_start, "q_start", torch.int32, (B + 1,), dev)
-    mp = 0 if tree_mask is None else _index(tree_mask, "tree_mask", torch.int64, (total,), dev)
-    da = (0, 0) if draft_probs is None else _rows(draft_probs, "draft_probs", torch.float32, s, dev)
-    ep = 0 if temperature is None else _index(temperature, "temperature", torch.float32, (B,), dev)
     if max_q is None:
         max_q = 1 if q_start is None else max(1, min(total, 64))
-    m = max(0, min(max_q, 64))  # (a max_q out of range is refused by the call)
-    accepted = torch.empty(B, dtype=torch.int32, device=device)
-    path = torch.empty((B, m), dtype=torch.int32, device=device)
-    out = torch.empty((B, m), dtype=torch.int64, device=device)
-    probs = torch.empty((B, m), dtype=torch.float32, device=device)
     stream = _current_stream(dev)
     if workspace is not None:
         wb = workspace.numel()
@@ -232,6 +243,24 @@ def w4a16_verify_drafts(logits: torch.Tensor, tokens: torch.Tensor, uniforms: to
             need = _verify_ws[key] = w4a16_verify_drafts_workspace_size(total, V)
         ws = workspace_for(device, stream, need)
         wp, wb = ws.data_ptr(), ws.numel()
+    fast = _bind_fast() if _fast is None else _fast
+    if fast:
+        y = fast.verify_drafts(logits, tokens, uniforms, noise, q_start, tree_mask, draft_probs, temperature, max_q, wp, wb)
+        if y is not None:
+            return y
+    la = _rows(logits, "logits", dtype, s, dev)
+    na = _rows(noise, "noise", torch.float32, (B, V), dev)
+    tp = _index(tokens, "tokens", torch.int64, (total,), dev)
+    up = _index(uniforms, "uniforms", torch.float32, (total,), dev)
+    qp = 0 if q_start is None else _index(q_start, "q_start", torch.int32, (B + 1,), dev)
+    mp = 0 if tree_mask is None else _index(tree_mask, "tree_mask", torch.int64, (total,), dev)
+    da = (0, 0) if draft_probs is None else _rows(draft_probs, "draft_probs", torch.float32, s, dev)
+    ep = 0 if temperature is None else _index(temperature, "temperature", torch.float32, (B,), dev)
+    m = max(0, min(max_q, 64))  # (a max_q out of range is refused by the call)
+    accepted = torch.empty(B, dtype=torch.int32, device=device)
+    path = torch.empty((B, m), dtype=torch.int32, device=device)
+    out = torch.empty((B, m), dtype=torch.int64, device=device)
+    probs = torch.empty((B, m), dtype=torch.float32, device=device)
     st = (_calls or _bind()).verify_drafts(*la, total, V, code, tp, qp, B, max_q, mp, up, *na, *da, ep, accepted.data_ptr(), path.data_ptr(),
                                            out.data_ptr(), probs.data_ptr(), wp, wb, stream)
     if st:
@@ -257,6 +286,11 @@ def w4a16_kv_fork(refs: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.T
                   page_size: int) -> Tuple[torch.Tensor, torch.Tensor]:
     """(new_table, new_lens): sequences that share the pages of `parents` (int32 [rows], rows of page_table [batch, max_pages]; one out
     of range: an empty sequence). refs (int32 [pages]) counts the new holders."""
+    fast = _bind_fast() if _fast is None else _fast
+    if fast:
+        y = fast.kv_fork(refs, page_table, kv_lens, parents, page_size)
+        if y is not None:
+            return y
     dev = _device(refs)
     if dev != _current_device():
         with torch.cuda.device(dev):
@@ -281,6 +315,11 @@ def w4a16_kv_reserve(refs: torch.Tensor, page_table: torch.Tensor, kv_lens: torc
     """(held, copies): free pages for the tokens up to new_lens (int32 [batch]) go into page_table, and a partly filled last page that others
     hold too is replaced by a page of the sequence's own: copies int32 [batch, 2] says {from, to} (else -1, -1), for
     w4a16_kv_copy. held int32 [batch]: the tokens that there is room for then (new_lens, unless pages ran out)."""
+    fast = _bind_fast() if _fast is None else _fast
+    if fast:
+        y = fast.kv_reserve(refs, page_table, kv_lens, new_lens, page_size)
+        if y is not None:
+            return y
     dev = _device(refs)
     if dev != _current_device():
         with torch.cuda.device(dev):
@@ -300,6 +339,11 @@ def w4a16_kv_reserve(refs: torch.Tensor, page_table: torch.Tensor, kv_lens: torc
 def w4a16_kv_free(refs: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, page_size: int,
                   keep: Optional[torch.Tensor] = None) -> None:
     """Gives back the pages of the tokens from keep (int32 [batch]; None: all) on: refs shrink, the table's entries become -1."""
+    fast = _bind_fast() if _fast is None else _fast
+    if fast:
+        y = fast.kv_free(refs, page_table, kv_lens, page_size, keep)
+        if y is not None:
+            return
     dev = _device(refs)
     if dev != _current_device():
         with torch.cuda.device(dev):
@@ -334,6 +378,11 @@ def _layers(cache: torch.Tensor, head_dim: Optional[int], dev: int):
 def w4a16_kv_copy(cache: torch.Tensor, copies: torch.Tensor) -> None:
     """Copies whole pages of the cache (all layers of a stack): copies int32 [n, 2], {from, to}; pairs with a page out of range (-1) are
     skipped. No page is written twice, or both read and written."""
+    fast = _bind_fast() if _fast is None else _fast
+    if fast:
+        y = fast.kv_copy(cache, copies)
+        if y is not None:
+            return
     dev = _device(cache)
     if dev != _current_device():
         with torch.cuda.device(dev):
@@ -354,6 +403,11 @@ def w4a16_kv_compact(cache: torch.Tensor, head_dim: int, page_table: torch.Tenso
 
     path int32 [batch, max_q] as w4a16_verify_drafts gives it; q_start int32 [batch + 1]: the sequence's drafted tokens are the last
     q_start[b + 1] - q_start[b] of kv_lens (None: 1). Their pages belong to one sequence each (see w4a16_kv_reserve)."""
+    fast = _bind_fast() if _fast is None else _fast
+    if fast:
+        y = fast.kv_compact(cache, head_dim, page_table, kv_lens, path, q_start)
+        if y is not None:
+            return y
     dev = _device(cache)
     if dev != _current_device():
         with torch.cuda.device(dev):

@@ -96,7 +96,7 @@ def build_fast(force: bool = False) -> bool:
     tmp = FAST_PATH + ".tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", inc, "-I", INCLUDE,
            "-isystem", os.path.join(top, "include"), "-isystem", os.path.join(top, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
-           FAST_SRC, "-o", tmp, "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           FAST_SRC, "-o", tmp, "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         if os.environ.get("W4A16_BUILD_VERBOSE"):

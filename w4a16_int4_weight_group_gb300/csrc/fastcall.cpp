@@ -11,6 +11,7 @@
  *   bind(lora, verify_drafts, kv_fork, kv_reserve, kv_free, kv_copy, kv_compact, lora_workspace_size)   addresses
  */
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <Python.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -62,7 +63,8 @@ bool has_rows(const at::Tensor *t, int dev, ScalarType type, int64_t rows, int64
 bool half_type(ScalarType t) { return t == ScalarType::Half || t == ScalarType::BFloat16; }
 w4a16_dtype code(ScalarType t) { return t == ScalarType::Half ? W4A16_F16 : t == ScalarType::BFloat16 ? W4A16_BF16 : W4A16_F32; }
 at::Tensor make(std::initializer_list<int64_t> shape, ScalarType type, const at::Tensor &like) {
-  return at::empty(c10::IntArrayRef(shape), at::TensorOptions().dtype(type).device(like.device()));
+  // (what at::empty comes to, without its dispatch)
+  return at::detail::empty_cuda(c10::IntArrayRef(shape), type, like.device(), c10::nullopt);
 }
 w4a16_stream_t stream_of(int dev) {
   return reinterpret_cast<w4a16_stream_t>(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());

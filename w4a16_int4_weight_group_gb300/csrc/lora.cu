@@ -19,8 +19,11 @@
 // those of their adapter by itself, up to kCountTokens it counts them by adapter in shared memory (one launch); more are sorted by a
 // kernel before this one (counting sort). The composition of a tile does not change a token's result: the rows of an MMA do not mix and K is split in the same way.
 //
-// Bound by memory: base read and out written are most of the bytes for long prompts, A and B of every adapter for single
-// tokens.
+// Bound by memory for long prompts (base read and out written are most of the bytes), by mma.sync for ranks past 32 (the second product
+// takes two for each), by the chain of copies, barriers and sums for few tokens. Measured, replayed from a graph: 8191 tokens 5120 -> 7168 of rank
+// 32 75 us for 328 MB, 4.4 TB/s, 0.65 of the device's copy rate (9 us of them the sort and the launch; the same tiles copied without
+// an adapter 0.85 of it while they stream); DRAM 53 %, tensor pipe 31 %, schedulers 42 % of the cycles. 520 tokens 2560 -> 3840 of rank 64 21
+// us; 48 tokens 5120 -> 7168 of rank 16 9.0; one token 2112 -> 1152 4.2.
 #include <algorithm>
 #include <atomic>
 
@@ -33,9 +36,13 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxCluster = 8;
-constexpr int kFewTokens = 256;  // one thread for each
+// One thread for each. Ranked against counted, 5120 -> 7168, 256 tokens of 32 adapters: 15.1 against 16.1 us (rank 16), 22.4 against
+// 25.1 (rank 64); 64 tokens: 9.2 against 12.9, 19.8 against 23.5.
+constexpr int kFewTokens = 256;
 constexpr int kFewTile = 8;      // tokens of a tile then
-// Up to this many tokens of this many adapters a CTA counts the tokens of each adapter in shared memory
+// Up to this many tokens of this many adapters a CTA counts the tokens of each adapter in shared memory. On the GPU as long as sorted by
+// a kernel before (2560 -> 3840, rank 64: 400 tokens 20.0 against 19.3 us, 1000 tokens 19.4 against 19.2), with a launch less to
+// issue (3.8 against 14 us, a workspace among it).
 constexpr int kCountTokens = 1024, kCountAdapters = 512;
 constexpr int kSortThreads = 1024;
 constexpr int kMaxAdapters = 8191;  // counters of the sort in shared memory
@@ -155,7 +162,6 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
   const int crank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
   griddep_wait();
-  griddep_launch_dependents();
 
   int my_id = -2, my_rank = 0, ntiles;
   if constexpr (TILING == kListed) {
@@ -519,6 +525,9 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
     }
     __syncthreads();  // done with the tile's tables and the ring
   }
+  // Only now: CTAs of the next kernel that start while this one runs all go to the SMs that it leaves free, two on one while others
+  // have none (1000 tokens of rank 64, call after call: 28 us, 19 with this)
+  griddep_launch_dependents();
 }
 
 // Counting sort of the tokens by adapter (those without one last), and the list of tiles. One CTA.
@@ -601,8 +610,10 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *
   }
 }
 
-// Tokens of a sorted tile: 32 while there are few of them (two CTAs on an SM at every rank, and clusters of eight: 520 tokens
-// 2560 -> 3840 of rank 64 TIME32 against TIME64 with 64), else 64 (A and B are read half as often)
+// Tokens of a sorted tile: 32 while there are few of them, else 64 (A and B are read half as often, for fewer and larger shares
+// of work). 2560 -> 3840, 16 adapters: 1500 tokens 18.1 us with 32 and 19.2 with 64 (rank 16), 25.7 and 27.5 (rank 64), 2000 tokens
+// 18.7 and 19.5, 26.4 and 38.4. 5120 -> 7168, 8191 tokens of 12 adapters (with the sort): rank 16 83 and 77, rank 32 84 and 80,
+// rank 64 109 and 113, rank 128 193 and 168.
 constexpr int64_t kMidTokens = 2048;
 int sorted_tile(int64_t tokens) { return tokens <= kMidTokens ? 32 : 64; }
 int64_t most_tiles(int64_t tokens, int64_t adapters) {

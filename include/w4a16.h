@@ -427,15 +427,15 @@ size_t w4a16_lora_workspace_size(int64_t tokens, int rank, int64_t adapters);
  * what comes out has the distribution of the target's own samples.
  *   logits       [total, vocab], rows row_stride elements apart, F16, BF16 or F32: row i is the target's, after token i
  *   tokens       int64 [total]: of each sequence its last token (the root, which is not judged), then the drafted ones
- *   q_start      int32 [batch + 1]: sequence b has the tokens q_start[b] .. q_start[b + 1] - 1, the first max_q (<= 64) of which
- *                count; NULL: one for each sequence (total == batch), which is plain sampling
+ *   q_start      int32 [batch + 1], ascending: sequence b has the tokens q_start[b] .. q_start[b + 1] - 1, the first max_q (<= 64)
+ *                of which count; NULL: one for each sequence (total == batch), which is plain sampling
  *   tree_mask    uint64 [total], as for w4a16_tree_attention: a token's parent is the highest bit below its own (a token
  *                without one cannot stand); NULL: chains
  *   uniforms     float32 [total], in [0, 1): token i's own
  *   noise        float32 [batch, vocab], rows noise_stride elements apart, positive: exponential numbers
  *   draft_probs  float32 [total, vocab], rows draft_stride elements apart, or NULL; only without tree_mask: row i is the
  *                distribution that the token after token i was drawn from
- *   temperature  float32 [batch] or NULL (1): 0 (all probability on the largest logit, the lowest index of equal ones) or positive
+ *   temperature  float32 [batch] or NULL (1): 0 (all probability on the largest logit, the lowest index of equal ones) or positive and finite
  * p = softmax(row / temperature). With draft_probs q, token d stands if u q(d) < p(d); the first that does not is replaced by a
  * draw from max(p - q, 0). Without, the children of a token are judged in ascending order: child d stands if u Z < p(d), Z being 1 minus the
  * p of the ones rejected at that token so far (p(d) counts as 0 for a token rejected there before); when none stands, the draw is from p
@@ -445,7 +445,7 @@ size_t w4a16_lora_workspace_size(int64_t tokens, int rank, int64_t adapters);
  *   path         int32 [batch, max_q]: indices (within the sequence) of the root and the accepted tokens, then -1
  *   out_tokens   int64 [batch, max_q]: the accepted tokens and the one after them, then -1
  *   out_probs    float32 [batch, max_q]: the target's probability of each, then 0
- * A row with a NaN or +infinity, or without a finite logit, has no probabilities: none of its children stands, and the token after it is
+ * A row with a NaN or +infinity, without a finite logit, or with a temperature that is negative or NaN, has no probabilities: none of its children stands, and the token after it is
  * -1, with probability NaN. A sequence without tokens gives accepted 0 and path and out_tokens of -1.
  *   workspace    device memory, 256-byte aligned, w4a16_verify_drafts_workspace_size bytes; its first 4 KiB are not touched.
  * Errors: INVALID_ARG, UNSUPPORTED (dtype, max_q, draft_probs with tree_mask), MISALIGNED, CUDA.

@@ -229,6 +229,14 @@ def test_verify_rows_without_probabilities(w):
             assert out[0][0] == 0 and out[2][0, 0] == -1
 
 
+def test_temperatures_out_of_range(w):
+    c = make_verify([3, 2, 4, 2], 900, "bf16", False, False, seed=8, temps=[-1.0, math.nan, 1e-30, 0.0])
+    out = w.w4a16_verify_drafts(**cuda(c))
+    assert out[2][:2, 0].tolist() == [-1, -1] and out[0][:2].tolist() == [0, 0] and torch.isnan(out[3][:2, 0]).all()
+    best = c["logits"][5].float()
+    assert int(out[2][2, 0]) == int((best == best.max()).nonzero()[0]) or int(out[0][2]) > 0  # a tiny one is as good as none
+
+
 def test_verify_borders(w):
     V = 600
     c = make_verify([3, 3], V, "f32", False, False, seed=7)

@@ -250,3 +250,59 @@ def test_ordinary_calls_and_the_bindings_own_agree(w, monkeypatch):
         with pytest.raises((ValueError, w.W4A16Error)):
             fn(*args)
     assert w.w4a16_debug_launch_count() == before
+
+
+FRESH = """
+import torch
+import w4a16_int4_weight_group_gb300 as w
+from tests.test_step_together import cases, everything, i32_cached
+lora, verify, refs, table, cache = cases()
+for x in ([40, 16, 90], [0, 2, 2, 1], [50, 95, 100, 40], [[0, 2, 4], [0, 1, -1], [3, 2, 1], [0, -1, -1]], [0, 5, 8, 12, 13]):
+    i32_cached(x)
+refs2, cache2 = refs.clone(), cache.clone()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = everything(w, lora, verify, refs, table, cache)
+g.replay()
+torch.cuda.synchronize()
+want = everything(w, lora, verify, refs2, table, cache2)
+assert all(torch.equal(x, y) for x, y in zip(got, want)) and torch.equal(refs, refs2) and torch.equal(cache, cache2)
+print("equal")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured(w):
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FRESH], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "equal" in r.stdout, r.stdout + r.stderr
+
+
+def test_two_threads_at_once(w):
+    """Host threads with a stream each, first calls of their shapes among them."""
+    import threading
+    c = [make_lora(T, 136, 264, 24, 4, "bf16", seed=T) for T in (3, 130, 300, 1100)]
+    dc = [cuda(x) for x in c]
+    v = make_verify([4, 5], 5001, "bf16", False, True, seed=5)
+    dv = cuda(v)
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(20):
+                    got[i] = w.w4a16_lora(**dc[i]), w.w4a16_verify_drafts(**dv)
+            s.synchronize()
+        except Exception as e:  # (told by the main thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    for i in range(4):
+        check_lora(w, c[i], "bf16", got[i][0])
+        check_verify(w, v, got[i][1])

@@ -3,13 +3,14 @@
 //     out_t = base_t + s_i (x_t A_i^T) B_i^T,   i = ids[t];  A_i [r, K], B_i [N, r]
 //
 // One kernel does both products; h = x A^T (r numbers a token) never leaves the SMs. A cluster of CTAs takes a tile of tokens
-// of one adapter. First product: the CTAs and their warps split K, so that A and x are read once a tile, each
-// straight from global memory into the fragments of mma.m16n8k16 (adapter rows on the M side, tokens on the N side). The order
-// of k within a sum is free, so a lane's 16 contiguous bytes of a row serve as its elements of two MMAs, for both operands
-// alike: no shared memory, no shuffles. The warps' partial sums are added in shared memory, the CTAs' through
-// distributed shared memory, in a fixed order. Second product: the CTAs and warps split N, tokens on the M side, h as
-// the A operand from shared memory; the columns of four n-tiles are dealt out so that a lane ends up with eight contiguous
-// columns of a token: 16-byte loads of base and stores of out.
+// of one adapter. First product: the CTAs and their warps split K, so that A and x are read once a tile, as fragments of
+// mma.m16n8k16 (adapter rows on the M side, tokens on the N side). The order of k within a sum is free, so a lane's 16
+// contiguous bytes of a row serve as its elements of two MMAs, for both operands alike: asynchronous copies bring them into slots that
+// only this thread reads, a stage ahead of the MMAs, with no barrier and no bank conflict. The slices' partial sums are added in shared
+// memory, the CTAs' through distributed shared memory, in a fixed order. Second product: the CTAs and warps split N, tokens on the M
+// side, h as the A operand from shared memory; the columns of four n-tiles are dealt out so that a lane ends up with eight
+// contiguous columns of a token: 16-byte copies of base and stores of out. (Steps of 128 instead of 64 bytes a row, in a ring that a warp
+// shares: the first product alone 3 us faster, the second 7 slower, since half the warps fit.)
 //
 // h is fp32 and goes into the second product as two numbers of the dtype, the upper part and the rest: 16 bits of it for
 // bfloat16, 22 below the token's largest for float16 (whose range its sums may leave: each token's h is scaled by a power
@@ -17,7 +18,8 @@
 //
 // Tiles: tokens of the same adapter wherever they stand. Up to kFewTokens tokens every CTA ranks the tokens among
 // those of their adapter by itself, up to kCountTokens it counts them by adapter in shared memory (one launch); more are sorted by a
-// kernel before this one (counting sort). The composition of a tile does not change a token's result: the rows of an MMA do not mix and K is split in the same way.
+// kernel before this one (counting sort). The composition of a tile does not change a token's result: the rows of an MMA do not mix
+// and K is split in the same way.
 //
 // Bound by memory for long prompts (base read and out written are most of the bytes), by mma.sync for ranks past 32 (the second product
 // takes two for each), by the chain of copies, barriers and sums for few tokens. Measured, replayed from a graph: 8191 tokens 5120 -> 7168 of rank

@@ -9,7 +9,11 @@
 // All of it is bytes moved or integers counted. reserve is one CTA, bound by the latency of its steps (holders of the
 // same page counted against each other in shared memory, sums over the sequences, free pages counted 4096 at a time); copy is
 // bound by memory; compact by the latency of load, barrier, store: a CTA reads all tokens of a sequence that move, for one
-// head and layer, before it writes one, so that a place may be read and written in any order.
+// head and some layers, before it writes one, so that a place may be read and written in any order.
+//
+// Measured: 128 pages of 128 tokens, 8 heads of 128 at 8 bits, in 8 layers copied in 62 us (553 MB, 8.9 TB/s with part of the writes left in
+// L2; the step of fork, reserve, copy, free and two copies of the tables 86 us replayed); reserve 8 to 12 us alone, fork and free 4 to 6.
+// compact: 64 sequences of up to 16 tokens in 16 layers 6.5 us replayed (a layer a CTA: 19 us a call), 4 of 8 in one layer 3.0.
 #include <algorithm>
 
 #include "common.cuh"

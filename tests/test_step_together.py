@@ -306,3 +306,22 @@ def test_two_threads_at_once(w):
     for i in range(4):
         check_lora(w, c[i], "bf16", got[i][0])
         check_verify(w, v, got[i][1])
+
+
+def test_bounded_waits_of_the_adapters_report_timeout_and_recover(w):
+    """No MMA is issued, so the waits for them run out: the status says so, and the next call is right."""
+    for r in (40, 128):
+        c = make_lora(2100, 200, 136, r, 2, "bf16", seed=r)
+        d = cuda(c)
+        assert w.w4a16_get_device_error() == 0
+        try:
+            w.w4a16_debug_set_wait_limit_ns(5_000_000)
+            w.w4a16_debug_inject_stall(True)
+            w.w4a16_lora(**d)
+            torch.cuda.synchronize()
+            assert w.w4a16_get_device_error() == 5  # W4A16_ERR_TIMEOUT
+        finally:
+            w.w4a16_debug_inject_stall(False)
+            w.w4a16_debug_set_wait_limit_ns(0)
+        assert w.w4a16_get_device_error() == 0
+        check_lora(w, c, "bf16", w.w4a16_lora(**d))

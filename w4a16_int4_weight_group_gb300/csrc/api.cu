@@ -700,12 +700,13 @@ uint64_t w4a16_stream_capture_id(w4a16_stream_t stream) {
 w4a16_status w4a16_get_device_error(void) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_fail(e, "synchronise");
-  uint32_t err = 0, err2 = 0, err3 = 0;
+  uint32_t err = 0, err2 = 0, err3 = 0, err4 = 0;
   e = prefill_take_device_error(&err);
   if (e == cudaSuccess) e = decode_take_device_error(&err2);
   if (e == cudaSuccess) e = attention_take_device_error(&err3);
+  if (e == cudaSuccess) e = lora_take_device_error(&err4);
   if (e != cudaSuccess) return cuda_fail(e, "read device error word");
-  err |= err2 | err3;
+  err |= err2 | err3 | err4;
   if (err) return fail(W4A16_ERR_TIMEOUT, "a bounded device-side wait gave up (code 0x%x)", err);
   return ok();
 }
@@ -732,6 +733,7 @@ w4a16_status w4a16_debug_set_wait_limit_ns(uint64_t ns) {
   cudaError_t e = prefill_set_wait_limit_ns(ns);
   if (e == cudaSuccess) e = decode_set_wait_limit_ns(ns);
   if (e == cudaSuccess) e = attention_set_wait_limit_ns(ns);
+  if (e == cudaSuccess) e = lora_set_wait_limit_ns(ns);
   if (e != cudaSuccess) return cuda_fail(e, "set wait limit");
   return ok();
 }
@@ -740,6 +742,7 @@ w4a16_status w4a16_debug_inject_stall(int on) {
   cudaError_t e = prefill_set_stall(on != 0);
   if (e == cudaSuccess) e = decode_set_stall(on != 0);
   if (e == cudaSuccess) e = attention_set_stall(on != 0);
+  if (e == cudaSuccess) e = lora_set_stall(on != 0);
   if (e != cudaSuccess) return cuda_fail(e, "set stall hook");
   return ok();
 }

@@ -217,8 +217,11 @@ struct LoraArgs {
 };
 cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev);
 // 0: none is needed
-size_t lora_workspace_bytes(int64_t tokens, int64_t adapters);
+size_t lora_workspace_bytes(int64_t tokens, int rank, int64_t adapters);
 int lora_most_adapters();
+cudaError_t lora_take_device_error(uint32_t *err);
+cudaError_t lora_set_wait_limit_ns(uint64_t ns);
+cudaError_t lora_set_stall(bool on);
 
 struct VerifyArgs {
   const void *logits;

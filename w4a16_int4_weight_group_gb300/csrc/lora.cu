@@ -29,10 +29,10 @@
 #include <algorithm>
 #include <atomic>
 
-#include "common.cuh"
-#include "internal.h"
+#include "lora_common.cuh"
 
 namespace w4a16 {
+using namespace lora;
 namespace {
 
 constexpr int kWarps = 8;
@@ -49,10 +49,6 @@ constexpr int kCountTokens = 1024, kCountAdapters = 512;
 constexpr int kSortThreads = 1024;
 constexpr int kMaxAdapters = 8191;  // counters of the sort in shared memory
 
-struct Tile {
-  int adapter, first, count;  // of the sorted tokens
-};
-
 struct Params {
   const uint16_t *x, *a, *b, *base;
   uint16_t *out;
@@ -67,45 +63,6 @@ struct Params {
   const Tile *tiles;
   const int32_t *num_tiles;
 };
-
-// upper and lower part of two numbers, as pairs of the dtype
-template <class DT>
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-  float ha, hb;
-  if constexpr (DT::kBF16) {  // truncated, so that a finite number's upper part is finite
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    hi = prmt(ua, ub, 0x7632);
-    ha = __uint_as_float(ua & 0xFFFF0000u), hb = __uint_as_float(ub & 0xFFFF0000u);
-    if (!(a == a)) hi |= 0x7FFFu;  // a NaN's payload may lie in the lost bits
-    if (!(b == b)) hi |= 0x7FFF0000u;
-  } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    hi = *reinterpret_cast<const uint32_t *>(&h);
-    ha = __low2float(h), hb = __high2float(h);
-  }
-  // an infinite or NaN number has no rest
-  const float ra = fabsf(a) < INFINITY ? a - ha : 0.f, rb = fabsf(b) < INFINITY ? b - hb : 0.f;
-  if constexpr (DT::kBF16) {
-    const __nv_bfloat162 l = __floats2bfloat162_rn(ra, rb);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
-  } else {
-    const __half2 l = __floats2half2_rn(ra, rb);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
-  }
-}
-
-// a pair of the dtype plus two sums (times a power of two), each rounded once
-template <class DT>
-__device__ __forceinline__ void add2(uint32_t &w, float a, float b, float f) {
-  if constexpr (DT::kBF16) {
-    const __nv_bfloat162 r = __floats2bfloat162_rn(__uint_as_float(w << 16) + a, __uint_as_float(w & 0xFFFF0000u) + b);
-    w = *reinterpret_cast<const uint32_t *>(&r);
-  } else {
-    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-    const __half2 r = __floats2half2_rn(fmaf(a, f, x.x), fmaf(b, f, x.y));
-    w = *reinterpret_cast<const uint32_t *>(&r);
-  }
-}
 
 // MR, NT: m-tiles (adapter rows) and n-tiles (tokens) of a warp's first product; RS: parts of the rank, each with its warps
 template <int MR_, int NT_, int RS_, int STAGES, int CTAS>
@@ -404,16 +361,14 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
         }
         __syncthreads();
       }
-      if constexpr (!DT::kBF16) {  // power of two that brings a token's largest to [2^13, 2^14)
+      if constexpr (!DT::kBF16) {  // each token's power of two
         for (int i = tid >> 3; i < S::kTokens; i += kThreads / 8) {  // eight threads a token
           float top = 0.f;
           for (int r = tid & 7; r < p.rank; r += 8) top = fmaxf(top, fabsf(h[i * S::kHStride + r]));  // (a NaN does not count)
           const unsigned eight = 0xFFu << (lane & 24);
 #pragma unroll
           for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(eight, top, o));
-          const int e = static_cast<int>(__float_as_uint(top) >> 23);  // 0: zero or subnormal; 255: infinite
-          const int d = e == 0 || e == 255 ? 0 : max(-126, min(126, e - 127 - 13));
-          if ((tid & 7) == 0) back[i] = __uint_as_float(static_cast<uint32_t>(127 + d) << 23);
+          if ((tid & 7) == 0) back[i] = unit_of_largest(top);
         }
         __syncthreads();
       }
@@ -617,9 +572,12 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *
 // 18.7 and 19.5, 26.4 and 38.4. 5120 -> 7168, 8191 tokens of 12 adapters (with the sort): rank 16 83 and 77, rank 32 84 and 80,
 // rank 64 109 and 113, rank 128 193 and 168.
 constexpr int64_t kMidTokens = 2048;
-int sorted_tile(int64_t tokens) { return tokens <= kMidTokens ? 32 : 64; }
-int64_t most_tiles(int64_t tokens, int64_t adapters) {
-  return tokens / sorted_tile(tokens) + std::min<int64_t>(tokens, adapters + 1);
+constexpr int kMidRank = 32;
+// More tokens of larger ranks go to the form on tcgen05.
+bool on_tcgen05(int64_t tokens, int rank) { return tokens > kMidTokens && rank > kMidRank; }
+int sorted_tile(int64_t tokens, int rank) { return tokens <= kMidTokens ? 32 : on_tcgen05(tokens, rank) ? kLongTile : 64; }
+int64_t most_tiles(int64_t tokens, int rank, int64_t adapters) {
+  return tokens / sorted_tile(tokens, rank) + std::min<int64_t>(tokens, adapters + 1);
 }
 
 template <class DT, class S, int TILING>
@@ -691,9 +649,7 @@ cudaError_t run(const Params &p, bool few, int64_t tiles, int64_t most, const De
     return go<DT, Shape<4, 4, 2, 2, 1>, kListed>(p, tiles, most, dev, stream);
   }
   if (r <= 16) return go<DT, Shape<1, 8, 1, 2, 2>, kListed>(p, tiles, most, dev, stream);
-  if (r <= 32) return go<DT, Shape<2, 8, 1, 2, 2>, kListed>(p, tiles, most, dev, stream);
-  if (r <= 64) return go<DT, Shape<4, 8, 1, 3, 1>, kListed>(p, tiles, most, dev, stream);
-  return go<DT, Shape<4, 8, 2, 2, 1>, kListed>(p, tiles, most, dev, stream);
+  return go<DT, Shape<2, 8, 1, 2, 2>, kListed>(p, tiles, most, dev, stream);
 }
 
 }  // namespace
@@ -701,9 +657,14 @@ cudaError_t run(const Params &p, bool few, int64_t tiles, int64_t most, const De
 // Whether the CTAs find their tiles by themselves
 static bool alone(int64_t tokens, int64_t adapters) { return tokens <= kFewTokens || (tokens <= kCountTokens && adapters <= kCountAdapters); }
 
-size_t lora_workspace_bytes(int64_t tokens, int64_t adapters) {
+// The workspace past the first 4 KiB (the counters of other calls): the number of tiles, the sorted tokens, the tiles, h
+static size_t tiles_at(int64_t tokens) { return 256 + static_cast<size_t>((tokens * 4 + 255) / 256 * 256); }
+static size_t h_at(int64_t tokens, int rank, int64_t adapters) {
+  return tiles_at(tokens) + (static_cast<size_t>(most_tiles(tokens, rank, adapters)) * sizeof(Tile) + 255) / 256 * 256;
+}
+size_t lora_workspace_bytes(int64_t tokens, int rank, int64_t adapters) {
   if (alone(tokens, adapters)) return 0;
-  return 4096 + 256 + static_cast<size_t>((tokens * 4 + 255) / 256 * 256) + static_cast<size_t>(most_tiles(tokens, adapters)) * sizeof(Tile);
+  return 4096 + h_at(tokens, rank, adapters) + (on_tcgen05(tokens, rank) ? long_workspace_bytes(tokens, rank, adapters) : 0);
 }
 int lora_most_adapters() { return kMaxAdapters; }
 
@@ -729,18 +690,17 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
   // tiles, as far as can be told here, and at most
   int64_t tiles = std::min<int64_t>(a.tokens, a.tokens / kFewTile + a.adapters), most = a.tokens;
   if (!few) {
-    tiles = (a.tokens + sorted_tile(a.tokens) - 1) / sorted_tile(a.tokens) + std::min<int64_t>(a.adapters, a.tokens / 2) / 2;
-    most = most_tiles(a.tokens, a.adapters);
+    tiles = (a.tokens + sorted_tile(a.tokens, a.rank) - 1) / sorted_tile(a.tokens, a.rank) + std::min<int64_t>(a.adapters, a.tokens / 2) / 2;
+    most = most_tiles(a.tokens, a.rank, a.adapters);
   }
   if (!alone(a.tokens, a.adapters)) {
-    // (past the first 4 KiB: the counters of other calls)
     uint8_t *ws = static_cast<uint8_t *>(a.workspace) + 4096;
     int32_t *num = reinterpret_cast<int32_t *>(ws);
     p.order = reinterpret_cast<int32_t *>(ws + 256);
-    Tile *list = reinterpret_cast<Tile *>(ws + 256 + (a.tokens * 4 + 255) / 256 * 256);
+    Tile *list = reinterpret_cast<Tile *>(ws + tiles_at(a.tokens));
     p.num_tiles = num;
     p.tiles = list;
-    const int per = sorted_tile(a.tokens);
+    const int per = sorted_tile(a.tokens, a.rank);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
@@ -754,6 +714,8 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
     const cudaError_t e = cudaLaunchKernelEx(&cfg, lora_sort_kernel, a.ids, static_cast<int>(a.tokens), p.adapters, per, p.copy, p.order, list, num);
     if (e != cudaSuccess) return e;
     note_launch();
+    if (on_tcgen05(a.tokens, a.rank))
+      return launch_long(a, dev, p.order, list, num, reinterpret_cast<float *>(ws + h_at(a.tokens, a.rank, a.adapters)));
   }
   return a.dtype == W4A16_BF16 ? run<BF16>(p, few, tiles, most, dev, a.stream) : run<F16>(p, few, tiles, most, dev, a.stream);
 }

@@ -1,0 +1,506 @@
+// Low-rank adapters of many tokens: both products on tcgen05, for sorted tiles of 128 tokens of one adapter.
+//
+//     h = x A^T,   out = base + s h B^T
+//
+// Two kernels. The first multiplies 128 gathered rows of x by A, 64 elements of K a step, K split over CTAs where the tiles do
+// not fill the device; fp32 sums go from tensor memory to a workspace (r numbers a token and part of K). The second adds the
+// parts, multiplies by s, keeps h as two numbers of the dtype, upper part and rest (float16: scaled by a power of two a
+// token), as an operand in shared memory, and multiplies it by columns of B, the rest's and the upper part's product into the
+// same accumulators; each thread adds a row of base to a row of these, and the rows go out in pieces of 128 bytes and more.
+//
+// All copies are asynchronous 16-byte ones (rows are gathered, so there is no box to describe) into the 128-byte swizzle, a stage
+// or more ahead of the MMAs that one thread issues; waits for MMAs are bounded, and the threads of a CTA vote before each
+// barrier, so that all give up together.
+//
+// Taken instead of the warp-level form where that is bound by mma.sync: for ranks past 32 (its second product takes two for each).
+// TIMES
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "lora_common.cuh"
+
+namespace w4a16 {
+namespace lora {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct Control {
+  unsigned int error;
+  unsigned int stall;  // no MMA is issued: the waits run out
+  unsigned long long limit_ns;
+};
+__device__ Control g_lora_control = {0u, 0u, 2000000000ull};
+
+struct Params {
+  const uint4 *x, *a, *b, *base;
+  uint4 *out;
+  const float *scales;
+  int64_t x_stride, base_stride, out_stride;  // in units of 16 bytes
+  int64_t tokens;
+  uint32_t k_units, n_units, r_units;  // of 8 elements
+  int r16;                             // the rank, rounded up to 16
+  int splits, per_split;               // of K, in blocks of 64 elements
+  int slices;                          // of N
+  bool copy;
+  const int32_t *order;
+  const Tile *tiles;
+  const int32_t *num_tiles;
+  float *h;  // [split][sorted token][r16]
+  Control *control;
+};
+
+// ---- tcgen05 and its shared-memory operands (K-major, 128-byte swizzle, eight rows in 1024 bytes)
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]),
+        "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// start >> 4 in bits 0-13, leading byte offset >> 4 in 16-29, stride byte offset >> 4 in 32-45, the fixed 0b001 in 46-48, swizzle mode
+// in 61-63 (2: 128 bytes)
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16u >> 4) << 16) | (static_cast<uint64_t>(1024u >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+template <class DT>
+__device__ __forceinline__ uint32_t idesc_of(int n) {  // D fp32, A and B of the dtype, both K-major, 128 x n
+  constexpr uint32_t t = DT::kBF16 ? 1u : 0u;
+  return (1u << 4) | (t << 7) | (t << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kLongTile >> 4) << 24);
+}
+// Byte offset of unit c (16 bytes) of a row in a tile of `rows` rows: pieces of 64 elements one after another, swizzled
+__device__ __forceinline__ uint32_t place(int row, int c, int rows) {
+  return static_cast<uint32_t>((c >> 3) * rows * 128 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+}
+
+// What a CTA's threads share, in front of its tiles
+struct Shared {
+  uint64_t stage_bar[4], done_bar, drain_bar;
+  uint32_t tmem, abort;
+  float back[kLongTile];
+};
+constexpr int kShared = 1024;
+static_assert(sizeof(Shared) <= kShared, "");
+
+// The start and the end of both kernels: barriers and tensor memory
+__device__ __forceinline__ void begin(Shared *sh, uint32_t cols) {
+  if (threadIdx.x == 0) {
+    for (uint64_t &b : sh->stage_bar) mbar_init(smem_u32(&b), 1);
+    mbar_init(smem_u32(&sh->done_bar), 1);
+    mbar_init(smem_u32(&sh->drain_bar), 1);
+    sh->abort = 0;
+    mbar_init_fence();
+  }
+  if (threadIdx.x < 32) tmem_alloc(smem_u32(&sh->tmem), cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+__device__ __forceinline__ void finish(Shared *sh, uint32_t cols, bool ok, Control *control) {
+  cp_async_wait<0>();
+  if (!ok && threadIdx.x == 0) {  // MMAs that are still under way
+    umma_commit(smem_u32(&sh->drain_bar));
+    drain_phase(smem_u32(&sh->drain_bar), 0, &control->error);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x < 32) tmem_dealloc(sh->tmem, cols);
+  griddep_launch_dependents();
+}
+
+// First product. RA: pieces of 64 of the rank
+template <class DT, int RA>
+__global__ void __launch_bounds__(kThreads, 2) long_first_kernel(const Params p) {
+  constexpr int kX = kLongTile * 128, kA = RA * 64 * 128, kStage = kX + kA, S = RA == 1 ? 4 : 3;
+  extern __shared__ uint8_t raw[];
+  uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  Shared *sh = reinterpret_cast<Shared *>(smem);
+  const uint32_t stages = smem_u32(smem) + kShared;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_wait();
+  begin(sh, 128);
+  const uint32_t tmem = sh->tmem, abort_flag = smem_u32(&sh->abort);
+  const uint64_t limit = p.control->limit_ns;
+  const bool stall = p.control->stall != 0;
+  const int64_t items = int64_t(*p.num_tiles) * p.splits;
+  const int blocks = static_cast<int>((p.k_units + 7) / 8);
+  const uint32_t idesc = idesc_of<DT>(p.r16);
+  uint32_t t = 0, done = 0;  // blocks and items so far
+  bool ok = true;
+  for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    const Tile d = p.tiles[item / p.splits];
+    const int split = static_cast<int>(item % p.splits);
+    if (d.adapter < 0) continue;  // (the same for the CTA)
+    const int b0 = split * p.per_split, nb = min(b0 + p.per_split, blocks) - b0;
+    const uint4 *a = p.a + int64_t(d.adapter) * p.r_units * 8 * p.k_units;
+    const int c = tid & 7;
+    uint32_t xr[4];  // (rows past the tile's last are the last one again: their sums are not stored)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) xr[j] = static_cast<uint32_t>(p.order[d.first + min(j * 32 + (tid >> 3), d.count - 1)] * p.x_stride);
+    auto fetch = [&](int i, uint32_t at) {  // block i of the item into the stage of the at-th block
+      const uint32_t k = static_cast<uint32_t>(b0 + i) * 8 + c;
+      const bool in = k < p.k_units;
+      const uint32_t kk = in ? k : 0, to = stages + at % S * kStage;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) cp_async_16(to + place(j * 32 + (tid >> 3), c, kLongTile), p.x + (xr[j] + kk), in);
+#pragma unroll
+      for (int j = 0; j < 2 * RA; ++j) {  // rows past the rank are zeros
+        const uint32_t row = j * 32 + (tid >> 3);
+        const bool has = in && row < p.r_units * 8;
+        cp_async_16(to + kX + row * 128 + ((c ^ (row & 7)) << 4), a + (has ? row * p.k_units + kk : 0), has);
+      }
+    };
+    // the stage of the at-th block is free: its last MMAs are done
+    auto freed = [&](uint32_t at) {
+      return at < S || wait_phase(smem_u32(&sh->stage_bar[at % S]), (at / S - 1) & 1, abort_flag, limit, &p.control->error);
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+      if (i < nb && ok) ok = freed(t + i);
+      if (i < nb && ok) fetch(i, t + i);
+      cp_async_commit();
+    }
+    for (int i = 0; i < nb; ++i) {
+      if (i + S - 1 < nb && ok) ok = freed(t + i + S - 1);
+      if (i + S - 1 < nb && ok) fetch(i + S - 1, t + i + S - 1);
+      cp_async_commit();
+      cp_async_wait<S - 1>();
+      fence_proxy_async_smem();
+      ok = __syncthreads_and(ok);
+      if (!ok) break;
+      if (tid == 0 && !stall) {
+        tc_fence_after();
+        const uint32_t at = stages + (t + i) % S * kStage;
+        const uint64_t xd = smem_desc(at), ad = smem_desc(at + kX);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma(tmem, xd + 2 * kk, ad + 2 * kk, idesc, i > 0 || kk > 0);
+        umma_commit(smem_u32(&sh->stage_bar[(t + i) % S]));
+        if (i == nb - 1) umma_commit(smem_u32(&sh->done_bar));
+      }
+    }
+    if (!ok) break;
+    t += nb;
+    ok = wait_phase(smem_u32(&sh->done_bar), done & 1, abort_flag, limit, &p.control->error);
+    ++done;
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+    tc_fence_after();
+    const int row = (warp & 3) * 32 + lane;
+    float *to = p.h + (int64_t(split) * p.tokens + d.first + row) * p.r16;
+    for (int c0 = (warp >> 2) * 16; c0 < p.r16; c0 += 32) {
+      float v[16];
+      tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, v);
+      tmem_wait_ld();
+      if (row < d.count)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) reinterpret_cast<float4 *>(to + c0)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    }
+    tc_fence_before();
+    __syncthreads();  // the accumulators have been read
+  }
+  finish(sh, 128, ok, p.control);
+}
+
+// Second product. NC: columns of a step
+template <class DT, int RA, int NC>
+__global__ void __launch_bounds__(kThreads, RA == 1 ? 2 : 1) long_second_kernel(const Params p) {
+  constexpr int kH = 2 * RA * kLongTile * 128, kB = RA * NC * 128, kBase = kLongTile * NC * 2, kRow = NC / 8;  // kRow: units of a row of base
+  extern __shared__ uint8_t raw[];
+  uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  Shared *sh = reinterpret_cast<Shared *>(smem);
+  uint8_t *hs = smem + kShared, *bs = hs + kH, *os = bs + 2 * kB;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_wait();
+  begin(sh, NC);
+  const uint32_t tmem = sh->tmem, abort_flag = smem_u32(&sh->abort);
+  const uint64_t limit = p.control->limit_ns;
+  const bool stall = p.control->stall != 0;
+  const int64_t items = int64_t(*p.num_tiles) * p.slices;
+  const int chunks = static_cast<int>((p.n_units + kRow - 1) / kRow), per = (chunks + p.slices - 1) / p.slices;
+  uint32_t done = 0;
+  bool ok = true;
+  for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
+    const Tile d = p.tiles[item / p.slices];
+    const int j0 = static_cast<int>(item % p.slices) * per, n = min(j0 + per, chunks) - j0;
+    if (n <= 0 || (d.adapter < 0 && !p.copy)) continue;
+    const uint4 *b = p.b + int64_t(max(d.adapter, 0)) * p.n_units * 8 * p.r_units;
+    const int32_t *tok = p.order + d.first;
+    const int c = tid % kRow;  // this thread's unit of the rows that it copies
+    constexpr int kRows = kLongTile * kRow / kThreads, kStep = kThreads / kRow;
+    int my[kRows];  // their tokens, -1 past the tile's last
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int row = j * kStep + tid / kRow;
+      my[j] = row < d.count ? tok[row] : -1;
+    }
+    auto fetch = [&](int i) {
+      const uint32_t n0 = static_cast<uint32_t>(j0 + i) * kRow;
+      const uint32_t to = smem_u32(os) + (i & 1) * kBase, bt = smem_u32(bs) + (i & 1) * kB;
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+        if (my[j] >= 0 && n0 + c < p.n_units) cp_async_16(to + place(j * kStep + tid / kRow, c, kLongTile), p.base + (my[j] * p.base_stride + n0 + c), true);
+      if (d.adapter >= 0) {
+        const uint32_t cols = (p.n_units - n0) * 8;
+#pragma unroll
+        for (int j = 0; j < NC * RA * 8 / kThreads; ++j) {  // columns and ranks past the ends are zeros
+          const uint32_t u = j * kThreads + tid, col = u / (RA * 8), cu = u % (RA * 8);
+          const bool in = col < cols && cu < p.r_units;
+          cp_async_16(bt + place(col, cu, NC), b + (in ? uint64_t(n0 * 8 + col) * p.r_units + cu : 0), in);
+        }
+      }
+    };
+    fetch(0);
+    cp_async_commit();
+    if (d.adapter >= 0) {
+      // h: the parts of K added, times s; two threads a token, every other unit of eight ranks each
+      const int row = tid >> 1;
+      const float s = p.scales ? p.scales[d.adapter] : 1.f;
+      float v[RA * 4][8];
+      float top = 0.f;
+#pragma unroll
+      for (int q = 0; q < RA * 4; ++q) {
+        const int r0 = (2 * q + (tid & 1)) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[q][e] = 0.f;
+        if (r0 < p.r16 && row < d.count) {
+          const float *from = p.h + int64_t(d.first + row) * p.r16 + r0;
+          for (int sp = 0; sp < p.splits; ++sp) {
+            const float4 lo = *reinterpret_cast<const float4 *>(from), hi = *reinterpret_cast<const float4 *>(from + 4);
+            v[q][0] += lo.x, v[q][1] += lo.y, v[q][2] += lo.z, v[q][3] += lo.w, v[q][4] += hi.x, v[q][5] += hi.y, v[q][6] += hi.z, v[q][7] += hi.w;
+            from += p.tokens * p.r16;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[q][e] *= s;
+            top = fmaxf(top, fabsf(v[q][e]));  // (a NaN does not count)
+          }
+        }
+      }
+      float f = 1.f;
+      if constexpr (!DT::kBF16) {
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        const float unit = unit_of_largest(top);
+        f = 1.f / unit;  // (exact: a power of two)
+        if ((tid & 1) == 0) sh->back[row] = unit;
+      }
+#pragma unroll
+      for (int q = 0; q < RA * 4; ++q) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split2<DT>(v[q][2 * e] * f, v[q][2 * e + 1] * f, hi[e], lo[e]);
+        const uint32_t at = place(row, 2 * q + (tid & 1), kLongTile);
+        *reinterpret_cast<uint4 *>(hs + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(hs + RA * kLongTile * 128 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+    for (int i = 0; i < n; ++i) {
+      if (i + 1 < n) fetch(i + 1);
+      cp_async_commit();
+      cp_async_wait<1>();
+      fence_proxy_async_smem();
+      __syncthreads();
+      uint8_t *ot = os + (i & 1) * kBase;
+      if (d.adapter >= 0) {
+        if (tid == 0 && !stall) {
+          tc_fence_after();
+          const uint64_t hd = smem_desc(smem_u32(hs)), bd = smem_desc(smem_u32(bs) + (i & 1) * kB);
+          const uint32_t idesc = idesc_of<DT>(NC);
+          for (int kk = 0; kk < p.r16 / 16; ++kk) {
+            const uint64_t ho = ((kk >> 2) * kLongTile * 128 + (kk & 3) * 32) >> 4, bo = ((kk >> 2) * NC * 128 + (kk & 3) * 32) >> 4;
+            umma(tmem, hd + (RA * kLongTile * 128 >> 4) + ho, bd + bo, idesc, kk > 0);
+            umma(tmem, hd + ho, bd + bo, idesc, 1);
+          }
+          umma_commit(smem_u32(&sh->done_bar));
+        }
+        ok = wait_phase(smem_u32(&sh->done_bar), done & 1, abort_flag, limit, &p.control->error);
+        ++done;
+        ok = __syncthreads_and(ok);
+        if (!ok) break;
+        tc_fence_after();
+        // a thread's row, half of its columns
+        const int row = (warp & 3) * 32 + lane;
+        float f = 1.f;
+        if constexpr (!DT::kBF16) f = sh->back[row];
+#pragma unroll
+        for (int c0 = 0; c0 < NC / 2; c0 += 16) {
+          const int col = (warp >> 2) * (NC / 2) + c0;
+          float v[16];
+          tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + col, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint4 *at = reinterpret_cast<uint4 *>(ot + place(row, col / 8 + u, kLongTile));
+            uint4 w = *at;
+            add2<DT>(w.x, v[8 * u], v[8 * u + 1], f), add2<DT>(w.y, v[8 * u + 2], v[8 * u + 3], f);
+            add2<DT>(w.z, v[8 * u + 4], v[8 * u + 5], f), add2<DT>(w.w, v[8 * u + 6], v[8 * u + 7], f);
+            *at = w;
+          }
+        }
+        tc_fence_before();
+        __syncthreads();
+      }
+      const uint32_t n0 = static_cast<uint32_t>(j0 + i) * kRow;
+#pragma unroll
+      for (int j = 0; j < kRows; ++j)
+        if (my[j] >= 0 && n0 + c < p.n_units)
+          __stcs(p.out + (my[j] * p.out_stride + n0 + c), *reinterpret_cast<const uint4 *>(ot + place(j * kStep + tid / kRow, c, kLongTile)));
+      __syncthreads();  // the stage may be filled again
+    }
+  }
+  finish(sh, NC, ok, p.control);
+}
+
+// CTAs that are resident at two on each of a GB300's 152 SMs; K is split by it whatever the device, so that the workspace depends on the
+// sizes alone
+constexpr int kRoom = 304;
+int64_t tiles_about(int64_t tokens, int64_t adapters) {
+  return (tokens + kLongTile - 1) / kLongTile + std::min<int64_t>(adapters, tokens / 2) / 2;
+}
+int most_splits(int64_t tokens, int64_t adapters) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, kRoom / tiles_about(tokens, adapters))));
+}
+int rounded(int rank) { return (rank + 15) / 16 * 16; }
+
+template <class K>
+cudaError_t prepare(K kernel, int smem, int device, std::atomic<bool> (&asked)[64]) {
+  if (device < 64 && asked[device].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && device < 64) asked[device].store(true, std::memory_order_release);
+  return e;
+}
+
+template <class DT, int RA, int NC>
+cudaError_t go(Params p, int64_t about, const DeviceInfo &dev, cudaStream_t stream) {
+  constexpr int kFirst = kShared + 1024 + (RA == 1 ? 4 : 3) * (kLongTile * 128 + RA * 64 * 128);
+  constexpr int kSecond = kShared + 1024 + 2 * RA * kLongTile * 128 + 2 * (RA * NC * 128 + kLongTile * NC * 2);
+  static std::atomic<bool> asked_first[64], asked_second[64];
+  cudaError_t e = prepare(long_first_kernel<DT, RA>, kFirst, dev.device, asked_first);
+  if (e == cudaSuccess) e = prepare(long_second_kernel<DT, RA, NC>, kSecond, dev.device, asked_second);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * dev.num_sms), 1, 1);
+  cfg.dynamicSmemBytes = kFirst;
+  e = cudaLaunchKernelEx(&cfg, long_first_kernel<DT, RA>, p);
+  if (e != cudaSuccess) return e;
+  note_launch();
+  // slices of N: the number whose last wave costs least, a slice's h counting as much as two of its steps
+  const int resident = (RA == 1 ? 2 : 1) * dev.num_sms;
+  const int64_t chunks = (p.n_units + NC / 8 - 1) / (NC / 8);
+  double best = 0;
+  for (int64_t s = 1; s <= std::min<int64_t>(chunks, 32); ++s) {
+    const double waves = static_cast<double>((about * s + resident - 1) / resident), cost = waves * (2.0 + static_cast<double>((chunks + s - 1) / s));
+    if (s == 1 || cost < best) best = cost, p.slices = static_cast<int>(s);
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(resident), 1, 1);
+  cfg.dynamicSmemBytes = kSecond;
+  e = cudaLaunchKernelEx(&cfg, long_second_kernel<DT, RA, NC>, p);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+cudaError_t control_of(int device, Control **out) {
+  static std::mutex mu;
+  static Control *known[64] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  if (device < 64 && known[device]) {
+    *out = known[device];
+    return cudaSuccess;
+  }
+  void *ptr = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&ptr, g_lora_control);
+  if (e != cudaSuccess) return e;
+  *out = static_cast<Control *>(ptr);
+  if (device < 64) known[device] = *out;
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t long_workspace_bytes(int64_t tokens, int rank, int64_t adapters) {
+  return static_cast<size_t>(most_splits(tokens, adapters)) * static_cast<size_t>(tokens) * rounded(rank) * 4;
+}
+
+cudaError_t launch_long(const LoraArgs &a, const DeviceInfo &dev, const int32_t *order, const Tile *tiles, const int32_t *num_tiles, float *h) {
+  Params p{};
+  p.x = static_cast<const uint4 *>(a.x);
+  p.a = static_cast<const uint4 *>(a.a);
+  p.b = static_cast<const uint4 *>(a.b);
+  p.base = static_cast<const uint4 *>(a.base);
+  p.out = static_cast<uint4 *>(a.out);
+  p.scales = a.scales;
+  p.x_stride = a.x_stride / 8;
+  p.base_stride = a.base_stride / 8;
+  p.out_stride = a.out_stride / 8;
+  p.tokens = a.tokens;
+  p.k_units = static_cast<uint32_t>(a.K / 8);
+  p.n_units = static_cast<uint32_t>(a.N / 8);
+  p.r_units = static_cast<uint32_t>(a.rank / 8);
+  p.r16 = rounded(a.rank);
+  const int blocks = static_cast<int>((a.K + 63) / 64);
+  const int splits = std::min(most_splits(a.tokens, a.adapters), blocks);
+  p.per_split = (blocks + splits - 1) / splits;
+  p.splits = (blocks + p.per_split - 1) / p.per_split;
+  p.copy = a.base != a.out;
+  p.order = order;
+  p.tiles = tiles;
+  p.num_tiles = num_tiles;
+  p.h = h;
+  const cudaError_t e = control_of(dev.device, &p.control);
+  if (e != cudaSuccess) return e;
+  const int64_t about = tiles_about(a.tokens, a.adapters);
+  if (a.dtype == W4A16_BF16)
+    return a.rank <= 64 ? go<BF16, 1, 64>(p, about, dev, a.stream) : go<BF16, 2, 128>(p, about, dev, a.stream);
+  return a.rank <= 64 ? go<F16, 1, 64>(p, about, dev, a.stream) : go<F16, 2, 128>(p, about, dev, a.stream);
+}
+
+}  // namespace lora
+
+cudaError_t lora_take_device_error(uint32_t *err) {
+  lora::Control c;
+  cudaError_t e = cudaMemcpyFromSymbol(&c, lora::g_lora_control, sizeof(c));
+  if (e != cudaSuccess) return e;
+  *err = c.error;
+  c.error = 0;
+  return *err ? cudaMemcpyToSymbol(lora::g_lora_control, &c, sizeof(c)) : cudaSuccess;
+}
+cudaError_t lora_set_wait_limit_ns(uint64_t ns) {
+  const unsigned long long v = ns ? ns : 2000000000ull;
+  return cudaMemcpyToSymbol(lora::g_lora_control, &v, sizeof(v), offsetof(lora::Control, limit_ns));
+}
+cudaError_t lora_set_stall(bool on) {
+  const unsigned int v = on ? 1u : 0u;
+  return cudaMemcpyToSymbol(lora::g_lora_control, &v, sizeof(v), offsetof(lora::Control, stall));
+}
+
+}  // namespace w4a16

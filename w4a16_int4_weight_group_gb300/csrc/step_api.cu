@@ -77,7 +77,7 @@ extern "C" {
 
 size_t w4a16_lora_workspace_size(int64_t tokens, int rank, int64_t adapters) {
   if (tokens < 0 || tokens >= kMaxTokens || rank < 1 || rank > kMaxRank || adapters < 1 || adapters > lora_most_adapters()) return 0;
-  return lora_workspace_bytes(tokens, adapters);
+  return lora_workspace_bytes(tokens, rank, adapters);
 }
 
 w4a16_status w4a16_lora(const void *x, int64_t x_stride, const void *a, const void *b, const int32_t *ids, const float *scales, const void *base,
@@ -101,7 +101,7 @@ w4a16_status w4a16_lora(const void *x, int64_t x_stride, const void *a, const vo
   if (!a || !b || !ids) return fail(W4A16_ERR_INVALID_ARG, "a, b and ids must not be NULL");
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(ids, 4) || !aligned(scales, 4))
     return fail(W4A16_ERR_MISALIGNED, "a and b must be 16-byte, ids and scales 4-byte aligned");
-  const size_t need = lora_workspace_bytes(tokens, adapters);
+  const size_t need = lora_workspace_bytes(tokens, rank, adapters);
   if (need && (!workspace || workspace_bytes < need))
     return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : size_t(0), need);
   if (workspace && !aligned(workspace, 256)) return fail(W4A16_ERR_MISALIGNED, "workspace must be 256-byte aligned");

@@ -664,7 +664,7 @@ static size_t h_at(int64_t tokens, int rank, int64_t adapters) {
 }
 size_t lora_workspace_bytes(int64_t tokens, int rank, int64_t adapters) {
   if (alone(tokens, adapters)) return 0;
-  return 4096 + h_at(tokens, rank, adapters) + (on_tcgen05(tokens, rank) ? long_workspace_bytes(tokens, rank, adapters) : 0);
+  return 4096 + h_at(tokens, rank, adapters) + (on_tcgen05(tokens, rank) ? long_workspace_bytes(tokens, rank) : 0);
 }
 int lora_most_adapters() { return kMaxAdapters; }
 

@@ -60,7 +60,7 @@ __device__ __forceinline__ void add2(uint32_t &w, float a, float b, float f) {
 // The form for many tokens (sorted tiles of kLongTile tokens, lists in `order`, `tiles` and `num_tiles`; h: workspace)
 constexpr int kLongTile = 128;
 cudaError_t launch_long(const LoraArgs &a, const DeviceInfo &dev, const int32_t *order, const Tile *tiles, const int32_t *num_tiles, float *h);
-size_t long_workspace_bytes(int64_t tokens, int rank, int64_t adapters);
+size_t long_workspace_bytes(int64_t tokens, int rank);
 
 }  // namespace lora
 }  // namespace w4a16

@@ -2,10 +2,10 @@
 //
 //     h = x A^T,   out = base + s h B^T
 //
-// Two kernels. The first multiplies 128 gathered rows of x by A, 64 elements of K a step, K split over CTAs where the tiles do
-// not fill the device; fp32 sums go from tensor memory to a workspace (r numbers a token and part of K). The second adds the
-// parts, multiplies by s, keeps h as two numbers of the dtype, upper part and rest (float16: scaled by a power of two a
-// token), as an operand in shared memory, and multiplies it by columns of B, the rest's and the upper part's product into the
+// Two kernels. The first multiplies 128 gathered rows of x by A, 64 elements of K a step, K split over the CTAs of a cluster where the tiles
+// do not fill the device; their fp32 sums are added through distributed shared memory, in order, and go to a workspace (r numbers a
+// token). The second multiplies them by s, puts h as two numbers of the dtype, upper part and rest (float16: scaled by a power of two a
+// token), into tensor memory, and multiplies it by columns of B, the rest's and the upper part's product into the
 // same accumulators; each thread adds a row of base to a row of these, and the rows go out in pieces of 128 bytes and more.
 //
 // All copies are asynchronous 16-byte ones (rows are gathered, so there is no box to describe) into the 128-byte swizzle, a stage
@@ -25,6 +25,9 @@ namespace lora {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kCols = 64;  // of a step of the second product
+template <int RA>
+constexpr int kSecondStages = RA == 1 ? 4 : 3;  // of 24 and 32 KB
 
 struct Control {
   unsigned int error;
@@ -41,13 +44,13 @@ struct Params {
   int64_t tokens;
   uint32_t k_units, n_units, r_units;  // of 8 elements
   int r16;                             // the rank, rounded up to 16
-  int splits, per_split;               // of K, in blocks of 64 elements
+  int csize, per_split;                // CTAs of a tile in the first product, and blocks of 64 elements of K for each
   int slices;                          // of N
   bool copy;
   const int32_t *order;
   const Tile *tiles;
   const int32_t *num_tiles;
-  float *h;  // [split][sorted token][r16]
+  float *h;  // [sorted token][r16]
   Control *control;
 };
 
@@ -68,6 +71,21 @@ __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// the same with A in tensor memory: a lane a row, two elements of k a column
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+               "r"(r[13]), "r"(r[14]), "r"(r[15])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
@@ -100,9 +118,9 @@ __device__ __forceinline__ uint32_t place(int row, int c, int rows) {
 struct Shared {
   uint64_t stage_bar[4], done_bar, drain_bar;
   uint32_t tmem, abort;
-  float back[kLongTile];
+  float back[2][kLongTile];  // of each half of a token's ranks: the largest; then what its h was divided by (float16)
 };
-constexpr int kShared = 1024;
+constexpr int kShared = 2048;
 static_assert(sizeof(Shared) <= kShared, "");
 
 // The start and the end of both kernels: barriers and tensor memory
@@ -146,16 +164,17 @@ __global__ void __launch_bounds__(kThreads, 2) long_first_kernel(const Params p)
   const uint32_t tmem = sh->tmem, abort_flag = smem_u32(&sh->abort);
   const uint64_t limit = p.control->limit_ns;
   const bool stall = p.control->stall != 0;
-  const int64_t items = int64_t(*p.num_tiles) * p.splits;
+  const int csize = p.csize, crank = csize > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int ntiles = *p.num_tiles;
   const int blocks = static_cast<int>((p.k_units + 7) / 8);
   const uint32_t idesc = idesc_of<DT>(p.r16);
   uint32_t t = 0, done = 0;  // blocks and items so far
   bool ok = true;
-  for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
-    const Tile d = p.tiles[item / p.splits];
-    const int split = static_cast<int>(item % p.splits);
-    if (d.adapter < 0) continue;  // (the same for the CTA)
-    const int b0 = split * p.per_split, nb = min(b0 + p.per_split, blocks) - b0;
+  // (a CTA that gave up a wait goes on without MMAs: the others of its cluster meet it at the barriers and read its shared memory)
+  for (int tile = blockIdx.x / csize; tile < ntiles; tile += gridDim.x / csize) {
+    const Tile d = p.tiles[tile];
+    if (d.adapter < 0) continue;  // (the same for the cluster)
+    const int b0 = crank * p.per_split, nb = ok ? max(min(b0 + p.per_split, blocks) - b0, 0) : 0;
     const uint4 *a = p.a + int64_t(d.adapter) * p.r_units * 8 * p.k_units;
     const int c = tid & 7;
     uint32_t xr[4];  // (rows past the tile's last are the last one again: their sums are not stored)
@@ -202,46 +221,74 @@ __global__ void __launch_bounds__(kThreads, 2) long_first_kernel(const Params p)
         if (i == nb - 1) umma_commit(smem_u32(&sh->done_bar));
       }
     }
-    if (!ok) break;
-    t += nb;
-    ok = wait_phase(smem_u32(&sh->done_bar), done & 1, abort_flag, limit, &p.control->error);
-    ++done;
-    ok = __syncthreads_and(ok);
-    if (!ok) break;
+    if (ok && nb > 0) {
+      t += nb;
+      ok = wait_phase(smem_u32(&sh->done_bar), done & 1, abort_flag, limit, &p.control->error);
+      ++done;
+      ok = __syncthreads_and(ok);
+    }
     tc_fence_after();
-    const int row = (warp & 3) * 32 + lane;
-    float *to = p.h + (int64_t(split) * p.tokens + d.first + row) * p.r16;
-    for (int c0 = (warp >> 2) * 16; c0 < p.r16; c0 += 32) {
-      float v[16];
-      tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, v);
-      tmem_wait_ld();
-      if (row < d.count)
+    // the sums of this CTA's part of K, in the ring's place, then an equal share of the tokens added over the cluster, in order
+    const int stride = p.r16 + 4;
+    float *sums = reinterpret_cast<float *>(smem + kShared);
+    cp_async_wait<0>();
+    __syncthreads();
+    {
+      const int row = (warp & 3) * 32 + lane;
+      for (int c0 = (warp >> 2) * 16; c0 < p.r16; c0 += 32) {
+        float v[16] = {};
+        if (ok && nb > 0) {
+          tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0, v);
+          tmem_wait_ld();
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) reinterpret_cast<float4 *>(to + c0)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4 *>(sums + row * stride + c0 + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      }
     }
     tc_fence_before();
-    __syncthreads();  // the accumulators have been read
+    if (csize > 1) cluster_sync_all();
+    else __syncthreads();
+    const int quads = p.r16 / 4, rows = kLongTile / csize;
+    for (int e = tid; e < rows * quads; e += kThreads) {
+      const int row = crank * rows + e / quads, q = e % quads;
+      const uint32_t mine = smem_u32(sums + row * stride + 4 * q);
+      float4 o[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (c < csize) o[c] = csize > 1 ? ld_dsmem_v4(map_to_rank(mine, c)) : *reinterpret_cast<const float4 *>(sums + row * stride + 4 * q);
+      float4 v = o[0];
+#pragma unroll
+      for (int c = 1; c < 8; ++c)
+        if (c < csize) v.x += o[c].x, v.y += o[c].y, v.z += o[c].z, v.w += o[c].w;
+      if (row < d.count) *reinterpret_cast<float4 *>(p.h + int64_t(d.first + row) * p.r16 + 4 * q) = v;
+    }
+    if (csize > 1) cluster_sync_all();
+    else __syncthreads();
   }
   finish(sh, 128, ok, p.control);
 }
 
-// Second product. NC: columns of a step
-template <class DT, int RA, int NC>
-__global__ void __launch_bounds__(kThreads, RA == 1 ? 2 : 1) long_second_kernel(const Params p) {
-  constexpr int kH = 2 * RA * kLongTile * 128, kB = RA * NC * 128, kBase = kLongTile * NC * 2, kRow = NC / 8;  // kRow: units of a row of base
+// Second product, 64 columns a step: a ring of copies (base, whose place the results take, and B), two accumulators, so that copies and
+// MMAs of the next steps run while this one's results are added and stored. h is in tensor memory, which leaves shared memory to the
+// ring of two CTAs on an SM (h in shared memory, rank 128: one CTA with two stages of 128 columns 70 us, three of 64 93).
+template <class DT, int RA>
+__global__ void __launch_bounds__(kThreads, 2) long_second_kernel(const Params p) {
+  constexpr int NC = kCols, S = kSecondStages<RA>, kHalf = 32 * RA;  // kHalf: columns of tensor memory of a part of h
+  constexpr int kB = RA * NC * 128, kBase = kLongTile * NC * 2, kRow = NC / 8;  // kRow: units of a row of base
   extern __shared__ uint8_t raw[];
   uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   Shared *sh = reinterpret_cast<Shared *>(smem);
-  uint8_t *hs = smem + kShared, *bs = hs + kH, *os = bs + 2 * kB;
+  uint8_t *bs = smem + kShared, *os = bs + S * kB;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();
-  begin(sh, NC);
-  const uint32_t tmem = sh->tmem, abort_flag = smem_u32(&sh->abort);
+  begin(sh, 256);
+  const uint32_t h_hi = sh->tmem, h_lo = h_hi + kHalf, tmem = h_lo + kHalf, abort_flag = smem_u32(&sh->abort);
   const uint64_t limit = p.control->limit_ns;
   const bool stall = p.control->stall != 0;
   const int64_t items = int64_t(*p.num_tiles) * p.slices;
   const int chunks = static_cast<int>((p.n_units + kRow - 1) / kRow), per = (chunks + p.slices - 1) / p.slices;
-  uint32_t done = 0;
+  uint32_t g = 0;  // steps with products so far: their accumulators and barriers take turns
   bool ok = true;
   for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x) {
     const Tile d = p.tiles[item / p.slices];
@@ -259,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, RA == 1 ? 2 : 1) long_second_kernel(
     }
     auto fetch = [&](int i) {
       const uint32_t n0 = static_cast<uint32_t>(j0 + i) * kRow;
-      const uint32_t to = smem_u32(os) + (i & 1) * kBase, bt = smem_u32(bs) + (i & 1) * kB;
+      const uint32_t to = smem_u32(os) + i % S * kBase, bt = smem_u32(bs) + i % S * kB;
 #pragma unroll
       for (int j = 0; j < kRows; ++j)
         if (my[j] >= 0 && n0 + c < p.n_units) cp_async_16(to + place(j * kStep + tid / kRow, c, kLongTile), p.base + (my[j] * p.base_stride + n0 + c), true);
@@ -273,83 +320,89 @@ __global__ void __launch_bounds__(kThreads, RA == 1 ? 2 : 1) long_second_kernel(
         }
       }
     };
-    fetch(0);
-    cp_async_commit();
-    if (d.adapter >= 0) {
-      // h: the parts of K added, times s; two threads a token, every other unit of eight ranks each
-      const int row = tid >> 1;
-      const float s = p.scales ? p.scales[d.adapter] : 1.f;
-      float v[RA * 4][8];
-      float top = 0.f;
-#pragma unroll
-      for (int q = 0; q < RA * 4; ++q) {
-        const int r0 = (2 * q + (tid & 1)) * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[q][e] = 0.f;
-        if (r0 < p.r16 && row < d.count) {
-          const float *from = p.h + int64_t(d.first + row) * p.r16 + r0;
-          for (int sp = 0; sp < p.splits; ++sp) {
-            const float4 lo = *reinterpret_cast<const float4 *>(from), hi = *reinterpret_cast<const float4 *>(from + 4);
-            v[q][0] += lo.x, v[q][1] += lo.y, v[q][2] += lo.z, v[q][3] += lo.w, v[q][4] += hi.x, v[q][5] += hi.y, v[q][6] += hi.z, v[q][7] += hi.w;
-            from += p.tokens * p.r16;
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[q][e] *= s;
-            top = fmaxf(top, fabsf(v[q][e]));  // (a NaN does not count)
-          }
-        }
-      }
-      float f = 1.f;
-      if constexpr (!DT::kBF16) {
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        const float unit = unit_of_largest(top);
-        f = 1.f / unit;  // (exact: a power of two)
-        if ((tid & 1) == 0) sh->back[row] = unit;
-      }
-#pragma unroll
-      for (int q = 0; q < RA * 4; ++q) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split2<DT>(v[q][2 * e] * f, v[q][2 * e + 1] * f, hi[e], lo[e]);
-        const uint32_t at = place(row, 2 * q + (tid & 1), kLongTile);
-        *reinterpret_cast<uint4 *>(hs + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4 *>(hs + RA * kLongTile * 128 + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-    }
-    for (int i = 0; i < n; ++i) {
-      if (i + 1 < n) fetch(i + 1);
-      cp_async_commit();
-      cp_async_wait<1>();
+    // step i's MMAs, by one thread, once its copies have landed for all
+    auto multiply = [&](int i) {
+      cp_async_wait<S - 2>();
       fence_proxy_async_smem();
       __syncthreads();
-      uint8_t *ot = os + (i & 1) * kBase;
-      if (d.adapter >= 0) {
-        if (tid == 0 && !stall) {
-          tc_fence_after();
-          const uint64_t hd = smem_desc(smem_u32(hs)), bd = smem_desc(smem_u32(bs) + (i & 1) * kB);
-          const uint32_t idesc = idesc_of<DT>(NC);
-          for (int kk = 0; kk < p.r16 / 16; ++kk) {
-            const uint64_t ho = ((kk >> 2) * kLongTile * 128 + (kk & 3) * 32) >> 4, bo = ((kk >> 2) * NC * 128 + (kk & 3) * 32) >> 4;
-            umma(tmem, hd + (RA * kLongTile * 128 >> 4) + ho, bd + bo, idesc, kk > 0);
-            umma(tmem, hd + ho, bd + bo, idesc, 1);
+      if (d.adapter < 0 || tid != 0 || stall) return;
+      tc_fence_after();
+      const uint64_t bd = smem_desc(smem_u32(bs) + i % S * kB);
+      const uint32_t idesc = idesc_of<DT>(NC), to = tmem + ((g + i) & 1) * NC;
+      for (int kk = 0; kk < p.r16 / 16; ++kk) {
+        const uint64_t bo = ((kk >> 2) * NC * 128 + (kk & 3) * 32) >> 4;
+        umma_ts(to, h_lo + 8 * kk, bd + bo, idesc, kk > 0);
+        umma_ts(to, h_hi + 8 * kk, bd + bo, idesc, 1);
+      }
+      umma_commit(smem_u32(&sh->stage_bar[(g + i) & 1]));
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+      if (i < n) fetch(i);
+      cp_async_commit();
+    }
+    if (d.adapter >= 0) {
+      // h, times s: half of a token's ranks a thread
+      const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const float s = p.scales ? p.scales[d.adapter] : 1.f;
+      float v[kHalf];
+#pragma unroll
+      for (int e = 0; e < kHalf; ++e) v[e] = 0.f;
+      if (row < d.count) {
+        const float *from = p.h + int64_t(d.first + row) * p.r16 + half * kHalf;
+#pragma unroll
+        for (int e = 0; e < kHalf; e += 4)
+          if (half * kHalf + e < p.r16) {
+            const float4 q = *reinterpret_cast<const float4 *>(from + e);
+            v[e] = q.x, v[e + 1] = q.y, v[e + 2] = q.z, v[e + 3] = q.w;
           }
-          umma_commit(smem_u32(&sh->done_bar));
-        }
-        ok = wait_phase(smem_u32(&sh->done_bar), done & 1, abort_flag, limit, &p.control->error);
-        ++done;
+      }
+      float f = s;
+      if constexpr (!DT::kBF16) {
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < kHalf; ++e) top = fmaxf(top, fabsf(v[e] * s));  // (a NaN does not count)
+        sh->back[half][row] = top;
+        __syncthreads();
+        const float unit = unit_of_largest(fmaxf(sh->back[0][row], sh->back[1][row]));
+        __syncthreads();
+        if (half == 0) sh->back[0][row] = unit;
+#pragma unroll
+        for (int e = 0; e < kHalf; ++e) v[e] *= s;
+        f = 1.f / unit;  // (exact: a power of two)
+      }
+#pragma unroll
+      for (int e0 = 0; e0 < kHalf; e0 += 32) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) split2<DT>(v[e0 + 2 * e] * f, v[e0 + 2 * e + 1] * f, hi[e], lo[e]);
+        tmem_st16(h_hi + lanes + (half * kHalf + e0) / 2, hi);
+        tmem_st16(h_lo + lanes + (half * kHalf + e0) / 2, lo);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+    }
+    multiply(0);
+    for (int i = 0; i < n; ++i) {
+      if (i + S - 1 < n) fetch(i + S - 1);  // (where step i - 1 was: its results have been stored)
+      cp_async_commit();
+      if (i + 1 < n) multiply(i + 1);
+      uint8_t *ot = os + i % S * kBase;
+      if (d.adapter >= 0) {
+        ok = wait_phase(smem_u32(&sh->stage_bar[(g + i) & 1]), (g + i) >> 1 & 1, abort_flag, limit, &p.control->error);
         ok = __syncthreads_and(ok);
         if (!ok) break;
         tc_fence_after();
         // a thread's row, half of its columns
         const int row = (warp & 3) * 32 + lane;
         float f = 1.f;
-        if constexpr (!DT::kBF16) f = sh->back[row];
+        if constexpr (!DT::kBF16) f = sh->back[0][row];
 #pragma unroll
         for (int c0 = 0; c0 < NC / 2; c0 += 16) {
           const int col = (warp >> 2) * (NC / 2) + c0;
           float v[16];
-          tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + col, v);
+          tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + ((g + i) & 1) * NC + col, v);
           tmem_wait_ld();
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -370,19 +423,13 @@ __global__ void __launch_bounds__(kThreads, RA == 1 ? 2 : 1) long_second_kernel(
           __stcs(p.out + (my[j] * p.out_stride + n0 + c), *reinterpret_cast<const uint4 *>(ot + place(j * kStep + tid / kRow, c, kLongTile)));
       __syncthreads();  // the stage may be filled again
     }
+    if (d.adapter >= 0) g += n;
   }
-  finish(sh, NC, ok, p.control);
+  finish(sh, 256, ok, p.control);
 }
 
-// CTAs that are resident at two on each of a GB300's 152 SMs; K is split by it whatever the device, so that the workspace depends on the
-// sizes alone
-constexpr int kRoom = 304;
-int64_t tiles_about(int64_t tokens, int64_t adapters) {
-  return (tokens + kLongTile - 1) / kLongTile + std::min<int64_t>(adapters, tokens / 2) / 2;
-}
-int most_splits(int64_t tokens, int64_t adapters) {
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, kRoom / tiles_about(tokens, adapters))));
-}
+// Every adapter may leave a tile that is not full: more than it turns out to be rather than less, which costs a second wave
+int64_t tiles_about(int64_t tokens, int64_t adapters) { return tokens / kLongTile + std::min<int64_t>(adapters, tokens / 4) + 1; }
 int rounded(int rank) { return (rank + 15) / 16 * 16; }
 
 template <class K>
@@ -393,38 +440,43 @@ cudaError_t prepare(K kernel, int smem, int device, std::atomic<bool> (&asked)[6
   return e;
 }
 
-template <class DT, int RA, int NC>
+template <class DT, int RA>
 cudaError_t go(Params p, int64_t about, const DeviceInfo &dev, cudaStream_t stream) {
   constexpr int kFirst = kShared + 1024 + (RA == 1 ? 4 : 3) * (kLongTile * 128 + RA * 64 * 128);
-  constexpr int kSecond = kShared + 1024 + 2 * RA * kLongTile * 128 + 2 * (RA * NC * 128 + kLongTile * NC * 2);
+  constexpr int kSecond = kShared + 1024 + kSecondStages<RA> * (RA * kCols * 128 + kLongTile * kCols * 2);
   static std::atomic<bool> asked_first[64], asked_second[64];
   cudaError_t e = prepare(long_first_kernel<DT, RA>, kFirst, dev.device, asked_first);
-  if (e == cudaSuccess) e = prepare(long_second_kernel<DT, RA, NC>, kSecond, dev.device, asked_second);
+  if (e == cudaSuccess) e = prepare(long_second_kernel<DT, RA>, kSecond, dev.device, asked_second);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.csize);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * dev.num_sms), 1, 1);
+  cfg.numAttrs = p.csize > 1 ? 2 : 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(about * p.csize, 2 * dev.num_sms / p.csize * p.csize)), 1, 1);
   cfg.dynamicSmemBytes = kFirst;
   e = cudaLaunchKernelEx(&cfg, long_first_kernel<DT, RA>, p);
   if (e != cudaSuccess) return e;
   note_launch();
   // slices of N: the number whose last wave costs least, a slice's h counting as much as two of its steps
-  const int resident = (RA == 1 ? 2 : 1) * dev.num_sms;
-  const int64_t chunks = (p.n_units + NC / 8 - 1) / (NC / 8);
+  const int resident = 2 * dev.num_sms;
+  const int64_t chunks = (p.n_units + kCols / 8 - 1) / (kCols / 8);
   double best = 0;
   for (int64_t s = 1; s <= std::min<int64_t>(chunks, 32); ++s) {
     const double waves = static_cast<double>((about * s + resident - 1) / resident), cost = waves * (2.0 + static_cast<double>((chunks + s - 1) / s));
     if (s == 1 || cost < best) best = cost, p.slices = static_cast<int>(s);
   }
   cfg.gridDim = dim3(static_cast<unsigned>(resident), 1, 1);
+  cfg.numAttrs = 1;
   cfg.dynamicSmemBytes = kSecond;
-  e = cudaLaunchKernelEx(&cfg, long_second_kernel<DT, RA, NC>, p);
+  e = cudaLaunchKernelEx(&cfg, long_second_kernel<DT, RA>, p);
   if (e == cudaSuccess) note_launch();
   return e;
 }
@@ -447,9 +499,7 @@ cudaError_t control_of(int device, Control **out) {
 
 }  // namespace
 
-size_t long_workspace_bytes(int64_t tokens, int rank, int64_t adapters) {
-  return static_cast<size_t>(most_splits(tokens, adapters)) * static_cast<size_t>(tokens) * rounded(rank) * 4;
-}
+size_t long_workspace_bytes(int64_t tokens, int rank) { return static_cast<size_t>(tokens) * rounded(rank) * 4; }
 
 cudaError_t launch_long(const LoraArgs &a, const DeviceInfo &dev, const int32_t *order, const Tile *tiles, const int32_t *num_tiles, float *h) {
   Params p{};
@@ -468,9 +518,12 @@ cudaError_t launch_long(const LoraArgs &a, const DeviceInfo &dev, const int32_t 
   p.r_units = static_cast<uint32_t>(a.rank / 8);
   p.r16 = rounded(a.rank);
   const int blocks = static_cast<int>((a.K + 63) / 64);
-  const int splits = std::min(most_splits(a.tokens, a.adapters), blocks);
-  p.per_split = (blocks + splits - 1) / splits;
-  p.splits = (blocks + p.per_split - 1) / p.per_split;
+  // CTAs of a tile: while all are resident (a cluster stays within a group of SMs: of eight there are 36 at two CTAs on each of 152
+  // SMs, not 38) and each keeps four blocks
+  const int64_t about = tiles_about(a.tokens, a.adapters);
+  p.csize = 1;
+  while (p.csize < 8 && about * p.csize * 2 <= (p.csize == 4 ? 36 * dev.num_sms / 19 : 2 * dev.num_sms) && blocks / (p.csize * 2) >= 4) p.csize *= 2;
+  p.per_split = (blocks + p.csize - 1) / p.csize;
   p.copy = a.base != a.out;
   p.order = order;
   p.tiles = tiles;
@@ -478,10 +531,9 @@ cudaError_t launch_long(const LoraArgs &a, const DeviceInfo &dev, const int32_t 
   p.h = h;
   const cudaError_t e = control_of(dev.device, &p.control);
   if (e != cudaSuccess) return e;
-  const int64_t about = tiles_about(a.tokens, a.adapters);
   if (a.dtype == W4A16_BF16)
-    return a.rank <= 64 ? go<BF16, 1, 64>(p, about, dev, a.stream) : go<BF16, 2, 128>(p, about, dev, a.stream);
-  return a.rank <= 64 ? go<F16, 1, 64>(p, about, dev, a.stream) : go<F16, 2, 128>(p, about, dev, a.stream);
+    return a.rank <= 64 ? go<BF16, 1>(p, about, dev, a.stream) : go<BF16, 2>(p, about, dev, a.stream);
+  return a.rank <= 64 ? go<F16, 1>(p, about, dev, a.stream) : go<F16, 2>(p, about, dev, a.stream);
 }
 
 }  // namespace lora

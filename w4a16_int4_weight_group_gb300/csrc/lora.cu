@@ -21,8 +21,7 @@
 // kernel before this one (counting sort). The composition of a tile does not change a token's result: the rows of an MMA do not mix
 // and K is split in the same way.
 //
-// Bound by memory for long prompts (base read and out written are most of the bytes), by mma.sync for ranks past 32 (the second product
-// takes two for each), by the chain of copies, barriers and sums for few tokens. Measured, replayed from a graph: 8191 tokens 5120 -> 7168 of rank
+// Bound by memory for long prompts (base read and out written are most of the bytes), by the chain of copies, barriers and sums for few tokens. Measured, replayed from a graph: 8191 tokens 5120 -> 7168 of rank
 // 32 75 us for 328 MB, 4.4 TB/s, 0.65 of the device's copy rate (9 us of them the sort and the launch; the same tiles copied without
 // an adapter 0.85 of it while they stream); DRAM 53 %, tensor pipe 31 %, schedulers 42 % of the cycles. 520 tokens 2560 -> 3840 of rank 64 21
 // us; 48 tokens 5120 -> 7168 of rank 16 9.0; one token 2112 -> 1152 4.2.
@@ -568,14 +567,18 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *
 }
 
 // Tokens of a sorted tile: 32 while there are few of them, else 64 (A and B are read half as often, for fewer and larger shares
-// of work). 2560 -> 3840, 16 adapters: 1500 tokens 18.1 us with 32 and 19.2 with 64 (rank 16), 25.7 and 27.5 (rank 64), 2000 tokens
-// 18.7 and 19.5, 26.4 and 38.4. 5120 -> 7168, 8191 tokens of 12 adapters (with the sort): rank 16 83 and 77, rank 32 84 and 80,
-// rank 64 109 and 113, rank 128 193 and 168.
+// of work). 2560 -> 3840, 16 adapters, rank 16: 1500 tokens 18.1 us with 32 and 19.2 with 64, 2000 tokens 18.7 and 19.5. 5120 -> 7168, 8191 tokens
+// of 12 adapters: rank 16 83 and 77, rank 32 84 and 80.
 constexpr int64_t kMidTokens = 2048;
+// Many tokens of ranks past 32 go to the form on tcgen05. Warp-level against tcgen05 (16 adapters 2560 -> 3840; 6 adapters 5120 -> 7168), replayed:
+// rank 40, 1030 tokens 25.4 against 22.6 us; 28.9 against 28.0; 2000 tokens 27.2 against 25.7; 37.0 against 34.6
+// rank 64, 1030 tokens 24.7 against 23.5; 27.9 against 29.7; 2000 tokens 26.5 against 28.0; 35.7 against 36.8; 8191 tokens 113 against 87
+// rank 128, 1030 tokens 36.8 against 31.6; 36.0 against 37.3; 2000 tokens 37.5 against 33.5; 56.6 against 45.9; 8191 tokens 167 against 104
+// and for ranks to 32: 4000 tokens of rank 32 44.2 against 45.5, 16000 tokens 77.7 against 80.9. Up to 1024 tokens the warp-level form needs one launch
+// instead of three (600 tokens of rank 128: 28.4 against 28.5 and 42.8 against 28.7).
 constexpr int kMidRank = 32;
-// More tokens of larger ranks go to the form on tcgen05.
-bool on_tcgen05(int64_t tokens, int rank) { return tokens > kMidTokens && rank > kMidRank; }
-int sorted_tile(int64_t tokens, int rank) { return tokens <= kMidTokens ? 32 : on_tcgen05(tokens, rank) ? kLongTile : 64; }
+bool on_tcgen05(int64_t tokens, int rank) { return tokens > kCountTokens && rank > kMidRank; }
+int sorted_tile(int64_t tokens, int rank) { return on_tcgen05(tokens, rank) ? kLongTile : tokens <= kMidTokens ? 32 : 64; }
 int64_t most_tiles(int64_t tokens, int rank, int64_t adapters) {
   return tokens / sorted_tile(tokens, rank) + std::min<int64_t>(tokens, adapters + 1);
 }

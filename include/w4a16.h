@@ -413,7 +413,7 @@ w4a16_status w4a16_token_logprobs(const void *logits, int64_t row_stride, int64_
  * Sums are fp32; x a_i^T keeps 16 (BF16) or, below the token's largest, 22 bits (F16) for the second product; out is rounded
  * once. A token's result does not depend on the other tokens of the call, apart from how its sums are split.
  *   workspace  device memory, 256-byte aligned, w4a16_lora_workspace_size bytes (0, and NULL will do, for up to 256 tokens, and for up
- *              to 1024 of up to 512 adapters); its first 4 KiB are not touched, so that a stream's buffer for the layer and the attention serves here too.
+ *              to 1024 of up to 512 adapters where the rank is at most 64); its first 4 KiB are not touched, so that a stream's buffer for the layer and the attention serves here too.
  * Errors: INVALID_ARG (sizes, nulls, overlap, workspace), UNSUPPORTED (dtype, k, n, rank, adapters), MISALIGNED, CUDA. A kernel that
  * gives up a bounded wait is reported by w4a16_get_device_error.
  */

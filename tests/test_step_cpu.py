@@ -56,6 +56,8 @@ def test_lora_refusals(w):
     need = w.w4a16_lora_workspace_size(1100, 16, 4)
     assert need > 4096 + 1100 * 4 and w.w4a16_lora_workspace_size(1100, 16, 9000) == 0
     assert [w.w4a16_lora_workspace_size(T, 16, L) for T, L in ((256, 8191), (1024, 512))] == [0, 0]
+    assert [w.w4a16_lora_workspace_size(T, 72, L) > 0 for T, L in ((256, 1), (300, 1), (300, 30), (640, 30), (641, 30))] == [False, True, False, False, True]
+    refused(w, call(T=300, r=72, L=1), 1, "workspace of 0 bytes")
     refused(w, call(T=1100, ws=0x7000000, wb=need - 1), 1, "needed")
     refused(w, call(T=1100, ws=0x7000080, wb=need), 3, "256-byte")
     refused(w, call(T=1100, ws=0x5000000, wb=need), 1, "overlaps")

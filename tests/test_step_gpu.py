@@ -55,7 +55,8 @@ def cuda(c):
                                        (48, 640, 1160, 64, 48), (64, 264, 72, 128, 7), (256, 72, 96, 48, 2), (257, 136, 104, 16, 3),
                                        (300, 264, 200, 8, 300), (333, 520, 328, 40, 2), (400, 200, 264, 72, 9), (600, 328, 136, 128, 4), (1000, 64, 32, 32, 1),
                                        (1024, 72, 40, 8, 512), (270, 72, 40, 24, 513), (1025, 136, 72, 32, 4), (2049, 64, 40, 16, 30), (2100, 72, 96, 64, 2),
-                                       (2500, 64, 72, 128, 3), (2200, 2600, 200, 40, 3), (3000, 1032, 520, 72, 40), (2049, 8, 8, 48, 700), (2500, 712, 1160, 104, 1), (1100, 5120, 264, 64, 3)])
+                                       (2500, 64, 72, 128, 3), (2200, 2600, 200, 40, 3), (3000, 1032, 520, 72, 40), (2049, 8, 8, 48, 700), (2500, 712, 1160, 104, 1), (1100, 5120, 264, 64, 3),
+                                       (300, 4000, 136, 72, 2), (641, 200, 3904, 128, 40), (640, 4096, 40, 96, 8), (700, 64, 72, 80, 600)])
 def test_lora(w, T, K, N, r, n, dtype):
     c = make_lora(T, K, N, r, n, dtype, seed=T + r)
     d = cuda(c)

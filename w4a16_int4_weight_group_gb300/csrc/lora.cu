@@ -41,7 +41,7 @@ constexpr int kMaxCluster = 8;
 // 25.1 (rank 64); 64 tokens: 9.2 against 12.9, 19.8 against 23.5.
 constexpr int kFewTokens = 256;
 constexpr int kFewTile = 8;      // tokens of a tile then
-// Up to this many tokens of this many adapters a CTA counts the tokens of each adapter in shared memory. On the GPU as long as sorted by
+// Up to this many tokens of this many adapters (and ranks that stay with this form) a CTA counts the tokens of each adapter in shared memory. On the GPU as long as sorted by
 // a kernel before (2560 -> 3840, rank 64: 400 tokens 20.0 against 19.3 us, 1000 tokens 19.4 against 19.2), with a launch less to
 // issue (3.8 against 14 us, a workspace among it).
 constexpr int kCountTokens = 1024, kCountAdapters = 512;
@@ -574,14 +574,23 @@ constexpr int64_t kMidTokens = 2048;
 // rank 40, 1030 tokens 25.4 against 22.6 us; 28.9 against 28.0; 2000 tokens 27.2 against 25.7; 37.0 against 34.6
 // rank 64, 1030 tokens 24.7 against 23.5; 27.9 against 29.7; 2000 tokens 26.5 against 28.0; 35.7 against 36.8; 8191 tokens 113 against 87
 // rank 128, 1030 tokens 36.8 against 31.6; 36.0 against 37.3; 2000 tokens 37.5 against 33.5; 56.6 against 45.9; 8191 tokens 167 against 104
-// and for ranks to 32: 4000 tokens of rank 32 44.2 against 45.5, 16000 tokens 77.7 against 80.9. Up to 1024 tokens the warp-level form needs one launch
-// instead of three (600 tokens of rank 128: 28.4 against 28.5 and 42.8 against 28.7).
-constexpr int kMidRank = 32;
-bool on_tcgen05(int64_t tokens, int rank) { return tokens > kCountTokens && rank > kMidRank; }
-int sorted_tile(int64_t tokens, int rank) { return on_tcgen05(tokens, rank) ? kLongTile : tokens <= kMidTokens ? 32 : 64; }
-int64_t most_tiles(int64_t tokens, int rank, int64_t adapters) {
-  return tokens / sorted_tile(tokens, rank) + std::min<int64_t>(tokens, adapters + 1);
+// and for ranks to 32: 4000 tokens of rank 32 44.2 against 45.5, 16000 tokens 77.7 against 80.9.
+// Up to 1024 tokens for ranks past 64 alone, whose warp-level form has one CTA on an SM: from 641 tokens, and from 257 where the tiles of
+// 128 are likely full, unless the layer is so small that three launches show. Rank 72, 3 adapters in runs: 300 tokens 5120 -> 7168 29.5
+// against 23.2, 500 tokens 888 -> 7432 35.8 against 25.6; 30 adapters at random: 500 tokens 41.1 against 43.6, 800 tokens 68.9 against 46.0;
+// rank 128 512 -> 512 13.3 to 14.1 against 18.5 to 20.2.
+constexpr int kMidRank = 32, kWideRank = 64;
+constexpr int64_t kWideTokens = 640, kWideFill = 96, kWideLayer = 4096;
+bool may_be_long(int64_t tokens, int rank, int64_t adapters) {
+  if (tokens > kCountTokens) return rank > kMidRank;
+  return rank > kWideRank && (tokens > kWideTokens || (tokens > kFewTokens && tokens >= kWideFill * adapters));
 }
+bool is_long(const LoraArgs &a) {
+  return may_be_long(a.tokens, a.rank, a.adapters) && (a.tokens > kCountTokens || a.K + a.N >= kWideLayer);
+}
+bool can_count(int64_t tokens, int64_t adapters) { return tokens <= kCountTokens && adapters <= kCountAdapters; }
+int sorted_tile(int64_t tokens) { return tokens <= kMidTokens ? 32 : 64; }
+int64_t most_tiles(int64_t tokens, int64_t adapters) { return tokens / sorted_tile(tokens) + std::min<int64_t>(tokens, adapters + 1); }
 
 template <class DT, class S, int TILING>
 cudaError_t go(Params p, int64_t tiles, int64_t most, const DeviceInfo &dev, cudaStream_t stream) {
@@ -657,17 +666,15 @@ cudaError_t run(const Params &p, bool few, int64_t tiles, int64_t most, const De
 
 }  // namespace
 
-// Whether the CTAs find their tiles by themselves
-static bool alone(int64_t tokens, int64_t adapters) { return tokens <= kFewTokens || (tokens <= kCountTokens && adapters <= kCountAdapters); }
-
 // The workspace past the first 4 KiB (the counters of other calls): the number of tiles, the sorted tokens, the tiles, h
 static size_t tiles_at(int64_t tokens) { return 256 + static_cast<size_t>((tokens * 4 + 255) / 256 * 256); }
-static size_t h_at(int64_t tokens, int rank, int64_t adapters) {
-  return tiles_at(tokens) + (static_cast<size_t>(most_tiles(tokens, rank, adapters)) * sizeof(Tile) + 255) / 256 * 256;
+static size_t h_at(int64_t tokens, int64_t adapters) {
+  return tiles_at(tokens) + (static_cast<size_t>(most_tiles(tokens, adapters)) * sizeof(Tile) + 255) / 256 * 256;
 }
 size_t lora_workspace_bytes(int64_t tokens, int rank, int64_t adapters) {
-  if (alone(tokens, adapters)) return 0;
-  return 4096 + h_at(tokens, rank, adapters) + (on_tcgen05(tokens, rank) ? long_workspace_bytes(tokens, rank) : 0);
+  const bool maybe = may_be_long(tokens, rank, adapters);
+  if (tokens <= kFewTokens || (can_count(tokens, adapters) && !maybe)) return 0;
+  return 4096 + h_at(tokens, adapters) + (maybe ? long_workspace_bytes(tokens, rank) : 0);
 }
 int lora_most_adapters() { return kMaxAdapters; }
 
@@ -689,21 +696,21 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
   p.rank = a.rank;
   p.adapters = static_cast<int>(a.adapters);
   p.copy = a.base != a.out;
-  const bool few = a.tokens <= kFewTokens;
+  const bool few = a.tokens <= kFewTokens, long_form = !few && is_long(a);
   // tiles, as far as can be told here, and at most
   int64_t tiles = std::min<int64_t>(a.tokens, a.tokens / kFewTile + a.adapters), most = a.tokens;
   if (!few) {
-    tiles = (a.tokens + sorted_tile(a.tokens, a.rank) - 1) / sorted_tile(a.tokens, a.rank) + std::min<int64_t>(a.adapters, a.tokens / 2) / 2;
-    most = most_tiles(a.tokens, a.rank, a.adapters);
+    tiles = (a.tokens + sorted_tile(a.tokens) - 1) / sorted_tile(a.tokens) + std::min<int64_t>(a.adapters, a.tokens / 2) / 2;
+    most = most_tiles(a.tokens, a.adapters);
   }
-  if (!alone(a.tokens, a.adapters)) {
+  if (!few && (long_form || !can_count(a.tokens, a.adapters))) {
     uint8_t *ws = static_cast<uint8_t *>(a.workspace) + 4096;
     int32_t *num = reinterpret_cast<int32_t *>(ws);
     p.order = reinterpret_cast<int32_t *>(ws + 256);
     Tile *list = reinterpret_cast<Tile *>(ws + tiles_at(a.tokens));
     p.num_tiles = num;
     p.tiles = list;
-    const int per = sorted_tile(a.tokens, a.rank);
+    const int per = long_form ? kLongTile : sorted_tile(a.tokens);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
@@ -717,8 +724,7 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
     const cudaError_t e = cudaLaunchKernelEx(&cfg, lora_sort_kernel, a.ids, static_cast<int>(a.tokens), p.adapters, per, p.copy, p.order, list, num);
     if (e != cudaSuccess) return e;
     note_launch();
-    if (on_tcgen05(a.tokens, a.rank))
-      return launch_long(a, dev, p.order, list, num, reinterpret_cast<float *>(ws + h_at(a.tokens, a.rank, a.adapters)));
+    if (long_form) return launch_long(a, dev, p.order, list, num, reinterpret_cast<float *>(ws + h_at(a.tokens, a.adapters)));
   }
   return a.dtype == W4A16_BF16 ? run<BF16>(p, few, tiles, most, dev, a.stream) : run<F16>(p, few, tiles, most, dev, a.stream);
 }

@@ -142,8 +142,8 @@ def w4a16_lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Ten
     are multiples of 8, rank one up to 128.
 
     workspace: contiguous uint8 of the caller's own, for calls of one stream (or one graph) at a time; unless given, the binding
-    keeps one for each stream, and one for each capture by torch.cuda.graph. Calls of up to 256 tokens need none, nor those of up to 1024 tokens
-    and 512 adapters.
+    keeps one for each stream, and one for each capture by torch.cuda.graph. Calls of up to 256 tokens need none, nor those of up to 1024 tokens,
+    512 adapters and rank 64.
     """
     if workspace is None:
         fast = _bind_fast() if _fast is None else _fast

@@ -274,6 +274,18 @@ def test_verify_borders(w):
     assert out[0].tolist() == [0] and int(out[2][0, 0]) == 6
 
 
+def test_a_repeated_guess_does_not_stand_for_rounding(w):
+    """All tokens of a small vocabulary guessed and rejected: what is left of 1 may be less than nothing, the repeated guess has no weight."""
+    B, V = 3000, 3
+    g = torch.Generator().manual_seed(4)
+    tokens = torch.tensor([0, 0, 1, 2, 0]).repeat(B)
+    mask = torch.tensor([1, 3, 5, 9, 17]).repeat(B)
+    out = w.w4a16_verify_drafts(torch.randn(5 * B, V, generator=g).cuda(), tokens.cuda(), torch.ones(5 * B).cuda(),
+                                torch.empty(B, V).exponential_(generator=g).cuda(), q_start=(torch.arange(B + 1) * 5).to(torch.int32).cuda(),
+                                tree_mask=mask.cuda(), max_q=5)
+    assert not (out[1] == 4).any() and (out[2][:, 0] >= 0).all()
+
+
 def test_verify_draws_from_the_targets_distribution(w):
     """Frequencies of the first token that comes out, for a sampled chain and for two guesses: those of p."""
     B, V = 20000, 6

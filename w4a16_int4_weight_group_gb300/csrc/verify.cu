@@ -419,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_walk_kernel(const Params p
         if (parent[j] == parent[own]) gone += weight[j];
     gone += __shfl_xor_sync(quad, gone, 1);
     gone += __shfl_xor_sync(quad, gone, 2);
-    if (part == 0) passed[own] = parent[own] >= 0 && (p.draft ? us[own] * qd[own] < weight[own] : us[own] * (1.f - gone) < weight[own]);
+    // (rejected siblings may add up to more than 1 by rounding: a token of no weight does not stand for that)
+    if (part == 0) passed[own] = parent[own] >= 0 && us[own] * (p.draft ? qd[own] : fmaxf(1.f - gone, 0.f)) < weight[own];
   }
   __syncthreads();
   if (own < n) {

@@ -626,9 +626,14 @@ cudaError_t go(Params p, int64_t tiles, int64_t most, const DeviceInfo &dev, cud
     }
     if (e != cudaSuccess) return e;
   }
-  // CTAs of a tile: up to eight, while all tiles are resident together
+  // CTAs of a tile: up to eight, while all tiles are resident together and the split pays for the cluster's barriers and sums. With 1, 2, 4 and
+  // 8 CTAs, us: 48 tokens of rank 16, K + N = 512 3.9, 4.8, 5.0, 6.0; 2048 5.8, 5.3, 5.0, 6.0; 4096 8.4, 6.8, 5.8, 6.2; 7680 17.8, 11.5, 8.2, 8.4;
+  // 300 of rank 32: 512 5.8, 7.2, 7.5, 9.4; 2048 12.0, 9.4, 7.7, 9.6; 5632 21.4, 14.3, 10.9, 12.1; 12288 48.6, 28.8, 18.1, 16.8.
+  const int64_t both = p.K + p.N;
+  // (one tile alone, 1 token of rank 16: 512 3.3, 4.1, 4.1, 4.3; 4096 7.7, 6.2, 4.8, 4.4)
+  const int most_c = both < 1536 ? 0 : both < 7168 && tiles > 2 ? 2 : 3;
   int c = 0;
-  while (c < 3 && tiles <= room[c + 1]) ++c;
+  while (c < most_c && tiles <= room[c + 1]) ++c;
   p.csize = 1 << c;
   attr[0].val.clusterDim.x = 1u << c;
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(most, room[c]) << c), 1, 1);
@@ -645,7 +650,7 @@ cudaError_t run(const Params &p, bool few, int64_t tiles, int64_t most, const De
   if (few) {
     if (r <= 16) return go<DT, Shape<1, 1, 1, 3, 3>, kRanked>(p, tiles, most, dev, stream);
     if (r <= 32) return go<DT, Shape<2, 1, 1, 3, 3>, kRanked>(p, tiles, most, dev, stream);
-    if (r <= 64) return go<DT, Shape<4, 1, 1, 3, 2>, kRanked>(p, tiles, most, dev, stream);
+    if (r <= 64) return go<DT, Shape<4, 1, 1, 2, 2>, kRanked>(p, tiles, most, dev, stream);
     return go<DT, Shape<4, 1, 2, 2, 1>, kRanked>(p, tiles, most, dev, stream);
   }
   if (!p.tiles) {

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
       for (int m = 0; m < MR; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.f;
-      // rows in units of 16 bytes; a token past the tile's last is the last one again: its sums are not used
+      // rows in units of 16 bytes
       uint32_t xr[NT], ar[MR][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) xr[n] = static_cast<uint32_t>(tok[min(n * 8 + g, count - 1)] * p.x_stride >> 3);
@@ -269,6 +269,9 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
       const uint32_t u0 = (crank * S::kSlices + slice) * 4, step = csize * S::kSlices * 4;
       const int steps = u0 < units ? static_cast<int>((units - u0 + step - 1) / step) : 0;
       // loads of step i, into this thread's own slots: no barrier between them and their use
+      // (Tokens past the tile's last and eights of rows past the rank are left out, and so are the sums with what lies in their slots.
+      // The last row read once more in their place was a line that many asked for: 86 tokens 7960 -> 512 of rank 72 took 22 us, 11
+      // without.)
       auto fetch = [&](int i) {
         const uint32_t k = u0 + i * step + t;
         const bool in = k < units;
@@ -276,13 +279,11 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
         const uint32_t at = smem_u32(ring + (i % S::kStages1) * S::kSlots1 * kThreads);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          if (NT == 1 || n * 8 < count) cp_async_16(at + n * (kThreads * 16), x16 + (xr[n] + kk), in);
+          if (n * 8 + g < count) cp_async_16(at + n * (kThreads * 16), x16 + (xr[n] + kk), in);
 #pragma unroll
         for (int m = 0; m < MR; ++m)
 #pragma unroll
           for (int i2 = 0; i2 < 2; ++i2)
-            // (Eight rows past the rank are left out, and so are the sums with what lies in their slots. The last row read once
-            // more in their place was a line that many asked for: 86 tokens 7960 -> 512 took 22 us at rank 72, 11 without.)
             if ((ranks * MR + m) * 16 + i2 * 8 < p.rank) cp_async_16(at + (NT + m * 2 + i2) * (kThreads * 16), a16 + (ar[m][i2] + kk), in);
       };
 #pragma unroll

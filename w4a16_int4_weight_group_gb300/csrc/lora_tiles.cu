@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 2) long_first_kernel(const Params p)
     const int b0 = crank * p.per_split, nb = ok ? max(min(b0 + p.per_split, blocks) - b0, 0) : 0;
     const uint4 *a = p.a + int64_t(d.adapter) * p.r_units * 8 * p.k_units;
     const int c = tid & 7;
-    uint32_t xr[4];  // (rows past the tile's last are the last one again: their sums are not stored)
+    uint32_t xr[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) xr[j] = static_cast<uint32_t>(p.order[d.first + min(j * 32 + (tid >> 3), d.count - 1)] * p.x_stride);
     auto fetch = [&](int i, uint32_t at) {  // block i of the item into the stage of the at-th block
@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(kThreads, 2) long_first_kernel(const Params p)
       const bool in = k < p.k_units;
       const uint32_t kk = in ? k : 0, to = stages + at % S * kStage;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) cp_async_16(to + place(j * 32 + (tid >> 3), c, kLongTile), p.x + (xr[j] + kk), in);
+      for (int j = 0; j < 4; ++j)  // rows past the tile's last are zeros (the last row again: a line that many ask for)
+        cp_async_16(to + place(j * 32 + (tid >> 3), c, kLongTile), p.x + (xr[j] + kk), in && j * 32 + (tid >> 3) < d.count);
 #pragma unroll
       for (int j = 0; j < 2 * RA; ++j) {  // rows past the rank are zeros
         const uint32_t row = j * 32 + (tid >> 3);

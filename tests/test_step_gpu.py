@@ -56,7 +56,9 @@ def cuda(c):
                                        (300, 264, 200, 8, 300), (333, 520, 328, 40, 2), (400, 200, 264, 72, 9), (600, 328, 136, 128, 4), (1000, 64, 32, 32, 1),
                                        (1024, 72, 40, 8, 512), (270, 72, 40, 24, 513), (1025, 136, 72, 32, 4), (2049, 64, 40, 16, 30), (2100, 72, 96, 64, 2),
                                        (2500, 64, 72, 128, 3), (2200, 2600, 200, 40, 3), (3000, 1032, 520, 72, 40), (2049, 8, 8, 48, 700), (2500, 712, 1160, 104, 1), (1100, 5120, 264, 64, 3),
-                                       (300, 4000, 136, 72, 2), (641, 200, 3904, 128, 40), (640, 4096, 40, 96, 8), (700, 64, 72, 80, 600)])
+                                       (300, 4000, 136, 72, 2), (641, 200, 3904, 128, 40), (640, 4096, 40, 96, 8), (700, 64, 72, 80, 600),
+                                       (2100, 4032, 72, 64, 2), (2500, 64, 4072, 128, 3), (1281, 8, 4088, 40, 20), (1300, 4104, 8, 48, 20), (2600, 1000, 3104, 104, 81),
+                                       (2600, 1000, 3104, 104, 82), (2570, 520, 3608, 64, 41), (257, 72, 4024, 128, 1), (2400, 136, 3968, 72, 48)])
 def test_lora(w, T, K, N, r, n, dtype):
     c = make_lora(T, K, N, r, n, dtype, seed=T + r)
     d = cuda(c)
@@ -85,11 +87,12 @@ def test_lora_strided_rows_and_no_scales(w, T, r):
     assert (qkv[:, :160] == 7.0).all() and (qkv[:, 296:] == 7.0).all()
 
 
-@pytest.mark.parametrize("T,r", [(30, 32), (700, 32), (1500, 32), (2300, 32), (2300, 40), (2300, 96)])
+@pytest.mark.parametrize("T,r,N", [(30, 32, 264), (700, 32, 264), (1500, 32, 264), (2300, 32, 264), (2300, 40, 264), (2300, 96, 264), (2300, 40, 3656),
+                                   (2300, 96, 3656)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_lora_of_a_token_does_not_depend_on_its_neighbours(w, T, r, dtype):
+def test_lora_of_a_token_does_not_depend_on_its_neighbours(w, T, r, N, dtype):
     """The same token, among others in another order, on all ways of finding tiles: the same bits."""
-    c = make_lora(T, 520, 264, r, 4, dtype, seed=3, ids=[i % 4 for i in range(T)])
+    c = make_lora(T, 520, N, r, 4, dtype, seed=3, ids=[i % 4 for i in range(T)])
     d = cuda(c)
     first = w.w4a16_lora(**d)
     order = torch.randperm(T, generator=torch.Generator().manual_seed(5)).cuda()

@@ -311,7 +311,7 @@ def test_two_threads_at_once(w):
 def test_bounded_waits_of_the_adapters_report_timeout_and_recover(w):
     """No MMA is issued, so the waits for them run out: the status says so, and the next call is right."""
     for r in (40, 128):
-        c = make_lora(2100, 200, 136, r, 2, "bf16", seed=r)
+        c = make_lora(2100, 200, 3960, r, 2, "bf16", seed=r)
         d = cuda(c)
         assert w.w4a16_get_device_error() == 0
         try:

@@ -569,31 +569,29 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *
   }
 }
 
-// Tokens of a sorted tile: 32 while there are few of them, else 64 (A and B are read half as often, for fewer and larger shares
-// of work). 2560 -> 3840, 16 adapters, rank 16: 1500 tokens 18.1 us with 32 and 19.2 with 64, 2000 tokens 18.7 and 19.5. 5120 -> 7168, 8191 tokens
+// Tokens of a sorted tile: 32 while there are few of them or the rank is past 32 (the sums of 64 do not fit beside its h), else 64 (A and B
+// are read half as often, for fewer and larger shares of work). 2560 -> 3840, 16 adapters, rank 16: 1500 tokens 18.1 us with 32 and 19.2 with 64, 2000 tokens 18.7 and 19.5. 5120 -> 7168, 8191 tokens
 // of 12 adapters: rank 16 83 and 77, rank 32 84 and 80.
 constexpr int64_t kMidTokens = 2048;
-// Many tokens of ranks past 32 go to the form on tcgen05. Warp-level against tcgen05 (16 adapters 2560 -> 3840; 6 adapters 5120 -> 7168), replayed:
-// rank 40, 1030 tokens 25.4 against 22.6 us; 28.9 against 28.0; 2000 tokens 27.2 against 25.7; 37.0 against 34.6
-// rank 64, 1030 tokens 24.7 against 23.5; 27.9 against 29.7; 2000 tokens 26.5 against 28.0; 35.7 against 36.8; 8191 tokens 113 against 87
-// rank 128, 1030 tokens 36.8 against 31.6; 36.0 against 37.3; 2000 tokens 37.5 against 33.5; 56.6 against 45.9; 8191 tokens 167 against 104
-// and for ranks to 32: 4000 tokens of rank 32 44.2 against 45.5, 16000 tokens 77.7 against 80.9.
-// Up to 1024 tokens for ranks past 64 alone, whose warp-level form has one CTA on an SM: from 641 tokens, and from 257 where the tiles of
-// 128 are likely full, unless the layer is so small that three launches show. Rank 72, 3 adapters in runs: 300 tokens 5120 -> 7168 29.5
-// against 23.2, 500 tokens 888 -> 7432 35.8 against 25.6; 30 adapters at random: 500 tokens 41.1 against 43.6, 800 tokens 68.9 against 46.0;
-// rank 128 512 -> 512 13.3 to 14.1 against 18.5 to 20.2.
+// Which calls go to the form on tcgen05: ranks past 32, in layers of some size (three launches show: 512 -> 512, 2000 tokens of rank 128 15.0 us
+// warp-level, 20.7 on tcgen05; at 8000 tokens as long), and where its tiles of 128 tokens are not nearly empty, since each has A and B
+// read and multiplied in full. Warp-level against tcgen05, 5120 -> 7168, replayed:
+//   rank 40: 1000 tokens of 12 adapters 25.4 against 29.3; 1500 of 12 35.2 against 30.3; 4000 of 40 87 against 68, of 120 88 against 106;
+//     8000 of 3 101 against 78, of 400 154 against 288
+//   rank 72 (one CTA on an SM warp-level): 300 tokens of 3 26.2 against 23.1; 1000 of 40 63 against 56; 1100 of 120 79 against 116; 3000 of 120
+//     102 against 127; 4000 of 120 195 against 130; 8000 of 3 196 against 88
+// and for ranks to 32: 2560 -> 3840, 4000 tokens of rank 32 44.2 against 45.5, 16000 tokens 77.7 against 80.9.
 constexpr int kMidRank = 32, kWideRank = 64;
-constexpr int64_t kWideTokens = 640, kWideFill = 96, kWideLayer = 4096;
+constexpr int64_t kLongLayer = 4096, kLongTokens = 1280, kWideTokens = 640, kWideAdapters = 48;
 bool may_be_long(int64_t tokens, int rank, int64_t adapters) {
-  if (tokens > kCountTokens) return rank > kMidRank;
-  return rank > kWideRank && (tokens > kWideTokens || (tokens > kFewTokens && tokens >= kWideFill * adapters));
+  if (rank <= kMidRank) return false;
+  if (rank <= kWideRank) return tokens > kLongTokens && tokens >= 64 * adapters;
+  return tokens > kFewTokens && (tokens >= 32 * adapters || (adapters <= kWideAdapters && (tokens > kWideTokens || tokens >= 24 * adapters)));
 }
-bool is_long(const LoraArgs &a) {
-  return may_be_long(a.tokens, a.rank, a.adapters) && (a.tokens > kCountTokens || a.K + a.N >= kWideLayer);
-}
+bool is_long(const LoraArgs &a) { return a.K + a.N >= kLongLayer && may_be_long(a.tokens, a.rank, a.adapters); }
 bool can_count(int64_t tokens, int64_t adapters) { return tokens <= kCountTokens && adapters <= kCountAdapters; }
-int sorted_tile(int64_t tokens) { return tokens <= kMidTokens ? 32 : 64; }
-int64_t most_tiles(int64_t tokens, int64_t adapters) { return tokens / sorted_tile(tokens) + std::min<int64_t>(tokens, adapters + 1); }
+int sorted_tile(int64_t tokens, int rank) { return tokens <= kMidTokens || rank > kMidRank ? 32 : 64; }
+int64_t most_tiles(int64_t tokens, int64_t adapters, int rank) { return tokens / sorted_tile(tokens, rank) + std::min<int64_t>(tokens, adapters + 1); }
 
 template <class DT, class S, int TILING>
 cudaError_t go(Params p, int64_t tiles, int64_t most, const DeviceInfo &dev, cudaStream_t stream) {
@@ -663,7 +661,7 @@ cudaError_t run(const Params &p, bool few, int64_t tiles, int64_t most, const De
     if (r <= 64) return go<DT, Shape<4, 4, 1, 2, 2>, kCounted>(p, tiles, most, dev, stream);
     return go<DT, Shape<4, 4, 2, 2, 1>, kCounted>(p, tiles, most, dev, stream);
   }
-  if (p.tokens <= kMidTokens) {
+  if (p.tokens <= kMidTokens || r > kMidRank) {
     if (r <= 16) return go<DT, Shape<1, 4, 1, 3, 2>, kListed>(p, tiles, most, dev, stream);
     if (r <= 32) return go<DT, Shape<2, 4, 1, 3, 2>, kListed>(p, tiles, most, dev, stream);
     if (r <= 64) return go<DT, Shape<4, 4, 1, 2, 2>, kListed>(p, tiles, most, dev, stream);
@@ -677,13 +675,13 @@ cudaError_t run(const Params &p, bool few, int64_t tiles, int64_t most, const De
 
 // The workspace past the first 4 KiB (the counters of other calls): the number of tiles, the sorted tokens, the tiles, h
 static size_t tiles_at(int64_t tokens) { return 256 + static_cast<size_t>((tokens * 4 + 255) / 256 * 256); }
-static size_t h_at(int64_t tokens, int64_t adapters) {
-  return tiles_at(tokens) + (static_cast<size_t>(most_tiles(tokens, adapters)) * sizeof(Tile) + 255) / 256 * 256;
+static size_t h_at(int64_t tokens, int64_t adapters, int rank) {
+  return tiles_at(tokens) + (static_cast<size_t>(most_tiles(tokens, adapters, rank)) * sizeof(Tile) + 255) / 256 * 256;
 }
 size_t lora_workspace_bytes(int64_t tokens, int rank, int64_t adapters) {
   const bool maybe = may_be_long(tokens, rank, adapters);
   if (tokens <= kFewTokens || (can_count(tokens, adapters) && !maybe)) return 0;
-  return 4096 + h_at(tokens, adapters) + (maybe ? long_workspace_bytes(tokens, rank) : 0);
+  return 4096 + h_at(tokens, adapters, rank) + (maybe ? long_workspace_bytes(tokens, rank) : 0);
 }
 int lora_most_adapters() { return kMaxAdapters; }
 
@@ -709,8 +707,8 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
   // tiles, as far as can be told here, and at most
   int64_t tiles = std::min<int64_t>(a.tokens, a.tokens / kFewTile + a.adapters), most = a.tokens;
   if (!few) {
-    tiles = (a.tokens + sorted_tile(a.tokens) - 1) / sorted_tile(a.tokens) + std::min<int64_t>(a.adapters, a.tokens / 2) / 2;
-    most = most_tiles(a.tokens, a.adapters);
+    tiles = (a.tokens + sorted_tile(a.tokens, a.rank) - 1) / sorted_tile(a.tokens, a.rank) + std::min<int64_t>(a.adapters, a.tokens / 2) / 2;
+    most = most_tiles(a.tokens, a.adapters, a.rank);
   }
   if (!few && (long_form || !can_count(a.tokens, a.adapters))) {
     uint8_t *ws = static_cast<uint8_t *>(a.workspace) + 4096;
@@ -719,7 +717,7 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
     Tile *list = reinterpret_cast<Tile *>(ws + tiles_at(a.tokens));
     p.num_tiles = num;
     p.tiles = list;
-    const int per = long_form ? kLongTile : sorted_tile(a.tokens);
+    const int per = long_form ? kLongTile : sorted_tile(a.tokens, a.rank);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1, 1, 1);
     cfg.blockDim = dim3(kSortThreads, 1, 1);
@@ -733,7 +731,7 @@ cudaError_t launch_lora(const LoraArgs &a, const DeviceInfo &dev) {
     const cudaError_t e = cudaLaunchKernelEx(&cfg, lora_sort_kernel, a.ids, static_cast<int>(a.tokens), p.adapters, per, p.copy, p.order, list, num);
     if (e != cudaSuccess) return e;
     note_launch();
-    if (long_form) return launch_long(a, dev, p.order, list, num, reinterpret_cast<float *>(ws + h_at(a.tokens, a.adapters)));
+    if (long_form) return launch_long(a, dev, p.order, list, num, reinterpret_cast<float *>(ws + h_at(a.tokens, a.adapters, a.rank)));
   }
   return a.dtype == W4A16_BF16 ? run<BF16>(p, few, tiles, most, dev, a.stream) : run<F16>(p, few, tiles, most, dev, a.stream);
 }

@@ -12,8 +12,8 @@
 // or more ahead of the MMAs that one thread issues; waits for MMAs are bounded, and the threads of a CTA vote before each
 // barrier, so that all give up together.
 //
-// Taken instead of the warp-level form where that is bound by mma.sync: for ranks past 32 (its second product takes two for each,
-// and one m16n8k16 takes about 16 cycles on a quarter of an SM). Bound by what the SMs read and write through L2: base, out, and B
+// Taken instead of the warp-level form where that is bound by mma.sync: for many tokens of ranks past 32 (its second product takes two for
+// each, and one m16n8k16 takes about 16 cycles on a quarter of an SM), a good part of a tile for each adapter. Bound by what the SMs read and write through L2: base, out, and B
 // once a tile, 6.6 to 7.1 TB/s in the second kernel. Measured: 8191 tokens 5120 -> 7168 of 12 adapters, rank 64 23 + 50 us and 7 for the sort (87 a
 // call out of L2), rank 128 28 + 63 (104).
 #include <algorithm>

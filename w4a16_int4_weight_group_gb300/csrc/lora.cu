@@ -630,10 +630,10 @@ cudaError_t go(Params p, int64_t tiles, int64_t most, const DeviceInfo &dev, cud
   // CTAs of a tile: up to eight, while all tiles are resident together and the split pays for the cluster's barriers and sums. With 1, 2, 4 and
   // 8 CTAs, us: 48 tokens of rank 16, K + N = 512 3.9, 4.8, 5.0, 6.0; 2048 5.8, 5.3, 5.0, 6.0; 4096 8.4, 6.8, 5.8, 6.2; 7680 17.8, 11.5, 8.2, 8.4;
   // 300 of rank 32: 512 5.8, 7.2, 7.5, 9.4; 2048 12.0, 9.4, 7.7, 9.6; 5632 21.4, 14.3, 10.9, 12.1; 12288 48.6, 28.8, 18.1, 16.8.
-  // Ranks past 64 do about three times as much in a step (313 tokens of rank 72, K + N = 1336: 22.4 with one, 16.7 with four).
-  const int64_t both = (p.K + p.N) * (S::RS > 1 ? 3 : 1);
-  // (one tile alone, 1 token of rank 16: 512 3.3, 4.1, 4.1, 4.3; 4096 7.7, 6.2, 4.8, 4.4)
-  const int most_c = both < 1536 ? 0 : both < 7168 && tiles > 2 ? 2 : 3;
+  // 6 tokens of as many adapters, K + N = 6400: rank 16 11.6, 8.4, 6.2, 5.1; rank 64 16.6, 11.6, 8.2, 6.5. One tile alone, 1 token of rank 16: 512
+  // 3.3, 4.1, 4.1, 4.3; 4096 7.7, 6.2, 4.8, 4.4. Ranks past 64 do about twice as much in a step: 6 tokens of rank 128, 512 4.8, 5.9, 6.2, 6.3.
+  const int64_t both = (p.K + p.N) * (S::RS > 1 ? 2 : 1);
+  const int most_c = both < 1536 ? 0 : tiles > 2 && both < (tiles > 12 ? 7168 : 5120) ? 2 : 3;
   int c = 0;
   while (c < most_c && tiles <= room[c + 1]) ++c;
   p.csize = 1 << c;

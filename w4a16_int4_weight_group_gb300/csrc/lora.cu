@@ -23,8 +23,8 @@
 //
 // Bound by memory for long prompts (base read and out written are most of the bytes), by the chain of copies, barriers and sums for few tokens. Measured, replayed from a graph: 8191 tokens 5120 -> 7168 of rank
 // 32 75 us for 328 MB, 4.4 TB/s, 0.65 of the device's copy rate (9 us of them the sort and the launch; the same tiles copied without
-// an adapter 0.85 of it while they stream); DRAM 53 %, tensor pipe 31 %, schedulers 42 % of the cycles. 520 tokens 2560 -> 3840 of rank 64 21
-// us; 48 tokens 5120 -> 7168 of rank 16 9.0; one token 2112 -> 1152 4.2.
+// an adapter 0.85 of it while they stream); DRAM 53 %, tensor pipe 31 %, schedulers 42 % of the cycles. 520 tokens 2560 -> 3840 of rank 64 19.2
+// us; 48 tokens 5120 -> 7168 of rank 16 8.7; one token 2112 -> 1152 4.1.
 #include <algorithm>
 #include <atomic>
 

@@ -469,10 +469,11 @@ size_t w4a16_verify_drafts_workspace_size(int64_t total, int64_t vocab);
  *   parent outside [0, batch) gives an empty sequence.
  * w4a16_kv_reserve - room for the tokens up to new_lens (int32 [batch], batch <= 4096). A sequence that grows and whose last page is
  *   partly filled and held by others too gets a page of its own in its place, of which copies[b] (int32 [batch, 2]) says {from,
- *   to}; else copies[b] is {-1, -1}. (The last holder among the call's sequences keeps the page, if no one else holds it.) Then new pages up
+ *   to}; else copies[b] is {-1, -1}. (The last holder among the call's sequences keeps the page, if no one else holds it once the
+ *   others have their copies.) Then new pages up
  *   to new_lens. Pages are the free ones in ascending order, for the sequences in ascending order; each gets
  *   refs 1. held[b]: the tokens that the sequence has room for: new_lens[b], less where pages (or the table's row) ran
- *   out (no room for a copy: kv_lens[b]), and kv_lens[b] where it does not grow. Entries of pages that it did not get stay as they are.
+ *   out (its last page is still held by others too: kv_lens[b]), and kv_lens[b] where it does not grow. Entries of pages that it did not get stay as they are.
  * w4a16_kv_copy - copies of whole pages, copies int32 [n, 2] {from, to}, in all layers; pairs with a page outside the cache are
  *   skipped. No page is written twice, or read and written, in one call.
  * w4a16_kv_free - the pages of the tokens from keep (int32 [batch], NULL: 0) on are given back: refs shrink by one (not

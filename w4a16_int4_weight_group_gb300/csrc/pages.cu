@@ -4,7 +4,7 @@
 // refs[page] counts the sequences that hold a page; a page with none is free. fork and free only add and subtract, and
 // reserve hands out the free pages in ascending order to the sequences in theirs: there is no list whose order could depend on
 // timing. A sequence that is to write into a page that others hold too gets a copy (the last holder in the call keeps the
-// page): reserve says which pages, copy moves them in all layers. Nothing comes back to the host.
+// page, once the others have theirs): reserve says which pages, copy moves them in all layers. Nothing comes back to the host.
 //
 // All of it is bytes moved or integers counted. reserve is one CTA, bound by the latency of its steps (holders of the
 // same page counted against each other in shared memory, sums over the sequences, free pages counted 4096 at a time); copy is
@@ -183,13 +183,17 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_kernel(const Pool p, 
     }
     found += total;
   }
+  __syncthreads();  // the copies are counted
   for (int b = tid; b < batch; b += kReserveThreads) {
     const int64_t len = old_len(b);
     int64_t now = len;
     if (new_lens[b] > len) {
       const bool copy = first[b] & 0x40000000;
       const int got = min(start_of(b + 1), found) - min(start_of(b), found);
-      if (!copy || got > 0) now = max(len, min(int64_t(new_lens[b]), (pages_of(len, p) + got - copy) * p.page_size));
+      // (A page kept in place is the sequence's own only if every earlier holder got its copy; one that did not used up the free pages,
+      // so that this one got none either.)
+      const bool own = copy ? got > 0 : tail[b] < 0 || __ldcg(p.refs + tail[b]) <= 1;
+      if (own) now = max(len, min(int64_t(new_lens[b]), (pages_of(len, p) + got - copy) * p.page_size));
     }
     held[b] = static_cast<int32_t>(now);
   }

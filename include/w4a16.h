@@ -410,8 +410,8 @@ w4a16_status w4a16_token_logprobs(const void *logits, int64_t row_stride, int64_
  *   ids     int32 [tokens]; a token whose id is not in [0, adapters) has no adapter: its row of out is base's
  *   scales  float32 [adapters] or NULL (1)
  *   k, n: multiples of 8; rank: a multiple of 8, at most 128; adapters: at most 8191
- * Sums are fp32; x a_i^T keeps 16 (BF16) or, below the token's largest, 22 bits (F16) for the second product; out is rounded
- * once. A token's result does not depend on the other tokens of the call, apart from how its sums are split.
+ * Sums are fp32; x a_i^T keeps all 24 (BF16) or, below the token's largest, 22 bits (F16) for the second product; out is rounded
+ * once. An infinite element of b gives NaN (its product with a part of x a_i^T that is 0). A token's result does not depend on the other tokens of the call, apart from how its sums are split.
  *   workspace  device memory, 256-byte aligned, w4a16_lora_workspace_size bytes (0, and NULL will do, for up to 256 tokens, and for up
  *              to 1024 of up to 512 adapters where the rank is at most 64); its first 4 KiB are not touched, so that a stream's buffer for the layer and the attention serves here too.
  * Errors: INVALID_ARG (sizes, nulls, overlap, workspace), UNSUPPORTED (dtype, k, n, rank, adapters), MISALIGNED, CUDA. A kernel that

@@ -12,9 +12,11 @@
 // contiguous columns of a token: 16-byte copies of base and stores of out. (Steps of 128 instead of 64 bytes a row, in a ring that a warp
 // shares: the first product alone 3 us faster, the second 7 slower, since half the warps fit.)
 //
-// h is fp32 and goes into the second product as two numbers of the dtype, the upper part and the rest: 16 bits of it for
-// bfloat16, 22 below the token's largest for float16 (whose range its sums may leave: each token's h is scaled by a power
-// of two). The rounding of out is then the only one that shows.
+// h is fp32 and goes into the second product whole, as a sum of numbers of the dtype: three for bfloat16, which hold all 24 bits (with
+// two, 16 of them, every 500th element of out was rounded the other way, and what cancels between the products was off), two for
+// float16, 22 bits below the token's largest (whose range its sums may leave: each token's h is scaled by a power
+// of two). The rounding of out is then the only one that shows. The third part costs 7 to 9 % at ranks 17 to 64 of long prompts (8191 tokens 5120 -> 7168, rank 32:
+// 74.6 -> 81.3 us); up to rank 16, and for few tokens, the parts share a pass whose half was empty, and it costs nothing or 2 %.
 //
 // Tiles: tokens of the same adapter wherever they stand. Up to kFewTokens tokens every CTA ranks the tokens among
 // those of their adapter by itself, up to kCountTokens it counts them by adapter in shared memory (one launch); more are sorted by a
@@ -83,8 +85,12 @@ struct Shape {
   static_assert(kSlices * kSums * 16 + kH * 4 <= kRing, "the partial sums and h lie in the ring");
   static_assert(kSums % kMaxCluster == 0, "equal shares of the sums for the CTAs of a cluster");
   static_assert(kStages1 >= 2 && kStages2 >= 2, "one stage is in flight while another is used");
-  static constexpr int kFrag = kMT * kChunks * 2 * 2 * 32 * 16;  // bytes: [m-tile][chunk][step][upper, lower][lane]
-  static constexpr int kSmem = kRing + kFrag;
+  // The parts of h that one pass of the second product takes: where a rank of 16 leaves half of a chunk's k empty, and a single n-tile half of
+  // the m-tile's rows, these hold further parts (their B again, their sums added)
+  static constexpr int kKParts = MR * RS == 1 ? 2 : 1, kMParts = NT == 1 ? 2 : 1;
+  template <int PARTS>
+  static constexpr int kPasses = (PARTS + kKParts * kMParts - 1) / (kKParts * kMParts);
+  static constexpr int kFrag = kMT * kChunks * 2 * 32 * 16;  // bytes of a pass: [m-tile][chunk][step][pass][lane]
 };
 
 __device__ __forceinline__ void st_dsmem_f32(uint32_t cluster_addr, float v) {
@@ -105,12 +111,16 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
   uint4 *ring = reinterpret_cast<uint4 *>(smem) + threadIdx.x;           // this thread's slots, kThreads apart
   float4 *part = reinterpret_cast<float4 *>(smem);                       // [slice][m-tile][n-tile][lane], in the ring's place
   float *h = reinterpret_cast<float *>(part + S::kSlices * S::kSums);    // [token][rank], behind it
+  constexpr int kP = kParts<DT>, kPasses = S::template kPasses<kP>;
   uint4 *frag = reinterpret_cast<uint4 *>(smem + S::kRing);
   __shared__ int tok[S::kTokens];
   __shared__ float back[S::kMT * 16];  // what a token's h was divided by (float16)
-  constexpr int kIds = TILING == kRanked ? kFewTokens : TILING == kCounted ? kCountTokens : 4;
-  __shared__ __align__(16) int ids_s[kIds];  // counted: adapter << 16 | the token's rank in it
-  __shared__ uint16_t leaders[TILING == kCounted ? kCountTokens / S::kTokens + kCountAdapters + 1 : kIds];  // counted: adapter << 5 | its tile
+  constexpr int kIds = TILING == kRanked ? kFewTokens : 4, kCodes = TILING == kCounted ? kCountTokens : 4;
+  __shared__ __align__(16) int ids_s[kIds];
+  // counted: each token's tile (adapter << 5 | the tile's number in it) and place there, in 3 KB, which lets two CTAs of rank 64 on an SM
+  __shared__ uint16_t codes[kCodes];
+  __shared__ uint8_t places[kCodes];
+  __shared__ uint16_t leaders[TILING == kCounted ? kCountTokens / S::kTokens + kCountAdapters + 1 : kIds];  // counted: the tiles
   __shared__ int warp_count[kWarps];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -125,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
   if constexpr (TILING == kListed) {
     ntiles = *p.num_tiles;
   } else if constexpr (TILING == kCounted) {
-    static_assert(kCountTokens / S::kTokens <= 32 && kCountAdapters < 2048, "a tile in 16 bits");
+    static_assert(kCountTokens / S::kTokens <= 32 && kCountAdapters < 2048 && S::kTokens <= 256, "a tile in 16 bits, a place in 8");
     static_assert(((kWarps + 1) * (kCountAdapters + 1)) * 4 <= S::kRing, "the counters lie in the ring");
     constexpr int kEach = kCountTokens / kThreads;
     int *counts = reinterpret_cast<int *>(smem);  // [warp][adapter], tokens without one last; then the sums
@@ -168,7 +178,10 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
-      if (id[j] >= 0) ids_s[warp * per + j * 32 + lane] = id[j] << 16 | (mine[id[j]] + rank[j]);
+      if (id[j] >= 0) {
+        const int i = warp * per + j * 32 + lane, r = mine[id[j]] + rank[j];
+        codes[i] = static_cast<uint16_t>(id[j] << 5 | r / S::kTokens), places[i] = static_cast<uint8_t>(r % S::kTokens);
+      }
     if (warp == 0) {
       int listed = 0;
       for (int a0 = 0; a0 < na; a0 += 32) {
@@ -221,13 +234,13 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
       adapter = d.adapter, count = d.count;
       if (tid < count) tok[tid] = p.order[d.first + tid];
     } else if constexpr (TILING == kCounted) {
-      const int d = leaders[tile], a = d >> 5, first = (d & 31) * S::kTokens;
+      const int d = leaders[tile], a = d >> 5;
       adapter = a == p.adapters ? -1 : a;
       count = 0;
       for (int i0 = 0; i0 < p.tokens; i0 += kThreads) {
-        const int i = i0 + tid, v = i < p.tokens ? ids_s[i] : -1, at = (v & 0xFFFF) - first;
-        const bool in = v >= 0 && (v >> 16) == a && at >= 0 && at < S::kTokens;
-        if (in) tok[at] = i;
+        const int i = i0 + tid;
+        const bool in = i < p.tokens && codes[i] == d;
+        if (in) tok[places[i]] = i;
         count += __syncthreads_count(in);
       }
     } else {
@@ -374,27 +387,30 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
         }
         __syncthreads();
       }
-      for (int e = tid; e < S::kMT * S::kChunks * 32; e += kThreads) {
-        const int l = e & 31, c = (e >> 5) % S::kChunks, m = (e >> 5) / S::kChunks;
-        uint32_t hi[2][4], lo[2][4];  // [row g, g + 8][pair]
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = m * 16 + i * 8 + (l >> 2), r0 = c * 32 + (l & 3) * 8;
-          const bool in = row < S::kTokens;  // (one n-tile fills half an m-tile)
-          float f = 1.f;
-          if constexpr (!DT::kBF16) f = in ? 1.f / back[row] : 1.f;  // (exact: a power of two)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const bool ok = in && r0 + 2 * j < p.rank;  // (rank is even)
-            const float v0 = ok ? h[row * S::kHStride + r0 + 2 * j] * f : 0.f, v1 = ok ? h[row * S::kHStride + r0 + 2 * j + 1] * f : 0.f;
-            split2<DT>(v0, v1, hi[i][j], lo[i][j]);
-          }
+      // a thread's words: of a lane's fragment of a step those of row g (i = 0) or g + 8
+      uint32_t *words = reinterpret_cast<uint32_t *>(frag);
+      for (int e = tid; e < S::kMT * S::kChunks * 128; e += kThreads) {
+        const int i = e & 1, l = e >> 1 & 31, st = e >> 6 & 1, c = (e >> 7) % S::kChunks, m = (e >> 7) / S::kChunks;
+        const int row = m * 16 + (S::kMParts == 1 ? i * 8 : 0) + (l >> 2);
+        const int r0 = (S::kKParts == 1 ? c * 32 + (l & 3) * 8 : (l & 1) * 8) + 4 * st;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r0 < p.rank) v = *reinterpret_cast<const float4 *>(h + row * S::kHStride + r0);  // (the rank is a multiple of 8)
+        if constexpr (!DT::kBF16) {
+          const float unit = 1.f / back[row];  // (exact: a power of two)
+          v.x *= unit, v.y *= unit, v.z *= unit, v.w *= unit;
         }
-        uint4 *at = frag + ((m * S::kChunks + c) * 4) * 32 + l;
+        uint32_t part[2][kP];
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          at[(st * 2) * 32] = make_uint4(hi[0][2 * st], hi[1][2 * st], hi[0][2 * st + 1], hi[1][2 * st + 1]);
-          at[(st * 2 + 1) * 32] = make_uint4(lo[0][2 * st], lo[1][2 * st], lo[0][2 * st + 1], lo[1][2 * st + 1]);
+        for (int q = 0; q < kP; ++q) part[0][q] = take_part<DT>(v.x, v.y), part[1][q] = take_part<DT>(v.z, v.w);
+        const int first = (S::kMParts == 1 ? 0 : i) * S::kKParts + (S::kKParts == 1 ? 0 : l >> 1 & 1);  // of the first pass
+        uint32_t *at = words + (((m * S::kChunks + c) * 2 + st) * kPasses * 32 + l) * 4 + i;
+#pragma unroll
+        for (int q = 0; q < kPasses; ++q) {
+          uint2 w = make_uint2(0, 0);  // the part first + q kMParts kKParts, if there is one
+#pragma unroll
+          for (int k = 0; k < kP; ++k)
+            if (k == first + q * S::kMParts * S::kKParts) w = make_uint2(part[0][k], part[1][k]);
+          at[q * 128] = w.x, at[q * 128 + 2] = w.y;
         }
       }
       // (the ring takes the second product's loads: the partial sums in its place were read by the whole cluster)
@@ -425,9 +441,10 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int c = 0; c < S::kChunks; ++c) {
-            const bool in = has && c * 4 + t < r_units;
+            const uint32_t unit = S::kKParts == 1 ? c * 4 + t : t & 1;
+            const bool in = has && unit < r_units;
             cp_async_16(at + (S::kMT * S::kHalves + j * S::kChunks + c) * (kThreads * 16),
-                        b16 + (in ? uint64_t(brow + 2 * j) * r_units + c * 4 + t : 0), in);
+                        b16 + (in ? uint64_t(brow + 2 * j) * r_units + unit : 0), in);
           }
       }
     };
@@ -461,16 +478,18 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) lora_kernel(const Params p
           for (int c = 0; c < S::kChunks; ++c)
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
-              const uint4 *f = frag + ((m * S::kChunks + c) * 4 + st * 2) * 32 + lane;
-              const uint4 hi = f[0], lo = f[32];
-              const uint32_t fh[4] = {hi.x, hi.y, hi.z, hi.w}, fl[4] = {lo.x, lo.y, lo.z, lo.w};
+              const uint4 *f = frag + ((m * S::kChunks + c) * 2 + st) * kPasses * 32 + lane;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t b0 = st ? bv[j][c].z : bv[j][c].x, b1 = st ? bv[j][c].w : bv[j][c].y;
-                mma_16816<DT::kBF16>(acc[j], fl, b0, b1);
-                mma_16816<DT::kBF16>(acc[j], fh, b0, b1);
+              for (int q = kPasses - 1; q >= 0; --q) {  // the smallest parts first
+                const uint4 v = f[q * 32];
+                const uint32_t fr[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mma_16816<DT::kBF16>(acc[j], fr, st ? bv[j][c].z : bv[j][c].x, st ? bv[j][c].w : bv[j][c].y);
               }
             }
+          if constexpr (S::kMParts == 2)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j][0] += acc[j][2], acc[j][1] += acc[j][3];
           float f0 = 1.f, f1 = 1.f;
           if constexpr (!DT::kBF16) f0 = back[i0 < S::kTokens ? i0 : 0], f1 = back[i1 < S::kTokens ? i1 : 0];
           add2<DT>(o0.x, acc[0][0], acc[0][1], f0), add2<DT>(o1.x, acc[0][2], acc[0][3], f1);
@@ -599,7 +618,8 @@ cudaError_t go(Params p, int64_t tiles, int64_t most, const DeviceInfo &dev, cud
   auto kernel = lora_kernel<DT, S, TILING>;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = S::kSmem;
+  constexpr int kSmem = S::kRing + S::kFrag * S::template kPasses<kParts<DT>>;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -616,7 +636,7 @@ cudaError_t go(Params p, int64_t tiles, int64_t most, const DeviceInfo &dev, cud
   const bool kept = dev.device < kDevices;
   for (int i = 0; i < 4; ++i) room[i] = kept ? resident[dev.device][i].load(std::memory_order_acquire) : 0;
   if (room[0] == 0) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     for (int i = 3; i >= 0 && e == cudaSuccess; --i) {  // (the first entry, which says that all are there, last)
       attr[0].val.clusterDim.x = 1u << i;
       cfg.gridDim = dim3(8, 1, 1);

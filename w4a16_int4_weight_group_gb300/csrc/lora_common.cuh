@@ -11,30 +11,29 @@ struct Tile {
   int adapter, first, count;  // of the sorted tokens
 };
 
-// upper and lower part of two numbers, as pairs of the dtype
+// A number of h as the sum of this many of the dtype: all 24 bits for bfloat16, 22 below the token's largest for float16 (scaled before)
 template <class DT>
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+constexpr int kParts = DT::kBF16 ? 3 : 2;
+
+// The next part of two numbers, as a pair of the dtype; the numbers become what is left of them
+template <class DT>
+__device__ __forceinline__ uint32_t take_part(float &a, float &b) {
+  uint32_t w;
   float ha, hb;
-  if constexpr (DT::kBF16) {  // truncated, so that a finite number's upper part is finite
+  if constexpr (DT::kBF16) {  // truncated, so that a finite number's part is finite; the third one is exact
     const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    hi = prmt(ua, ub, 0x7632);
+    w = prmt(ua, ub, 0x7632);
     ha = __uint_as_float(ua & 0xFFFF0000u), hb = __uint_as_float(ub & 0xFFFF0000u);
-    if (!(a == a)) hi |= 0x7FFFu;  // a NaN's payload may lie in the lost bits
-    if (!(b == b)) hi |= 0x7FFF0000u;
+    if (!(a == a)) w |= 0x7FFFu;  // a NaN's payload may lie in the lost bits
+    if (!(b == b)) w |= 0x7FFF0000u;
   } else {
     const __half2 h = __floats2half2_rn(a, b);
-    hi = *reinterpret_cast<const uint32_t *>(&h);
+    w = *reinterpret_cast<const uint32_t *>(&h);
     ha = __low2float(h), hb = __high2float(h);
   }
   // an infinite or NaN number has no rest
-  const float ra = fabsf(a) < INFINITY ? a - ha : 0.f, rb = fabsf(b) < INFINITY ? b - hb : 0.f;
-  if constexpr (DT::kBF16) {
-    const __nv_bfloat162 l = __floats2bfloat162_rn(ra, rb);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
-  } else {
-    const __half2 l = __floats2half2_rn(ra, rb);
-    lo = *reinterpret_cast<const uint32_t *>(&l);
-  }
+  a = fabsf(a) < INFINITY ? a - ha : 0.f, b = fabsf(b) < INFINITY ? b - hb : 0.f;
+  return w;
 }
 
 // The power of two that brings a token's largest number to [2^13, 2^14), as what its sums are multiplied by in the end (float16)

@@ -4,8 +4,8 @@
 //
 // Two kernels. The first multiplies 128 gathered rows of x by A, 64 elements of K a step, K split over the CTAs of a cluster where the tiles
 // do not fill the device; their fp32 sums are added through distributed shared memory, in order, and go to a workspace (r numbers a
-// token). The second multiplies them by s, puts h as two numbers of the dtype, upper part and rest (float16: scaled by a power of two a
-// token), into tensor memory, and multiplies it by columns of B, the rest's and the upper part's product into the
+// token). The second multiplies them by s, puts h as a sum of numbers of the dtype (three for bfloat16, which hold all of its bits, two for float16: scaled by a
+// power of two a token) into tensor memory, and multiplies it by columns of B, all parts' products into the
 // same accumulators; each thread adds a row of base to a row of these, and the rows go out in pieces of 128 bytes and more.
 //
 // All copies are asynchronous 16-byte ones (rows are gathered, so there is no box to describe) into the 128-byte swizzle, a stage
@@ -274,10 +274,13 @@ __global__ void __launch_bounds__(kThreads, 2) long_first_kernel(const Params p)
 
 // Second product, 64 columns a step: a ring of copies (base, whose place the results take, and B), two accumulators, so that copies and
 // MMAs of the next steps run while this one's results are added and stored. h is in tensor memory, which leaves shared memory to the
-// ring of two CTAs on an SM (h in shared memory, rank 128: one CTA with two stages of 128 columns 70 us, three of 64 93).
+// ring of two CTAs on an SM (h in shared memory, rank 128: one CTA with two stages of 128 columns 70 us, three of 64 93). Three parts of 128
+// ranks leave room for one accumulator beside them: the next step's MMAs are issued once it has been read.
 template <class DT, int RA>
 __global__ void __launch_bounds__(kThreads, 2) long_second_kernel(const Params p) {
   constexpr int NC = kCols, S = kSecondStages<RA>, kHalf = 32 * RA;  // kHalf: columns of tensor memory of a part of h
+  constexpr int kP = kParts<DT>, kAccs = kP * kHalf + 2 * NC <= 256 ? 2 : 1;
+  static_assert(kP * kHalf + kAccs * NC <= 256, "two CTAs on an SM");
   constexpr int kB = RA * NC * 128, kBase = kLongTile * NC * 2, kRow = NC / 8;  // kRow: units of a row of base
   extern __shared__ uint8_t raw[];
   uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -286,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 2) long_second_kernel(const Params p
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();
   begin(sh, 256);
-  const uint32_t h_hi = sh->tmem, h_lo = h_hi + kHalf, tmem = h_lo + kHalf, abort_flag = smem_u32(&sh->abort);
+  const uint32_t ht = sh->tmem, tmem = ht + kP * kHalf, abort_flag = smem_u32(&sh->abort);
   const uint64_t limit = p.control->limit_ns;
   const bool stall = p.control->stall != 0;
   const int64_t items = int64_t(*p.num_tiles) * p.slices;
@@ -331,13 +334,13 @@ __global__ void __launch_bounds__(kThreads, 2) long_second_kernel(const Params p
       if (d.adapter < 0 || tid != 0 || stall) return;
       tc_fence_after();
       const uint64_t bd = smem_desc(smem_u32(bs) + i % S * kB);
-      const uint32_t idesc = idesc_of<DT>(NC), to = tmem + ((g + i) & 1) * NC;
+      const uint32_t idesc = idesc_of<DT>(NC), to = tmem + (g + i) % kAccs * NC;
       for (int kk = 0; kk < p.r16 / 16; ++kk) {
         const uint64_t bo = ((kk >> 2) * NC * 128 + (kk & 3) * 32) >> 4;
-        umma_ts(to, h_lo + 8 * kk, bd + bo, idesc, kk > 0);
-        umma_ts(to, h_hi + 8 * kk, bd + bo, idesc, 1);
+#pragma unroll
+        for (int q = kP - 1; q >= 0; --q) umma_ts(to, ht + q * kHalf + 8 * kk, bd + bo, idesc, kk > 0 || q < kP - 1);  // the smallest part first
       }
-      umma_commit(smem_u32(&sh->stage_bar[(g + i) & 1]));
+      umma_commit(smem_u32(&sh->stage_bar[(g + i) % kAccs]));
     };
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) {
@@ -376,13 +379,16 @@ __global__ void __launch_bounds__(kThreads, 2) long_second_kernel(const Params p
         f = 1.f / unit;  // (exact: a power of two)
       }
 #pragma unroll
-      for (int e0 = 0; e0 < kHalf; e0 += 32) {
-        uint32_t hi[16], lo[16];
+      for (int e = 0; e < kHalf; ++e) v[e] *= f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) split2<DT>(v[e0 + 2 * e] * f, v[e0 + 2 * e + 1] * f, hi[e], lo[e]);
-        tmem_st16(h_hi + lanes + (half * kHalf + e0) / 2, hi);
-        tmem_st16(h_lo + lanes + (half * kHalf + e0) / 2, lo);
-      }
+      for (int e0 = 0; e0 < kHalf; e0 += 32)
+#pragma unroll
+        for (int q = 0; q < kP; ++q) {
+          uint32_t part[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) part[e] = take_part<DT>(v[e0 + 2 * e], v[e0 + 2 * e + 1]);
+          tmem_st16(ht + q * kHalf + lanes + (half * kHalf + e0) / 2, part);
+        }
       tmem_wait_st();
       tc_fence_before();
     }
@@ -390,10 +396,10 @@ __global__ void __launch_bounds__(kThreads, 2) long_second_kernel(const Params p
     for (int i = 0; i < n; ++i) {
       if (i + S - 1 < n) fetch(i + S - 1);  // (where step i - 1 was: its results have been stored)
       cp_async_commit();
-      if (i + 1 < n) multiply(i + 1);
+      if (i + 1 < n && (kAccs > 1 || d.adapter < 0)) multiply(i + 1);
       uint8_t *ot = os + i % S * kBase;
       if (d.adapter >= 0) {
-        ok = wait_phase(smem_u32(&sh->stage_bar[(g + i) & 1]), (g + i) >> 1 & 1, abort_flag, limit, &p.control->error);
+        ok = wait_phase(smem_u32(&sh->stage_bar[(g + i) % kAccs]), (g + i) / kAccs & 1, abort_flag, limit, &p.control->error);
         ok = __syncthreads_and(ok);
         if (!ok) break;
         tc_fence_after();
@@ -401,18 +407,27 @@ __global__ void __launch_bounds__(kThreads, 2) long_second_kernel(const Params p
         const int row = (warp & 3) * 32 + lane;
         float f = 1.f;
         if constexpr (!DT::kBF16) f = sh->back[0][row];
+        const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (g + i) % kAccs * NC + (warp >> 2) * (NC / 2);
+        float v[NC / 32][16];
+        if constexpr (kAccs == 1) {
 #pragma unroll
-        for (int c0 = 0; c0 < NC / 2; c0 += 16) {
-          const int col = (warp >> 2) * (NC / 2) + c0;
-          float v[16];
-          tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + ((g + i) & 1) * NC + col, v);
+          for (int k = 0; k < NC / 32; ++k) tmem_ld16(from + 16 * k, v[k]);
           tmem_wait_ld();
+          tc_fence_before();
+          if (i + 1 < n) multiply(i + 1);
+        }
+#pragma unroll
+        for (int k = 0; k < NC / 32; ++k) {
+          if constexpr (kAccs > 1) {
+            tmem_ld16(from + 16 * k, v[k]);
+            tmem_wait_ld();
+          }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            uint4 *at = reinterpret_cast<uint4 *>(ot + place(row, col / 8 + u, kLongTile));
+            uint4 *at = reinterpret_cast<uint4 *>(ot + place(row, (warp >> 2) * (NC / 16) + 2 * k + u, kLongTile));
             uint4 w = *at;
-            add2<DT>(w.x, v[8 * u], v[8 * u + 1], f), add2<DT>(w.y, v[8 * u + 2], v[8 * u + 3], f);
-            add2<DT>(w.z, v[8 * u + 4], v[8 * u + 5], f), add2<DT>(w.w, v[8 * u + 6], v[8 * u + 7], f);
+            add2<DT>(w.x, v[k][8 * u], v[k][8 * u + 1], f), add2<DT>(w.y, v[k][8 * u + 2], v[k][8 * u + 3], f);
+            add2<DT>(w.z, v[k][8 * u + 4], v[k][8 * u + 5], f), add2<DT>(w.w, v[k][8 * u + 6], v[k][8 * u + 7], f);
             *at = w;
           }
         }

@@ -38,7 +38,6 @@ constexpr int kStatCtas = 4;   // on an SM
 constexpr int kMaxQ = 64;
 constexpr int kMaxSplits = 32;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kFar = -1.0e4f;  // exp2(kFar) is zero; keeps infinities out of differences
 
 // Two fp32 numbers in one 64-bit register pair
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
@@ -149,9 +148,10 @@ __device__ __forceinline__ float unit_of(float temp) {
   const float c = kLog2e / temp;
   return c > 1e30f ? 1e30f : temp > 0.f ? c : __int_as_float(0x7FFFFFFF);
 }
-// exp2((a - m) c) of a running maximum a that grows to m
+// exp2((a - m) c) of a running maximum a that grows to m. (No bound on the difference: at a high temperature elements far below the
+// largest count too, and one that leaves fp32's range is -infinity, whose exponential is zero. A maximum of +infinity gives NaN.)
 __device__ __forceinline__ float shrink(float a, float m, float c) {
-  return a == -INFINITY ? 0.f : exp2_approx(max_nan(a - m, kFar) * c);
+  return a == -INFINITY ? 0.f : exp2_approx((a - m) * c);
 }
 __device__ __forceinline__ void join(float &m, float &s, float om, float os, float c) {
   const float top = max_nan(m, om);

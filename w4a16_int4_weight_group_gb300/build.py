@@ -32,6 +32,7 @@ PYCALL_PATH = os.path.join(HERE, "_w4a16_call" + (sysconfig.get_config_var("EXT_
 # binding reads the tensors from Python)
 FAST_SRC = os.path.join(CSRC, "fastcall.cpp")
 FAST_PATH = os.path.join(HERE, "_w4a16_fast" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+FAST_STAMP = os.path.join(OBJ_DIR, "fast.key")  # what it was last built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
                      "-I", INCLUDE, "-Xptxas", "-warn-spills"]
@@ -78,11 +79,16 @@ def build_pycall(force: bool = False) -> bool:
     return True
 
 
+def fast_key() -> str:
+    """What the module of ordinary calls is compiled against: it reads tensors by the layout in torch's own headers, so that it serves no
+    other torch than this one."""
+    import torch
+    return f"torch {torch.__version__} {torch.version.git_version} abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+
+
 def build_fast(force: bool = False) -> bool:
-    """Compile the module of ordinary calls beside the library; False when it cannot be built."""
-    header = os.path.join(INCLUDE, "w4a16.h")
-    if not force and os.path.exists(FAST_PATH) and os.path.getmtime(FAST_PATH) >= max(os.path.getmtime(FAST_SRC), os.path.getmtime(header)):
-        return True
+    """Compile the module of ordinary calls beside the library; False when it cannot be built. It is built again for another
+    torch, and what could not be compiled for this one is not tried again until a source changes."""
     inc = sysconfig.get_paths().get("include")
     cxx = shutil.which(os.environ.get("CXX", "c++")) or shutil.which("g++")
     try:
@@ -93,17 +99,30 @@ def build_fast(force: bool = False) -> bool:
         return False
     if not cxx or not inc or not os.path.exists(os.path.join(inc, "Python.h")) or not os.path.isdir(os.path.join(top, "include")):
         return False
+    key = fast_key()
+    newest = max(os.path.getmtime(f) for f in (FAST_SRC, os.path.join(INCLUDE, "w4a16.h"), os.path.abspath(__file__)))
+    if not force and os.path.exists(FAST_STAMP) and os.path.getmtime(FAST_STAMP) >= newest:
+        with open(FAST_STAMP) as f:
+            built = f.read()
+        if built == "failed for " + key:
+            return False
+        if built == key and os.path.exists(FAST_PATH):
+            return True
+    os.makedirs(os.path.dirname(FAST_STAMP), exist_ok=True)
     tmp = FAST_PATH + ".tmp"
-    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", inc, "-I", INCLUDE,
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DW4A16_BUILT_FOR="{key}"', "-I", inc, "-I", INCLUDE,
            "-isystem", os.path.join(top, "include"), "-isystem", os.path.join(top, "include", "torch", "csrc", "api", "include"), "-isystem", cuda,
            FAST_SRC, "-o", tmp, "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        if os.environ.get("W4A16_BUILD_VERBOSE"):
-            print(r.stderr, file=sys.stderr)
-        return False
-    os.replace(tmp, FAST_PATH)
-    return True
+    if r.returncode == 0:
+        os.replace(tmp, FAST_PATH)
+    else:
+        print("w4a16: the module of ordinary calls could not be compiled; its calls go through the slower binding"
+              + (":\n" + r.stderr if os.environ.get("W4A16_BUILD_VERBOSE") else " (W4A16_BUILD_VERBOSE=1 says why)"), file=sys.stderr)
+    with open(FAST_STAMP, "w") as f:
+        f.write(key if r.returncode == 0 else "failed for " + key)
+    return r.returncode == 0
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:

@@ -340,4 +340,12 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_w4a16_fast", "Ordinary calls of 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__w4a16_fast(void) { return PyModule_Create(&kModule); }
+// built_for: the torch whose headers this was compiled with, which the binding compares with the one that runs before it makes a call
+PyMODINIT_FUNC PyInit__w4a16_fast(void) {
+  PyObject *m = PyModule_Create(&kModule);
+  if (m && PyModule_AddStringConstant(m, "built_for", W4A16_BUILT_FOR) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

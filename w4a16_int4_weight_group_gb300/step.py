@@ -61,7 +61,7 @@ def _bind():
     return _calls
 
 
-_fast = None  # the module of ordinary calls (see csrc/fastcall.cpp), False when it was not built
+_fast = None  # the module of ordinary calls (see csrc/fastcall.cpp), False when it was not built for this torch
 
 
 def _bind_fast():
@@ -71,6 +71,9 @@ def _bind_fast():
     L = lib()
     try:
         from . import _w4a16_fast as m
+        from .build import fast_key
+        if getattr(m, "built_for", None) != fast_key():  # (another torch's layout of tensors)
+            raise ImportError
         m.bind(*(ctypes.cast(getattr(L, "w4a16_" + n), _vp).value
                  for n in ("lora", "verify_drafts", "kv_fork", "kv_reserve", "kv_free", "kv_copy", "kv_compact", "lora_workspace_size")))
         _fast = m

@@ -46,12 +46,19 @@ class Server:
         y = layer[name](x)
         return w4.w4a16_lora(x, *layer[name + "_adapter"], users, y, out=y)
 
+    def give_back(self, table, lens, keep=None):
+        w4.w4a16_kv_free(self.refs, table, lens, self.page, keep=keep)
+
     def step(self, table, lens, users, tokens, positions, q_start, mask, max_q):
-        """Logits of the sequences' next tokens; these go into the cache behind the `lens` that are there. Returns the lengths too."""
+        """Logits of the sequences' next tokens; these go into the cache behind the `lens` that are there. Returns the lengths too.
+        MemoryError where the pool has no room for all of them: nothing was written, and what was reserved has been given back."""
         count = q_start[1:] - q_start[:-1]
         want = lens + count
-        _, copies = w4.w4a16_kv_reserve(self.refs, table, lens, want, self.page)
+        held, copies = w4.w4a16_kv_reserve(self.refs, table, lens, want, self.page)
         w4.w4a16_kv_copy(self.caches, copies)
+        if bool((held < want).any()):  # (a page that others hold too, or none at all, stands where tokens would be written)
+            self.give_back(table, held, keep=lens)
+            raise MemoryError(f"{int((held < want).sum())} of {len(lens)} sequences have no room for their tokens")
         seq = torch.repeat_interleave(torch.arange(len(count), device="cuda"), count, output_size=tokens.numel())
         place = torch.arange(tokens.numel(), device="cuda") - q_start[seq] + lens[seq]
         slots = table[seq, place // self.page].long() * self.page + place % self.page
@@ -71,23 +78,34 @@ class Server:
         table = torch.full((1, self.max_pages), -1, dtype=torch.int32, device="cuda")
         lens = torch.zeros(1, dtype=torch.int32, device="cuda")
         users = torch.tensor([user], dtype=torch.int32, device="cuda")
-        for at in range(0, len(prompt) - 1, 64):
-            part = torch.tensor(prompt[at:min(at + 64, len(prompt) - 1)], device="cuda")
-            start = torch.tensor([0, part.numel()], dtype=torch.int32, device="cuda")
-            _, lens = self.step(table, lens, users, part, torch.arange(at, at + part.numel(), device="cuda"), start, None, part.numel())
+        try:
+            for at in range(0, len(prompt) - 1, 64):
+                part = torch.tensor(prompt[at:min(at + 64, len(prompt) - 1)], device="cuda")
+                start = torch.tensor([0, part.numel()], dtype=torch.int32, device="cuda")
+                _, lens = self.step(table, lens, users, part, torch.arange(at, at + part.numel(), device="cuda"), start, None, part.numel())
+        except MemoryError:
+            self.give_back(table, lens)
+            raise
         return table, lens
 
 
 def decode(server, prompts, users, answers, steps, draft, temperature=1.0, seed=0):
     """`answers` samples of at least `steps` tokens after each prompt (a list of lists of tokens). draft(tokens) -> guesses for what
     follows: a list of (parent, token), parent an earlier index of the list or -1. Returns the token lists and the guesses that
-    were accepted. users[i]: the adapter of prompt i, or -1."""
+    were accepted. users[i]: the adapter of prompt i, or -1. MemoryError where the pages run out; all of them are given back then."""
     g = torch.Generator(device="cuda").manual_seed(seed)
-    rows = [server.read(p, u) for p, u in zip(prompts, users)]
+    rows = []
+    try:
+        for p, u in zip(prompts, users):
+            rows.append(server.read(p, u))
+    except MemoryError:
+        for t, n in rows:
+            server.give_back(t, n)
+        raise
     first, first_lens = torch.cat([t for t, _ in rows]), torch.cat([n for _, n in rows])
     parents = torch.arange(len(prompts) * answers, dtype=torch.int32, device="cuda") // answers
     table, lens = w4.w4a16_kv_fork(server.refs, first, first_lens, parents, server.page)
-    w4.w4a16_kv_free(server.refs, first, first_lens, server.page)  # the answers hold the prompts' pages now
+    server.give_back(first, first_lens)  # the answers hold the prompts' pages now
     out = [list(p) for p in prompts for _ in range(answers)]
     user = torch.tensor(users, dtype=torch.int32, device="cuda")[parents.long()].contiguous()
     temp = torch.full((len(out),), temperature, device="cuda")
@@ -109,17 +127,21 @@ def decode(server, prompts, users, answers, steps, draft, temperature=1.0, seed=
         n = max(b - a for a, b in zip(start, start[1:]))
         start = torch.tensor(start, dtype=torch.int32, device="cuda")
         mask, ids = torch.tensor(masks, device="cuda"), torch.tensor(tokens, device="cuda")
-        logits, want = server.step(table, lens, user, ids, torch.tensor(depth, device="cuda"), start, mask, n)
+        try:
+            logits, want = server.step(table, lens, user, ids, torch.tensor(depth, device="cuda"), start, mask, n)
+        except MemoryError:
+            server.give_back(table, lens)
+            raise
         uniforms = torch.rand(len(tokens), generator=g, device="cuda")
         noise = torch.empty(len(out), server.vocab, device="cuda").exponential_(generator=g)
         _, path, new, _ = w4.w4a16_verify_drafts(logits, ids, uniforms, noise, q_start=start, tree_mask=mask, temperature=temp, max_q=n)
         lens = w4.w4a16_kv_compact(server.caches, server.head_dim, table, want, path, q_start=start)
-        w4.w4a16_kv_free(server.refs, table, want, server.page, keep=lens)
+        server.give_back(table, want, keep=lens)
         for o, row in zip(out, new.tolist()):
             got = [t for t in row if t >= 0]
             o += got
             accepted += len(got) - 1
-    w4.w4a16_kv_free(server.refs, table, lens, server.page)
+    server.give_back(table, lens)
     return out, accepted
 
 

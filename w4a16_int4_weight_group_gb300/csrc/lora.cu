@@ -24,9 +24,9 @@
 // and K is split in the same way.
 //
 // Bound by memory for long prompts (base read and out written are most of the bytes), by the chain of copies, barriers and sums for few tokens. Measured, replayed from a graph: 8191 tokens 5120 -> 7168 of rank
-// 32 75 us for 328 MB, 4.4 TB/s, 0.65 of the device's copy rate (9 us of them the sort and the launch; the same tiles copied without
-// an adapter 0.85 of it while they stream); DRAM 53 %, tensor pipe 31 %, schedulers 42 % of the cycles. 520 tokens 2560 -> 3840 of rank 64 19.2
-// us; 48 tokens 5120 -> 7168 of rank 16 8.7; one token 2112 -> 1152 4.1.
+// 32 81 us for 328 MB, 4.0 TB/s, 0.60 of the device's copy rate (9 us of them the sort and the launch; the same tiles copied without
+// an adapter 0.85 of it while they stream); DRAM 49 %, tensor pipe 39 %, schedulers 40 % of the cycles. 520 tokens 2560 -> 3840 of rank 64 19.1
+// us in float16, 20.0 in bfloat16; 48 tokens 5120 -> 7168 of rank 16 8.9; one token 2112 -> 1152 4.2.
 #include <algorithm>
 #include <atomic>
 
@@ -592,14 +592,14 @@ __global__ void __launch_bounds__(kSortThreads) lora_sort_kernel(const int32_t *
 // are read half as often, for fewer and larger shares of work). 2560 -> 3840, 16 adapters, rank 16: 1500 tokens 18.1 us with 32 and 19.2 with 64, 2000 tokens 18.7 and 19.5. 5120 -> 7168, 8191 tokens
 // of 12 adapters: rank 16 83 and 77, rank 32 84 and 80.
 constexpr int64_t kMidTokens = 2048;
-// Which calls go to the form on tcgen05: ranks past 32, in layers of some size (three launches show: 512 -> 512, 2000 tokens of rank 128 15.0 us
-// warp-level, 20.7 on tcgen05; at 8000 tokens as long), and where its tiles of 128 tokens are not nearly empty, since each has A and B
-// read and multiplied in full. Warp-level against tcgen05, 5120 -> 7168, replayed:
-//   rank 40: 1000 tokens of 12 adapters 25.4 against 29.3; 1500 of 12 35.2 against 30.3; 4000 of 40 87 against 68, of 120 88 against 106;
-//     8000 of 3 101 against 78, of 400 154 against 288
-//   rank 72 (one CTA on an SM warp-level): 300 tokens of 3 26.2 against 23.1; 1000 of 40 63 against 56; 1100 of 120 79 against 116; 3000 of 120
-//     102 against 127; 4000 of 120 195 against 130; 8000 of 3 196 against 88
-// and for ranks to 32: 2560 -> 3840, 4000 tokens of rank 32 44.2 against 45.5, 16000 tokens 77.7 against 80.9.
+// Which calls go to the form on tcgen05: ranks past 32, in layers of some size (three launches show: 512 -> 512, 2000 tokens of rank 128 16.8 us
+// warp-level, 22.6 on tcgen05; at 8000 tokens as long), and where its tiles of 128 tokens are not nearly empty, since each has A and B
+// read and multiplied in full. Warp-level against tcgen05, 5120 -> 7168, bfloat16, replayed:
+//   rank 40: 1000 tokens of 12 adapters 28.2 against 31.6; 1300 of 12 39.4 against 34.5; 1500 of 23 39.7 against 41.4; 4000 of 62 106 against 86, of
+//     120 113 against 111 (float16 100 against 106); 8000 of 3 117 against 83, of 400 175 against 304
+//   rank 72 (one CTA on an SM warp-level): 300 tokens of 3 30.1 against 26.7; 1000 of 40 72 against 59; 1100 of 120 104 against 124; 3000 of 120
+//     115 against 132; 4000 of 120 216 against 134; 8000 of 3 221 against 94
+// and for ranks to 32: 4000 tokens of rank 32 49.6 against 54.9, 8191 82.2 against 79.6; 2560 -> 3840 4000 tokens 33.5 against 36.9, 16000 tokens 87.6 against 86.3.
 constexpr int kMidRank = 32, kWideRank = 64;
 constexpr int64_t kLongLayer = 4096, kLongTokens = 1280, kWideTokens = 640, kWideAdapters = 48;
 bool may_be_long(int64_t tokens, int rank, int64_t adapters) {

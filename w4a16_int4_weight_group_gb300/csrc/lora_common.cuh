@@ -1,4 +1,4 @@
-// What the two forms of the low-rank adapters share: tiles of sorted tokens and the numbers' two parts.
+// What the two forms of the low-rank adapters share: tiles of sorted tokens and the parts of h.
 #pragma once
 
 #include "common.cuh"

@@ -14,8 +14,9 @@
 //
 // Taken instead of the warp-level form where that is bound by mma.sync: for many tokens of ranks past 32 (its second product takes two for
 // each, and one m16n8k16 takes about 16 cycles on a quarter of an SM), a good part of a tile for each adapter. Bound by what the SMs read and write through L2: base, out, and B
-// once a tile, 6.6 to 7.1 TB/s in the second kernel. Measured: 8191 tokens 5120 -> 7168 of 12 adapters, rank 64 23 + 50 us and 7 for the sort (87 a
-// call out of L2), rank 128 28 + 63 (104).
+// once a tile, 6.2 to 6.5 TB/s in the second kernel. Measured: 8191 tokens 5120 -> 7168 of 12 adapters, rank 64 23 + 53 us and 7 for the sort (90 a
+// call out of L2), rank 128 26 + 69 (109). Replayed, bfloat16's three parts
+// and, at rank 128, one accumulator against float16's two of each: rank 64 85 and 82 us, rank 128 103 and 97.
 #include <algorithm>
 #include <atomic>
 #include <mutex>

@@ -12,7 +12,8 @@
 // head and some layers, before it writes one, so that a place may be read and written in any order.
 //
 // Measured: 128 pages of 128 tokens, 8 heads of 128 at 8 bits, in 8 layers copied in 62 us (553 MB, 8.9 TB/s with part of the writes left in
-// L2; the step of fork, reserve, copy, free and two copies of the tables 86 us replayed); reserve 8 to 12 us alone, fork and free 4 to 6.
+// L2; the step of fork, reserve, copy, free and two copies of the tables 86 us replayed); reserve 8 to 12 us alone, 5 replayed in a pool of 400 pages and 27
+// in one of 100000 whose free pages are the last; fork and free 4 to 6, free 2 replayed.
 // compact: 64 sequences of up to 16 tokens in 16 layers 6.5 us replayed (a layer a CTA: 19 us a call), 4 of 8 in one layer 3.0.
 #include <algorithm>
 

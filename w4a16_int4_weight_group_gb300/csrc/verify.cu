@@ -20,7 +20,7 @@
 // Bound by memory in the first kernel, by the latency of its chain of small steps (sequence, statistics, tokens, logits of the
 // drafted tokens, barriers) and then by loads in flight in the second. Measured: 64 sequences of up to 8 tokens, 128007 bf16 logits, with q:
 // 38 us replayed from a graph, 17 us for the first kernel's 74 MB (5 TB/s while it streams) and 25 for the second's 81 MB; 8 trees of up to 64
-// guesses, 65537 fp32 logits, 38 us; one chain of 5 tokens, 32003 logits, 9 us (11 to issue it). Read by neighbouring threads, the three rows
+// guesses, 65537 fp32 logits, 38 us; one chain of 5 tokens, 32003 logits, 9 us (11 to issue it); 64 single tokens sampled from 128007 logits 26, at temperature 0 9. Read by neighbouring threads, the three rows
 // of the second kernel take 25 us where vectors of one of them took 26 and 33 with half as many loads in flight twice; the noise
 // fetched into L2 while the last node is found delays that by more than it saves (40 us in all).
 #include <algorithm>

@@ -13,7 +13,7 @@
 // shares: the first product alone 3 us faster, the second 7 slower, since half the warps fit.)
 //
 // h is fp32 and goes into the second product whole, as a sum of numbers of the dtype: three for bfloat16, which hold all 24 bits (with
-// two, 16 of them, every 500th element of out was rounded the other way, and what cancels between the products was off), two for
+// two, 16 of them, 3 of 1000 elements of out were rounded the other way, and what cancels between the products was off), two for
 // float16, 22 bits below the token's largest (whose range its sums may leave: each token's h is scaled by a power
 // of two). The rounding of out is then the only one that shows. The third part costs 7 to 9 % at ranks 17 to 64 of long prompts (8191 tokens 5120 -> 7168, rank 32:
 // 74.6 -> 81.3 us); up to rank 16, and for few tokens, the parts share a pass whose half was empty, and it costs nothing or 2 %.
